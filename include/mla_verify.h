@@ -94,6 +94,8 @@ extern "C" {
 #define MLA_VERIFY_DEV_RANGE        256   /* a q or key value is outside the fp16 range
                                              (|x| >= 65536, or NaN): rows that used it
                                              are not reliable */
+#define MLA_VERIFY_DEV_BAD_POS      512   /* append: position outside the cos/sin table */
+#define MLA_VERIFY_DEV_BAD_REF     1024   /* page pool: a page's count contradicts its use */
 
 /* Output element type. */
 #define MLA_VERIFY_OUT_F32            0
@@ -403,6 +405,111 @@ int mla_verify_compact_kv(mla_verify_plan* plan, int batch, const void* kv_src, 
                           const int32_t* kv_lens, const int32_t* free_pages,
                           int64_t num_free_pages, void* kv_dst, int64_t dst_slots,
                           int32_t* page_table, int32_t* page_indptr, void* stream);
+
+/*
+ * New tokens' rows and queries, in one pass: the norm of each token's latent,
+ * the position rotation of its 64 rope dims and of every query head's, and
+ * the write into the cache.  For token n at slot s = slots[n] and position
+ * p = positions[n], with cos_i = cos_sin[p][i], sin_i = cos_sin[p][32 + i]:
+ *
+ *     c            = kv[n][0:512]
+ *     cache[s]     = bf16(c * weight / sqrt(mean(c^2) + eps)) | rot(kv[n][512:576])
+ *     q[n][h]      = q_nope[n][h] | rot(q_pe[n][h])
+ *     rot(x): x_a cos_i - x_b sin_i, x_b cos_i + x_a sin_i in places a and b;
+ *             (a, b) = (2i, 2i + 1) for MLA_VERIFY_ROPE_PAIRS, (i, i + 32)
+ *             for MLA_VERIFY_ROPE_HALVES; i = 0 .. 31.
+ *
+ *   kv           bf16, token n's 576 values at kv + n * kv_stride elements.
+ *   weight       bf16 [512]; eps finite and >= 0.
+ *   q_nope       bf16, the 512 absorbed dims of head h of token n at
+ *                q_nope + n * nope_stride_token + h * nope_stride_head; or
+ *                NULL when they are in q already (q's first 512 dims of each
+ *                head are then left alone).
+ *   q_pe         bf16, the 64 rope dims, by strides likewise; they may be
+ *                q's own last 64 dims (rotated in place).  NULL: no queries
+ *                (q and q_nope are ignored).
+ *   cos_sin      fp32 [max_pos][64].
+ *   positions, slots  int32 [num_tokens].  Slot -1 marks a padding token:
+ *                nothing of it is read or written.  The other slots are
+ *                distinct (of two tokens with one slot either may be kept).
+ *   kv_cache     bf16 [num_slots][576], the plan's num_slots.
+ *   q            bf16 [num_tokens][H][576], the plan's H.
+ *
+ * Strides count elements and are multiples of 8 (16 bytes); 0 repeats a
+ * vector.  Norm and rotation run in fp32 and are rounded to bf16 once.  A
+ * slot outside the cache (MLA_VERIFY_DEV_BAD_SLOT) or a position outside the
+ * table (MLA_VERIFY_DEV_BAD_POS) sets its bit and nothing of that token is
+ * written.  num_tokens may be 0 and is not bounded by the plan's max_batch.
+ * MLA_VERIFY_ERR_ARG for num_tokens < 0, max_pos < 1, a stride that is
+ * negative or not a multiple of 8, a bad eps or rope style; other errors as
+ * for mla_verify_attn.  Capturable; allocates nothing.
+ */
+#define MLA_VERIFY_ROPE_PAIRS         0
+#define MLA_VERIFY_ROPE_HALVES        1
+int mla_verify_append_kv(mla_verify_plan* plan, int64_t num_tokens, const void* kv,
+                         int64_t kv_stride, const void* weight, float eps, const void* q_nope,
+                         int64_t nope_stride_token, int64_t nope_stride_head, const void* q_pe,
+                         int64_t pe_stride_token, int64_t pe_stride_head, const float* cos_sin,
+                         int64_t max_pos, const int32_t* positions, const int32_t* slots,
+                         int rope_style, void* kv_cache, void* q, void* stream);
+
+/*
+ * Forking and freeing requests of a page_size 64 cache whose pages are
+ * counted.  The pool is three arrays of the caller:
+ *
+ *   page_refs    int32 [num_slots / 64]: tables that hold the page, 0 = free.
+ *   free_pages   int32 [num_slots / 64]: a stack of the free pages.
+ *   free_count   int32 [1]: its height (on the device: both calls capture).
+ *
+ * mla_verify_fork_kv: child c continues parent p = parents[c] (a request of
+ * the tables kv_indices / kv_indptr [num_parents + 1] / kv_lens
+ * [num_parents], whose first n = kv_lens[p] rows are in the cache).  It
+ * shares the parent's n / 64 full pages (their counts rise), takes fresh
+ * pages for the rest of its n + extra_rows rows (counts 1) and gets a copy of
+ * the n % 64 rows of the parent's last page, in each of the num_layers caches
+ * [num_slots][576] that start layer_stride elements apart at kv_cache.
+ *   child_indices int32 [capacity] out, child_indptr int32 [num_children + 1]
+ *                 out, child_lens int32 [num_children] out: the children's
+ *                 page tables; child_lens[c] = n + extra_rows, so with
+ *                 extra_rows = T they feed the verify attention directly, and
+ *                 children of one parent share their first n / 64 * 64 rows
+ *                 (mla_verify_attn_shared).
+ * The j-th fresh page of the call, in child order, is free_pages[free_count -
+ * 1 - j]; free_count falls by the pages taken.  A parent may be forked any
+ * number of times, or not at all; it keeps its own table.  The outputs must
+ * not be the inputs.  num_parents and num_children in [1, max_batch].
+ * Device-side problems: a parent index out of range (MLA_VERIFY_DEV_BAD_POOL),
+ * n outside [0, max_kv_len - extra_rows] (BAD_LEN) or a table that does not
+ * hold n rows (BAD_INDPTR) gives the child length 0 and no entries; when the
+ * stack or the capacity runs out the longest leading run of children that
+ * fits is forked and later ones get none (CAPACITY); a page outside the cache
+ * stays in the table uncounted, its rows are copied as zeros (BAD_SLOT); a
+ * held page whose count is not positive, or a fresh one whose count is not 0,
+ * is reported (BAD_REF).
+ *
+ * mla_verify_free_kv: ends the batch requests of a table: the count of every
+ * entry's page falls by one, and pages that reach 0 are pushed on the stack
+ * in ascending order.  A page may stand in several of the tables.  Entries
+ * outside the cache are skipped (BAD_SLOT), counts that are 0 already stay 0
+ * and push nothing (BAD_REF: a page freed twice); a kv_indptr that is
+ * negative or decreases (BAD_INDPTR) or a free_count outside [0, num_slots /
+ * 64] (CAPACITY) frees nothing.
+ *
+ * MLA_VERIFY_ERR_SHAPE when the plan's page_size is not 64; MLA_VERIFY_ERR_ARG
+ * for num_layers < 1, a layer_stride that is negative or not a multiple of 8,
+ * extra_rows outside [0, max_kv_len] or capacity outside [0, 2^31); other
+ * errors as for mla_verify_attn.  Both are capturable, allocate nothing, and
+ * share the plan's workspace like every call.
+ */
+int mla_verify_fork_kv(mla_verify_plan* plan, int num_children, const int32_t* parents,
+                       int num_parents, const int32_t* kv_indices, const int32_t* kv_indptr,
+                       const int32_t* kv_lens, void* kv_cache, int num_layers,
+                       int64_t layer_stride, int extra_rows, int32_t* page_refs,
+                       const int32_t* free_pages, int32_t* free_count, int32_t* child_indices,
+                       int64_t capacity, int32_t* child_indptr, int32_t* child_lens, void* stream);
+int mla_verify_free_kv(mla_verify_plan* plan, int batch, const int32_t* kv_indices,
+                       const int32_t* kv_indptr, int32_t* page_refs, int32_t* free_pages,
+                       int32_t* free_count, void* stream);
 
 /*
  * Allocation-free verify attention, for callers that cannot allocate device

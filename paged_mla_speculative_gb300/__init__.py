@@ -13,6 +13,9 @@ from .binding import (  # noqa: F401
     OUT_F32,
     MlaVerifyError,
     Plan,
+    append_kv,
+    fork_kv,
+    free_kv,
     load_library,
     mla_verify_attn,
     mla_verify_attn_host,

@@ -41,6 +41,11 @@ DEV_INTERNAL = 32
 DEV_BAD_POOL = 64
 DEV_CAPACITY = 128
 DEV_RANGE = 256
+DEV_BAD_POS = 512
+DEV_BAD_REF = 1024
+
+ROPE_PAIRS = 0
+ROPE_HALVES = 1
 
 STATUS = {0: "OK", -1: "ERR_NULL", -2: "ERR_ALIGN", -3: "ERR_SHAPE", -4: "ERR_BATCH",
           -5: "ERR_SCALE", -6: "ERR_CUDA", -7: "ERR_DEVICE", -8: "ERR_OOM", -9: "ERR_ARG",
@@ -77,6 +82,12 @@ SIGNATURES = {
                                       _P, _P, _P]),
     "mla_verify_compact_kv": (_I, [_P, _I, _P, ctypes.c_int64, _P, _P, _P, _P, ctypes.c_int64, _P,
                                    ctypes.c_int64, _P, _P, _P]),
+    "mla_verify_append_kv": (_I, [_P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_float, _P,
+                                  ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64,
+                                  ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _I, _P, _P, _P]),
+    "mla_verify_fork_kv": (_I, [_P, _I, _P, _I, _P, _P, _P, _P, _I, ctypes.c_int64, _I, _P, _P, _P, _P,
+                                ctypes.c_int64, _P, _P, _P]),
+    "mla_verify_free_kv": (_I, [_P, _I, _P, _P, _P, _P, _P, _P]),
     "mla_verify_strerror": (ctypes.c_char_p, [_I]),
     "mla_verify_version": (_I, []),
 }
@@ -147,6 +158,7 @@ class Plan:
         self.max_batch, self.T, self.H = max_batch, num_drafts, num_heads
         self.page_size, self.num_slots, self.max_kv_len = page_size, num_slots, max_kv_len
         self.out_dtype, self.device = out_dtype, device
+        self.torch_device = torch.device("cuda", device)
 
     @property
     def handle(self):
@@ -265,6 +277,23 @@ def _expect(t: torch.Tensor, name: str, dtype, device=None, shape=None):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _expect_strided(t: torch.Tensor, name: str, dtype, device, shape):
+    """A tensor whose vectors (last dim) are contiguous and 16-byte strided;
+    returns its other strides (0 for a dim of one vector)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    strides = [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], shape)]
+    if t.stride(-1) != 1 or any(s % 8 for s in strides):
+        raise ValueError(f"{name}'s last dim must be contiguous and its other strides multiples of 8")
+    return strides
 
 
 def mla_verify_attn(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_lens, draft_parent,
@@ -412,6 +441,118 @@ def compact_kv(plan: Plan, kv_src, kv_indices, kv_indptr, kv_lens, free_pages, k
         int(kv_dst.shape[0]), _ptr(page_table), _ptr(page_indptr), _stream_ptr(stream))
     _check(st, "mla_verify_compact_kv")
     return page_table, page_indptr
+
+
+def append_kv(plan: Plan, kv, weight, eps: float, cos_sin, positions, slots, kv_cache, q_nope=None,
+              q_pe=None, q=None, interleaved: bool = True, stream=None):
+    """New tokens' cache rows and queries; returns q (None without q_pe).
+
+    kv [N, 576] bf16 (latent | rope dims; any row stride that is a multiple of
+    8), weight [512] bf16, cos_sin [max_pos, 64] fp32 (32 cosines, 32 sines),
+    positions / slots [N] int32 (slot -1: padding, nothing of it is written),
+    kv_cache [num_slots, 576] bf16.  q_pe [N, H, 64] bf16 by strides, q_nope
+    [N, H, 512] bf16 by strides or None when q's first 512 dims hold it
+    already, q [N, H, 576] bf16 out.  ``interleaved`` rotates neighbours
+    (2i, 2i + 1), otherwise the halves (i, i + 32).  Enqueued on ``stream``;
+    no sync.
+    """
+    N = positions.shape[0]
+    dev = plan.torch_device
+    kv_stride = _expect_strided(kv, "kv", torch.bfloat16, dev, (N, 576))[0]
+    _expect(weight, "weight", torch.bfloat16, dev, (512,))
+    _expect(cos_sin, "cos_sin", torch.float32, dev)
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
+        raise ValueError("cos_sin must be [max_pos, 64]")
+    _expect(positions, "positions", torch.int32, dev, (N,))
+    _expect(slots, "slots", torch.int32, dev, (N,))
+    _expect(kv_cache, "kv_cache", torch.bfloat16, dev, (plan.num_slots, 576))
+    nope, nope_strides, pe, pe_strides = None, (0, 0), None, (0, 0)
+    if q_pe is not None:
+        pe, pe_strides = q_pe.data_ptr(), _expect_strided(q_pe, "q_pe", torch.bfloat16, dev, (N, plan.H, 64))
+        if q_nope is not None:
+            nope = q_nope.data_ptr()
+            nope_strides = _expect_strided(q_nope, "q_nope", torch.bfloat16, dev, (N, plan.H, 512))
+        elif q is None:
+            raise ValueError("without q_nope, q must hold the absorbed dims already")
+        if q is None:
+            q = torch.empty((N, plan.H, 576), dtype=torch.bfloat16, device=dev)
+        _expect(q, "q", torch.bfloat16, dev, (N, plan.H, 576))
+    elif q_nope is not None or q is not None:
+        raise ValueError("q and q_nope need q_pe")
+    st = load_library().mla_verify_append_kv(
+        plan.handle, N, kv.data_ptr(), kv_stride, weight.data_ptr(), eps, nope, nope_strides[0],
+        nope_strides[1], pe, pe_strides[0], pe_strides[1], cos_sin.data_ptr(), cos_sin.shape[0],
+        positions.data_ptr(), slots.data_ptr(), ROPE_PAIRS if interleaved else ROPE_HALVES,
+        kv_cache.data_ptr(), q.data_ptr() if q is not None else None, _stream_ptr(stream))
+    _check(st, "mla_verify_append_kv")
+    return q
+
+
+def _expect_pool(plan: Plan, page_refs, free_pages, free_count):
+    dev = plan.torch_device
+    pages = plan.num_slots // 64
+    _expect(page_refs, "page_refs", torch.int32, dev, (pages,))
+    _expect(free_pages, "free_pages", torch.int32, dev, (pages,))
+    _expect(free_count, "free_count", torch.int32, dev, (1,))
+
+
+def fork_kv(plan: Plan, parents, kv_indices, kv_indptr, kv_lens, kv_cache, page_refs, free_pages,
+            free_count, extra_rows: int = 0, child_indices=None, child_indptr=None, child_lens=None,
+            stream=None):
+    """Children of cached requests: full pages shared, the last page's rows
+    copied into a fresh one in every layer; returns (child_indices,
+    child_indptr, child_lens), the children's page tables with room for
+    ``extra_rows`` more rows each (included in child_lens).
+
+    parents [C] int32 indexes the requests of kv_indices / kv_indptr [P + 1] /
+    kv_lens [P]; kv_cache [num_slots, 576] or [layers, num_slots, 576] bf16;
+    page_refs / free_pages [num_slots / 64] and free_count [1] int32 are the
+    page pool (counts, stack of free pages, its height).  child_indices
+    defaults to C * (pages of max_kv_len) entries; its length is the capacity.
+    Page size 64 only.  Enqueued on ``stream``; no sync.
+    """
+    C, P = parents.shape[0], kv_lens.shape[0]
+    dev = plan.torch_device
+    _expect(parents, "parents", torch.int32, dev, (C,))
+    _expect(kv_indices, "kv_indices", torch.int32, dev)
+    _expect(kv_indptr, "kv_indptr", torch.int32, dev, (P + 1,))
+    _expect(kv_lens, "kv_lens", torch.int32, dev, (P,))
+    layers = 1 if kv_cache.dim() == 2 else kv_cache.shape[0]
+    layer = kv_cache if kv_cache.dim() == 2 else kv_cache[0]
+    _expect(layer, "kv_cache", torch.bfloat16, dev, (plan.num_slots, 576))
+    _expect_pool(plan, page_refs, free_pages, free_count)
+    if child_indices is None:
+        child_indices = torch.empty(C * -(-plan.max_kv_len // 64), dtype=torch.int32, device=dev)
+    if child_indptr is None:
+        child_indptr = torch.empty(C + 1, dtype=torch.int32, device=dev)
+    if child_lens is None:
+        child_lens = torch.empty(C, dtype=torch.int32, device=dev)
+    _expect(child_indices, "child_indices", torch.int32, dev)
+    _expect(child_indptr, "child_indptr", torch.int32, dev, (C + 1,))
+    _expect(child_lens, "child_lens", torch.int32, dev, (C,))
+    st = load_library().mla_verify_fork_kv(
+        plan.handle, C, parents.data_ptr(), P, kv_indices.data_ptr(), kv_indptr.data_ptr(),
+        kv_lens.data_ptr(), kv_cache.data_ptr(), layers, kv_cache.stride(0) if layers > 1 else 0,
+        extra_rows, page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+        child_indices.data_ptr(), child_indices.numel(), child_indptr.data_ptr(),
+        child_lens.data_ptr(), _stream_ptr(stream))
+    _check(st, "mla_verify_fork_kv")
+    return child_indices, child_indptr, child_lens
+
+
+def free_kv(plan: Plan, kv_indices, kv_indptr, page_refs, free_pages, free_count, stream=None):
+    """End the requests of a page table: every entry's page loses one count,
+    and pages that reach 0 are pushed on the pool's stack in ascending order.
+    Page size 64 only.  Enqueued on ``stream``; no sync."""
+    B = kv_indptr.shape[0] - 1
+    dev = plan.torch_device
+    _expect(kv_indices, "kv_indices", torch.int32, dev)
+    _expect(kv_indptr, "kv_indptr", torch.int32, dev)
+    _expect_pool(plan, page_refs, free_pages, free_count)
+    st = load_library().mla_verify_free_kv(
+        plan.handle, B, kv_indices.data_ptr(), kv_indptr.data_ptr(), page_refs.data_ptr(),
+        free_pages.data_ptr(), free_count.data_ptr(), _stream_ptr(stream))
+    _check(st, "mla_verify_free_kv")
 
 
 def mla_verify_attn_host(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_lens,

@@ -61,7 +61,11 @@ struct mla_verify_plan {
   cudaStream_t aux;
   // TMA descriptors of `packed` for the CTA-pair kernel.
   mlav::PackMaps pack_maps;
+  unsigned* page_bits;    // page_size 64: one bit per page of the cache (free_kv)
 };
+
+// The 256 bytes at mla_verify_plan::err: the error word, and fork_kv's ticket.
+constexpr int kTicketWord = 16;
 
 namespace {
 
@@ -274,7 +278,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 void free_all(mla_verify_plan* p) {
   void* bufs[] = {p->ws_o, p->ws_lse, p->err, p->st_q, p->st_idx, p->st_indptr,
-                  p->st_lens, p->st_parent, p->st_out, p->st_lse, p->packed, p->pack_sync};
+                  p->st_lens, p->st_parent, p->st_out, p->st_lse, p->packed, p->pack_sync,
+                  p->page_bits};
   for (void* b : bufs)
     if (b) cudaFree(b);
 }
@@ -313,7 +318,7 @@ int check_device(const mla_verify_plan* pl) {
 
 extern "C" {
 
-int mla_verify_version(void) { return 100; }
+int mla_verify_version(void) { return 101; }
 
 const char* mla_verify_strerror(int status) {
   switch (status) {
@@ -402,14 +407,17 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
       static_cast<size_t>(max_batch) * pl->pack_blocks * 32 * sizeof(unsigned long long);
   ok = ok && cudaMalloc(&pl->pack_sync, sync_bytes) == cudaSuccess;
   pl->pack_sync_bytes = sync_bytes;
+  const size_t bit_bytes = page_size == mlav::PAGE ? static_cast<size_t>(ceil_div(num_slots / mlav::PAGE, 32)) * 4 : 0;
+  ok = ok && (!bit_bytes || cudaMalloc(&pl->page_bits, bit_bytes) == cudaSuccess);
   if (!ok) {
     cudaGetLastError();
     free_all(pl);
     delete pl;
     return MLA_VERIFY_ERR_OOM;
   }
-  pl->ws_bytes = rows * (mlav::D_V + 1) * sizeof(float) + 256 + packed_bytes + sync_bytes;
+  pl->ws_bytes = rows * (mlav::D_V + 1) * sizeof(float) + 256 + packed_bytes + sync_bytes + bit_bytes;
   if (cudaMemset(pl->err, 0, 256) != cudaSuccess || cudaMemset(pl->pack_sync, 0, sync_bytes) != cudaSuccess ||
+      (bit_bytes && cudaMemset(pl->page_bits, 0, bit_bytes) != cudaSuccess) ||
       cudaEventCreateWithFlags(&pl->done_ev, cudaEventDisableTiming) != cudaSuccess ||
       cudaStreamCreateWithFlags(&pl->aux, cudaStreamNonBlocking) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
@@ -826,6 +834,132 @@ int mla_verify_compact_kv(mla_verify_plan* pl, int batch, const void* kv_src, in
   a.max_kv_len = pl->max_kv_len;
   a.err = pl->err;
   if (mlav::launch_compact_kv(a, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      note_done(pl, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return MLA_VERIFY_ERR_CUDA;
+  return MLA_VERIFY_OK;
+}
+
+int mla_verify_append_kv(mla_verify_plan* pl, int64_t num_tokens, const void* kv, int64_t kv_stride,
+                         const void* weight, float eps, const void* q_nope, int64_t nope_stride_token,
+                         int64_t nope_stride_head, const void* q_pe, int64_t pe_stride_token,
+                         int64_t pe_stride_head, const float* cos_sin, int64_t max_pos,
+                         const int32_t* positions, const int32_t* slots, int rope_style, void* kv_cache,
+                         void* q, void* stream) {
+  if (!pl) return MLA_VERIFY_ERR_NULL;
+  if (num_tokens == 0) return check_device(pl);
+  if (!kv || !weight || !cos_sin || !positions || !slots || !kv_cache || (q_pe && !q))
+    return MLA_VERIFY_ERR_NULL;
+  if (!aligned16(kv) || !aligned16(weight) || !aligned16(cos_sin) || !aligned16(positions) ||
+      !aligned16(slots) || !aligned16(kv_cache) ||
+      (q_pe && (!aligned16(q_pe) || !aligned16(q) || !aligned16(q_nope))))
+    return MLA_VERIFY_ERR_ALIGN;
+  auto bad_stride = [](int64_t s) { return s < 0 || s % 8; };
+  if (num_tokens < 0 || max_pos < 1 || bad_stride(kv_stride) || !(eps >= 0.f) || !std::isfinite(eps) ||
+      (rope_style != MLA_VERIFY_ROPE_PAIRS && rope_style != MLA_VERIFY_ROPE_HALVES) ||
+      (q_pe && (bad_stride(pe_stride_token) || bad_stride(pe_stride_head))) ||
+      (q_pe && q_nope && (bad_stride(nope_stride_token) || bad_stride(nope_stride_head))))
+    return MLA_VERIFY_ERR_ARG;
+  const int dev_status = check_device(pl);
+  if (dev_status != MLA_VERIFY_OK) return dev_status;
+  mlav::AppendArgs a{};
+  a.kv = static_cast<const uint16_t*>(kv);
+  a.kv_stride = kv_stride;
+  a.weight = static_cast<const uint16_t*>(weight);
+  a.eps = eps;
+  a.q_nope = static_cast<const uint16_t*>(q_nope);
+  a.nope_stride_n = nope_stride_token;
+  a.nope_stride_h = nope_stride_head;
+  a.q_pe = static_cast<const uint16_t*>(q_pe);
+  a.pe_stride_n = pe_stride_token;
+  a.pe_stride_h = pe_stride_head;
+  a.cos_sin = cos_sin;
+  a.max_pos = max_pos;
+  a.positions = positions;
+  a.slots = slots;
+  a.num_tokens = num_tokens;
+  a.heads = pl->H;
+  a.halves = rope_style == MLA_VERIFY_ROPE_HALVES;
+  a.kv_cache = static_cast<uint16_t*>(kv_cache);
+  a.num_slots = pl->num_slots;
+  a.q = static_cast<uint16_t*>(q);
+  a.err = pl->err;
+  if (mlav::launch_append_kv(a, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      note_done(pl, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return MLA_VERIFY_ERR_CUDA;
+  return MLA_VERIFY_OK;
+}
+
+int mla_verify_fork_kv(mla_verify_plan* pl, int num_children, const int32_t* parents, int num_parents,
+                       const int32_t* kv_indices, const int32_t* kv_indptr, const int32_t* kv_lens,
+                       void* kv_cache, int num_layers, int64_t layer_stride, int extra_rows,
+                       int32_t* page_refs, const int32_t* free_pages, int32_t* free_count,
+                       int32_t* child_indices, int64_t capacity, int32_t* child_indptr,
+                       int32_t* child_lens, void* stream) {
+  if (!pl || !parents || !kv_indices || !kv_indptr || !kv_lens || !kv_cache || !page_refs || !free_pages ||
+      !free_count || !child_indices || !child_indptr || !child_lens)
+    return MLA_VERIFY_ERR_NULL;
+  if (!aligned16(parents) || !aligned16(kv_indices) || !aligned16(kv_indptr) || !aligned16(kv_lens) ||
+      !aligned16(kv_cache) || !aligned16(page_refs) || !aligned16(free_pages) || !aligned16(free_count) ||
+      !aligned16(child_indices) || !aligned16(child_indptr) || !aligned16(child_lens))
+    return MLA_VERIFY_ERR_ALIGN;
+  if (pl->page_size != mlav::PAGE) return MLA_VERIFY_ERR_SHAPE;
+  if (num_children < 1 || num_children > pl->max_batch || num_parents < 1 || num_parents > pl->max_batch)
+    return MLA_VERIFY_ERR_BATCH;
+  if (num_layers < 1 || layer_stride < 0 || layer_stride % 8 || extra_rows < 0 ||
+      extra_rows > pl->max_kv_len || capacity < 0 || capacity > INT32_MAX)
+    return MLA_VERIFY_ERR_ARG;
+  const int dev_status = check_device(pl);
+  if (dev_status != MLA_VERIFY_OK) return dev_status;
+  mlav::ForkArgs a{};
+  a.parents = parents;
+  a.num_children = num_children;
+  a.num_parents = num_parents;
+  a.kv_indices = kv_indices;
+  a.kv_indptr = kv_indptr;
+  a.kv_lens = kv_lens;
+  a.kv_cache = static_cast<uint16_t*>(kv_cache);
+  a.num_layers = num_layers;
+  a.layer_stride = layer_stride;
+  a.extra = extra_rows;
+  a.num_pages = static_cast<int>(pl->num_slots / mlav::PAGE);
+  a.max_kv_len = pl->max_kv_len;
+  a.page_refs = page_refs;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.child_indices = child_indices;
+  a.capacity = capacity;
+  a.child_indptr = child_indptr;
+  a.child_lens = child_lens;
+  a.ticket = reinterpret_cast<unsigned*>(pl->err) + kTicketWord;
+  a.err = pl->err;
+  if (mlav::launch_fork_kv(a, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      note_done(pl, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return MLA_VERIFY_ERR_CUDA;
+  return MLA_VERIFY_OK;
+}
+
+int mla_verify_free_kv(mla_verify_plan* pl, int batch, const int32_t* kv_indices, const int32_t* kv_indptr,
+                       int32_t* page_refs, int32_t* free_pages, int32_t* free_count, void* stream) {
+  if (!pl || !kv_indices || !kv_indptr || !page_refs || !free_pages || !free_count)
+    return MLA_VERIFY_ERR_NULL;
+  if (!aligned16(kv_indices) || !aligned16(kv_indptr) || !aligned16(page_refs) || !aligned16(free_pages) ||
+      !aligned16(free_count))
+    return MLA_VERIFY_ERR_ALIGN;
+  if (pl->page_size != mlav::PAGE) return MLA_VERIFY_ERR_SHAPE;
+  if (batch < 1 || batch > pl->max_batch) return MLA_VERIFY_ERR_BATCH;
+  const int dev_status = check_device(pl);
+  if (dev_status != MLA_VERIFY_OK) return dev_status;
+  mlav::FreeArgs a{};
+  a.kv_indices = kv_indices;
+  a.kv_indptr = kv_indptr;
+  a.batch = batch;
+  a.num_pages = static_cast<int>(pl->num_slots / mlav::PAGE);
+  a.page_refs = page_refs;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.page_bits = pl->page_bits;
+  a.err = pl->err;
+  if (mlav::launch_free_kv(a, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
       note_done(pl, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
   return MLA_VERIFY_OK;

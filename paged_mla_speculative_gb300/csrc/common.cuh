@@ -26,6 +26,8 @@ enum : int {
   ERR_POOL = 64,       // index builder: pool row, prefix or length out of range
   ERR_CAPACITY = 128,  // index builder: kv_indices capacity exceeded
   ERR_RANGE = 256,     // an input value widened to fp16 is outside its range
+  ERR_POS = 512,       // append: position outside the cos/sin table
+  ERR_REF = 1024,      // page pool: a page's count contradicts its use
 };
 
 // Arguments of one verify call, shared by every kernel of the call.

@@ -97,4 +97,61 @@ struct CompactArgs {
 };
 cudaError_t launch_compact_kv(const CompactArgs& a, cudaStream_t stream);
 
+// New tokens' cache rows and queries (append_kv.cu).
+struct AppendArgs {
+  const uint16_t* kv;               // bf16 [num_tokens][576], rows kv_stride elements apart
+  long long kv_stride;
+  const uint16_t* weight;           // bf16 [512]
+  float eps;
+  const uint16_t* q_nope;           // bf16 [num_tokens][heads][512] by strides, or null: in q already
+  long long nope_stride_n, nope_stride_h;
+  const uint16_t* q_pe;             // bf16 [num_tokens][heads][64] by strides, or null: no queries
+  long long pe_stride_n, pe_stride_h;
+  const float* cos_sin;             // [max_pos][64]: 32 cosines, 32 sines
+  long long max_pos;
+  const int32_t* positions;         // [num_tokens]
+  const int32_t* slots;             // [num_tokens], -1: padding
+  long long num_tokens;
+  int heads, halves;                // halves: pairs (i, i + 32) instead of (2i, 2i + 1)
+  uint16_t* kv_cache;               // bf16 [num_slots][576]
+  long long num_slots;
+  uint16_t* q;                      // bf16 [num_tokens][heads][576]
+  int* err;
+};
+cudaError_t launch_append_kv(const AppendArgs& a, cudaStream_t stream);
+
+// Forking and freeing requests of a cache with counted pages (page_pool.cu).
+struct ForkArgs {
+  const int32_t* parents;           // [num_children]
+  int num_children, num_parents;
+  const int32_t* kv_indices;        // the parents' page tables
+  const int32_t* kv_indptr;         // [num_parents + 1]
+  const int32_t* kv_lens;           // [num_parents]
+  uint16_t* kv_cache;               // bf16 [num_layers][num_pages * 64][576], layers layer_stride elements apart
+  int num_layers;
+  long long layer_stride;
+  int extra, num_pages, max_kv_len;
+  int32_t* page_refs;               // [num_pages]
+  const int32_t* free_pages;        // [num_pages]
+  int32_t* free_count;              // [1]
+  int32_t* child_indices;           // [capacity] out
+  long long capacity;
+  int32_t* child_indptr;            // [num_children + 1] out
+  int32_t* child_lens;              // [num_children] out
+  unsigned* ticket;                 // plan workspace, 0 between calls
+  int* err;
+};
+cudaError_t launch_fork_kv(const ForkArgs& a, cudaStream_t stream);
+struct FreeArgs {
+  const int32_t* kv_indices;
+  const int32_t* kv_indptr;         // [batch + 1]
+  int batch, num_pages;
+  int32_t* page_refs;               // [num_pages]
+  int32_t* free_pages;              // [num_pages]
+  int32_t* free_count;              // [1]
+  unsigned* page_bits;              // plan workspace, one bit per page, 0 between calls
+  int* err;
+};
+cudaError_t launch_free_kv(const FreeArgs& a, cudaStream_t stream);
+
 }  // namespace mlav
