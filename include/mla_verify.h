@@ -313,6 +313,39 @@ int mla_verify_combine_parts(mla_verify_plan* plan, int batch, int num_parts,
                              float* lse, void* stream);
 
 /*
+ * The verify attention of groups of requests that share their first rows (a
+ * system prompt, the samples or beams of one prompt): the inputs and the
+ * result of mla_verify_attn, with each shared row read and scored once for
+ * its whole group.
+ *
+ *   group_indptr  int32 [num_groups + 1]: group g is the requests
+ *                 group_indptr[g] .. group_indptr[g+1] - 1; from 0 to batch,
+ *                 not decreasing (a group may be empty).
+ *   shared_lens   int32 [num_groups]: the first shared_lens[g] rows of every
+ *                 request of the group are the same, 0 <= shared_lens[g] <=
+ *                 P_b of each of its requests; they are read through the table
+ *                 of the group's first request that can be served.  0: nothing
+ *                 shared.
+ *
+ * num_groups in [1, max_batch], else MLA_VERIFY_ERR_ARG.  A request whose
+ * length, table or shared length is out of order comes out NaN
+ * (MLA_VERIFY_DEV_BAD_LEN / BAD_INDPTR) and the others of its group are
+ * served; a group_indptr that does not divide the batch makes every request
+ * NaN (BAD_INDPTR).  A row that sees a key with a value outside the fp16
+ * range (MLA_VERIFY_DEV_RANGE) comes out NaN; rows that do not see it are not
+ * touched by it.  A bad slot among the shared rows is masked for the whole
+ * group.  Plans with max_batch * max_kv_len of about 2^31 or more give
+ * MLA_VERIFY_ERR_SHAPE.  The split count, kernel and pack knobs and the
+ * profiling events do not apply.  Otherwise as mla_verify_attn (capturable, no
+ * allocation, the plan's workspace).
+ */
+int mla_verify_attn_shared(mla_verify_plan* plan, int batch, const void* q, const void* kv_cache,
+                           const int32_t* kv_indices, const int32_t* kv_indptr,
+                           const int32_t* kv_lens, const int32_t* draft_parent, float scale,
+                           int num_groups, const int32_t* group_indptr,
+                           const int32_t* shared_lens, void* out, float* lse, void* stream);
+
+/*
  * Read the sticky device error word (MLA_VERIFY_DEV_* bits) into
  * *device_status; clear it when `clear` is nonzero.  Waits for the plan's
  * last eagerly launched call (an event the plan records at the end of every

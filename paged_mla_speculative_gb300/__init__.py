@@ -19,5 +19,6 @@ from .binding import (  # noqa: F401
     load_library,
     mla_verify_attn,
     mla_verify_attn_host,
+    mla_verify_attn_shared,
     strerror,
 )

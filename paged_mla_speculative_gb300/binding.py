@@ -82,6 +82,8 @@ SIGNATURES = {
                                       _P, _P, _P]),
     "mla_verify_compact_kv": (_I, [_P, _I, _P, ctypes.c_int64, _P, _P, _P, _P, ctypes.c_int64, _P,
                                    ctypes.c_int64, _P, _P, _P]),
+    "mla_verify_attn_shared": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _I, _P, _P, _P, _P,
+                                    _P]),
     "mla_verify_append_kv": (_I, [_P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_float, _P,
                                   ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64,
                                   ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _I, _P, _P, _P]),
@@ -441,6 +443,42 @@ def compact_kv(plan: Plan, kv_src, kv_indices, kv_indptr, kv_lens, free_pages, k
         int(kv_dst.shape[0]), _ptr(page_table), _ptr(page_indptr), _stream_ptr(stream))
     _check(st, "mla_verify_compact_kv")
     return page_table, page_indptr
+
+
+def mla_verify_attn_shared(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_lens, draft_parent,
+                           scale: float, group_indptr, shared_lens, out=None, lse=None,
+                           stream=None):
+    """Verify attention of groups of requests that share their first rows;
+    returns (out, lse), the result of mla_verify_attn.
+
+    Arguments of mla_verify_attn, and group_indptr [G + 1] / shared_lens [G]
+    int32: requests group_indptr[g] .. group_indptr[g + 1] - 1 have the same
+    first shared_lens[g] rows, which are read and scored once for all of them.
+    Enqueued on ``stream`` (default: the current torch stream); no sync.
+    """
+    B, G = q.shape[0], shared_lens.shape[0]
+    dev = plan.torch_device
+    _expect(q, "q", torch.bfloat16, dev, (B, plan.T, plan.H, 576))
+    _expect(kv_cache, "kv_cache", torch.bfloat16, dev, (plan.num_slots, 576))
+    _expect(kv_indices, "kv_indices", torch.int32, dev)
+    _expect(kv_indptr, "kv_indptr", torch.int32, dev, (B + 1,))
+    _expect(kv_lens, "kv_lens", torch.int32, dev, (B,))
+    _expect(draft_parent, "draft_parent", torch.int32, dev, (B, plan.T))
+    _expect(group_indptr, "group_indptr", torch.int32, dev, (G + 1,))
+    _expect(shared_lens, "shared_lens", torch.int32, dev, (G,))
+    if out is None or lse is None:
+        o2, l2 = plan.new_outputs(B)
+        out = o2 if out is None else out
+        lse = l2 if lse is None else lse
+    _expect(out, "out", plan.out_dtype, dev, (B, plan.T, plan.H, 512))
+    _expect(lse, "lse", torch.float32, dev, (B, plan.T, plan.H))
+    st = load_library().mla_verify_attn_shared(
+        plan.handle, B, q.data_ptr(), kv_cache.data_ptr(), kv_indices.data_ptr(),
+        kv_indptr.data_ptr(), kv_lens.data_ptr(), draft_parent.data_ptr(), scale, G,
+        group_indptr.data_ptr(), shared_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        _stream_ptr(stream))
+    _check(st, "mla_verify_attn_shared")
+    return out, lse
 
 
 def append_kv(plan: Plan, kv, weight, eps: float, cos_sin, positions, slots, kv_cache, q_nope=None,

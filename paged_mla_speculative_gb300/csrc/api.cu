@@ -62,6 +62,15 @@ struct mla_verify_plan {
   // TMA descriptors of `packed` for the CTA-pair kernel.
   mlav::PackMaps pack_maps;
   unsigned* page_bits;    // page_size 64: one bit per page of the cache (free_kv)
+  // mla_verify_attn_shared: its packed keys and queries use `packed` and
+  // `st_q`, its partials ws_o and ws_lse; meta words and the call's layout
+  // have their own memory.
+  bool shared_ok;         // the packed key space has 32-bit positions
+  long long k_plane;      // keys it holds
+  int max_tiles;
+  int* sh_meta;
+  int* sh_layout;
+  mlav::SharedMaps sh_maps;
 };
 
 // The 256 bytes at mla_verify_plan::err: the error word, and fork_kv's ticket.
@@ -88,6 +97,32 @@ double step_us(int kernel) { return kernel == MLA_VERIFY_KERNEL_PAIR ? 4.8 : 3.4
 double fixed_us(int kernel) { return kernel == MLA_VERIFY_KERNEL_PAIR ? 20.0 : 16.0; }
 
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
+
+// Clusters of the shared-prefix attention kernel: one per SM pair.
+int shared_clusters(const mla_verify_plan* pl) { return pl->num_sms / 2; }
+
+// The layout arrays of a shared-prefix call, one after another in the plan's
+// sh_layout; returns the 32-bit words they take.
+size_t shared_layout(const mla_verify_plan* pl, mlav::SharedParams* p) {
+  size_t at = 0;
+  auto take = [&](size_t words) {
+    int* ptr = pl->sh_layout + at;
+    at += (words + 31) / 32 * 32;
+    return ptr;
+  };
+  const size_t B = static_cast<size_t>(pl->max_batch), tiles = static_cast<size_t>(pl->max_tiles);
+  p->base = take(2 * B + 1);
+  p->source = take(B);
+  p->group_of = take(B);
+  p->own = take(B);
+  p->anc = reinterpret_cast<uint32_t*>(take(B * pl->T));
+  p->tile0 = take(B + 1);
+  p->cost = take(tiles + 1);
+  p->tiles = reinterpret_cast<mlav::SharedTile*>(take(tiles * sizeof(mlav::SharedTile) / 4));
+  p->start = reinterpret_cast<mlav::SharedPos*>(take(2 * (static_cast<size_t>(shared_clusters(pl)) + 1)));
+  p->totals = take(2);
+  return at;
+}
 
 constexpr long long kDirectMaxTiles = 1;   // 2 tiles measured slower (each block gathered twice)
 
@@ -279,7 +314,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 void free_all(mla_verify_plan* p) {
   void* bufs[] = {p->ws_o, p->ws_lse, p->err, p->st_q, p->st_idx, p->st_indptr,
                   p->st_lens, p->st_parent, p->st_out, p->st_lse, p->packed, p->pack_sync,
-                  p->page_bits};
+                  p->page_bits, p->sh_meta, p->sh_layout};
   for (void* b : bufs)
     if (b) cudaFree(b);
 }
@@ -353,7 +388,8 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
   if (mlav::partial_mma_prepare() != cudaSuccess || mlav::partial_tc_prepare() != cudaSuccess ||
-      mlav::partial_pair_prepare() != cudaSuccess || mlav::pack_kv_prepare() != cudaSuccess)
+      mlav::partial_pair_prepare() != cudaSuccess || mlav::pack_kv_prepare() != cudaSuccess ||
+      mlav::partial_shared_prepare() != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
 
   mla_verify_plan* pl = new (std::nothrow) mla_verify_plan();
@@ -381,7 +417,9 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
   cap = std::max(cap, std::min(1LL * max_batch * std::min<long long>(mlav::MAX_NSPLIT, max_blocks),
                                std::max(floor_rs, std::min<long long>(mlav::MAX_NSPLIT, max_blocks))));
   pl->ws_capacity = cap;
-  const size_t rows = static_cast<size_t>(cap) * pl->R;
+  // The shared-prefix kernel's partials: two tiles per cluster.
+  const size_t rows = std::max(static_cast<size_t>(cap) * pl->R,
+                               static_cast<size_t>(2 * shared_clusters(pl)) * mlav::SH_ROWS);
   const size_t out_elt = out_dtype == MLA_VERIFY_OUT_BF16 ? 2 : 4;
   const long long idx_per_req = page_size == 1 ? max_kv_len : ceil_div(max_kv_len, mlav::PAGE);
   pl->st_idx_cap = idx_per_req * max_batch;
@@ -398,8 +436,13 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
             cudaMalloc(&pl->st_out, qrows * mlav::D_V * out_elt) == cudaSuccess &&
             cudaMalloc(&pl->st_lse, qrows * sizeof(float)) == cudaSuccess;
   pl->pack_blocks = static_cast<int>(ceil_div(max_kv_len, 128));
+  // One block more than the requests': the tail of the shared-prefix call's
+  // packed keys.
   const size_t packed_bytes =
-      static_cast<size_t>(max_batch) * pl->pack_blocks * mlav::packed_block_bytes();
+      (static_cast<size_t>(max_batch) * pl->pack_blocks + 1) * mlav::packed_block_bytes();
+  pl->k_plane = (static_cast<long long>(max_batch) * pl->pack_blocks + 1) * 128;
+  pl->max_tiles = static_cast<int>(std::min<long long>(ceil_div(1LL * max_batch * pl->R, mlav::SH_ROWS) + max_batch, INT32_MAX));
+  pl->shared_ok = pl->k_plane <= INT32_MAX && 1LL * max_batch * pl->R <= INT32_MAX / 2 && max_batch < mlav::SH_MAX_BATCH;
   ok = ok && cudaMalloc(&pl->packed, packed_bytes) == cudaSuccess;
   ok = ok && mlav::make_pack_maps(&pl->pack_maps, pl->packed, packed_bytes) == cudaSuccess;
   const size_t sync_bytes =
@@ -409,13 +452,22 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
   pl->pack_sync_bytes = sync_bytes;
   const size_t bit_bytes = page_size == mlav::PAGE ? static_cast<size_t>(ceil_div(num_slots / mlav::PAGE, 32)) * 4 : 0;
   ok = ok && (!bit_bytes || cudaMalloc(&pl->page_bits, bit_bytes) == cudaSuccess);
+  size_t shared_bytes = 0;
+  if (pl->shared_ok) {
+    mlav::SharedParams sp{};
+    shared_bytes = static_cast<size_t>(pl->k_plane) * 4 + shared_layout(pl, &sp) * 4;
+    ok = ok && cudaMalloc(&pl->sh_meta, static_cast<size_t>(pl->k_plane) * 4) == cudaSuccess &&
+         cudaMalloc(&pl->sh_layout, shared_layout(pl, &sp) * 4) == cudaSuccess &&
+         mlav::make_shared_maps(&pl->sh_maps, pl->packed, pl->k_plane, pl->st_q, static_cast<long long>(qrows)) == cudaSuccess;
+  }
   if (!ok) {
     cudaGetLastError();
     free_all(pl);
     delete pl;
     return MLA_VERIFY_ERR_OOM;
   }
-  pl->ws_bytes = rows * (mlav::D_V + 1) * sizeof(float) + 256 + packed_bytes + sync_bytes + bit_bytes;
+  pl->ws_bytes = rows * (mlav::D_V + 1) * sizeof(float) + 256 + packed_bytes + sync_bytes + bit_bytes +
+                 shared_bytes;
   if (cudaMemset(pl->err, 0, 256) != cudaSuccess || cudaMemset(pl->pack_sync, 0, sync_bytes) != cudaSuccess ||
       (bit_bytes && cudaMemset(pl->page_bits, 0, bit_bytes) != cudaSuccess) ||
       cudaEventCreateWithFlags(&pl->done_ev, cudaEventDisableTiming) != cudaSuccess ||
@@ -835,6 +887,64 @@ int mla_verify_compact_kv(mla_verify_plan* pl, int batch, const void* kv_src, in
   a.err = pl->err;
   if (mlav::launch_compact_kv(a, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
       note_done(pl, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return MLA_VERIFY_ERR_CUDA;
+  return MLA_VERIFY_OK;
+}
+
+int mla_verify_attn_shared(mla_verify_plan* pl, int batch, const void* q, const void* kv_cache,
+                           const int32_t* kv_indices, const int32_t* kv_indptr, const int32_t* kv_lens,
+                           const int32_t* draft_parent, float scale, int num_groups,
+                           const int32_t* group_indptr, const int32_t* shared_lens, void* out, float* lse,
+                           void* stream) {
+  if (!pl || !q || !kv_cache || !kv_indices || !kv_indptr || !kv_lens || !draft_parent || !group_indptr ||
+      !shared_lens || !out || !lse)
+    return MLA_VERIFY_ERR_NULL;
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(kv_indices) || !aligned16(kv_indptr) ||
+      !aligned16(kv_lens) || !aligned16(draft_parent) || !aligned16(group_indptr) || !aligned16(shared_lens) ||
+      !aligned16(out) || !aligned16(lse))
+    return MLA_VERIFY_ERR_ALIGN;
+  if (!pl->shared_ok) return MLA_VERIFY_ERR_SHAPE;
+  if (batch < 1 || batch > pl->max_batch) return MLA_VERIFY_ERR_BATCH;
+  if (!std::isfinite(scale)) return MLA_VERIFY_ERR_SCALE;
+  if (num_groups < 1 || num_groups > pl->max_batch) return MLA_VERIFY_ERR_ARG;
+  const int dev_status = check_device(pl);
+  if (dev_status != MLA_VERIFY_OK) return dev_status;
+  mlav::SharedParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint16_t*>(kv_cache);
+  p.kv_indices = kv_indices;
+  p.kv_indptr = kv_indptr;
+  p.kv_lens = kv_lens;
+  p.draft_parent = draft_parent;
+  p.group_indptr = group_indptr;
+  p.shared_lens = shared_lens;
+  p.scale_log2 = scale * mlav::kLog2e;
+  p.batch = batch;
+  p.groups = num_groups;
+  p.T = pl->T;
+  p.H = pl->H;
+  p.R = pl->R;
+  p.page_size = pl->page_size;
+  p.num_slots = pl->num_slots;
+  p.max_kv_len = pl->max_kv_len;
+  p.clusters = shared_clusters(pl);
+  p.max_tiles = static_cast<int>(ceil_div(1LL * batch * pl->R, mlav::SH_ROWS)) + num_groups;
+  p.out = out;
+  p.lse = lse;
+  p.out_bf16 = pl->out_dtype == MLA_VERIFY_OUT_BF16;
+  p.err = pl->err;
+  p.q16 = static_cast<uint16_t*>(pl->st_q);
+  p.q_plane = 1LL * pl->max_batch * pl->R;
+  p.k16 = static_cast<uint16_t*>(pl->packed);
+  p.k_plane = pl->k_plane;
+  p.meta = pl->sh_meta;
+  shared_layout(pl, &p);
+  p.part_o = pl->ws_o;
+  p.part_lse = pl->ws_lse;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (mlav::launch_shared_plan(p, s) != cudaSuccess || mlav::launch_shared_pack(p, pl->num_sms, s) != cudaSuccess ||
+      mlav::launch_partial_shared(p, pl->sh_maps, s) != cudaSuccess || mlav::launch_shared_join(p, s) != cudaSuccess ||
+      note_done(pl, s) != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
   return MLA_VERIFY_OK;
 }

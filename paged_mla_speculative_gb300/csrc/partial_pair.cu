@@ -54,6 +54,7 @@
 // copies, measured microseconds on this path.
 #include "common.cuh"
 #include "kernels.h"
+#include "pair_common.cuh"
 #include "tc_ptx.cuh"
 
 #include <cuda_bf16.h>
@@ -113,7 +114,6 @@ constexpr int MB_DONE = 18;    // after an abort: every MMA issued is done
 
 constexpr int TMEM_COLS = 512;
 constexpr uint32_t TM_S = 256;                  // S^T buffer u at 256 + 128u; O^T tile t at 128t
-constexpr long long WAIT_LIMIT = 1LL << 31;     // cycles before a wait gives up
 
 constexpr uint32_t IDESC_S = tc::idesc_f16(256, ROWS, 0, 0, 0);   // fp16, both K-major
 constexpr uint32_t IDESC_O = tc::idesc_f16(256, ROWS, 0, 1, 1);   // fp16, both MN-major
@@ -125,40 +125,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int sr
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src),
                "r"(src_bytes));
 }
-__device__ __forceinline__ void named_sync(int id, int count) {
-  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory");
-}
-
-// Bounded wait (acquire at cluster scope: some arrivals come from the peer
-// CTA).  A timeout, or an earlier one in this CTA, returns false.
-__device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, volatile int* abort, int* err) {
-  if (tc::mbar_try_cluster(mbar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-    if (tc::mbar_try_cluster(mbar, parity)) return true;
-    if (*abort) return false;
-    if (clock64() - t0 > WAIT_LIMIT) {
-      *abort = 1;
-      atomicOr(err, ERR_TIMEOUT);
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ void wait_warp(uint32_t mbar, uint32_t parity, volatile int* abort, int* err) {
-  wait_phase(mbar, parity, abort, err);
-  __syncwarp();
-}
-// Bounded wait that ignores the abort flag (own copies in flight at exit).
-__device__ __forceinline__ void wait_drain(uint32_t mbar, uint32_t parity, int* err) {
-  const long long t0 = clock64();
-  while (!tc::mbar_try(mbar, parity)) {
-    if (clock64() - t0 > WAIT_LIMIT) {
-      atomicOr(err, ERR_TIMEOUT);
-      return;
-    }
-  }
-}
-
 // Same as partial_tc.cu: wait (bounded) for the 32 ready flags of packed
 // block kb of request b carrying this call's tag.  Whole warp.
 __device__ __forceinline__ bool wait_packed(const Params& p, int b, int kb, unsigned long long tag,
@@ -194,41 +160,12 @@ __device__ __forceinline__ void finish_call(const Params& p) {
   }
 }
 
-// Column maxima / sums of a warp's 32 x 32 tile (lane = key, v[c] = column
-// c) in 31 shuffles: lane l ends with column l's result in v[0].
-template <bool SUM>
-__device__ __forceinline__ void transpose_reduce32(float (&v)[32], int lane) {
-#pragma unroll
-  for (int w = 16; w >= 1; w >>= 1) {
-    const bool upper = (lane & w) != 0;
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const float send = upper ? v[i] : v[i + w];
-      const float keep = upper ? v[i + w] : v[i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, w);
-      v[i] = SUM ? keep + got : fmaxf(keep, got);
-    }
-  }
-}
-
 // Slot of key r of 128-key block kb, or -1 past the call's keys or when the
 // table points outside the cache.
 __device__ __forceinline__ int block_slot(const Params& p, const Request& rq, int kb, int r) {
   const int j = kb * BN + r;
   if (j < rq.lo || j >= rq.hi) return -1;
   return static_cast<int>(key_slot(p, rq.ip0, j));
-}
-
-// Ring unit order shared by the copy warps and the MMA warp.  Phase f of 2n:
-// S(0), S(1), O(0), S(2), O(1), .., S(n-1), O(n-2), O(n-1); S(i) = the CTA's
-// own block's chunk pairs 0..3 (and its rope chunk, into the rope slot),
-// O(i) = for t in 0,1 and key half h in 0,1: chunk pair 2t + rank of block
-// 2i + h.  Unit n goes to slot n % 3.
-__device__ __forceinline__ void phase_of(int f, int n, bool& is_s, int& i) {
-  if (f == 0) { is_s = true; i = 0; }
-  else if (f == 2 * n - 1) { is_s = false; i = n - 1; }
-  else if (f & 1) { is_s = true; i = (f + 1) >> 1; }
-  else { is_s = false; i = (f >> 1) - 1; }
 }
 
 // Rows of this CTA's output: NaN (a request the kernel cannot serve).
@@ -254,14 +191,6 @@ __device__ __forceinline__ void write_nan_rows(const Params& p, int b, int split
   }
 }
 
-
-// Spin about `cycles` (an abort path: lets copies and remote stores that
-// are still in flight land before the pair leaves).
-__device__ __forceinline__ void settle(long long cycles) {
-  const long long t0 = clock64();
-  while (clock64() - t0 < cycles) {
-  }
-}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     partial_pair_kernel(const Params p, const __grid_constant__ CUtensorMap tm_pair,

@@ -1,0 +1,660 @@
+// Attention of groups of requests that share their first rows: a persistent
+// kernel on CTA pairs (tcgen05 cta_group::2) over the packed planes of
+// shared_pack.cu.
+//
+// A tile of 128 query rows of a group -- of one request, or of several -- is
+// scored against the group's shared keys once and then against its requests'
+// own keys, in one softmax: every shared row is read once per 128 query rows
+// of the group, not once per request.  The products, the softmax and the
+// exchange between the two CTAs of a pair are those of partial_pair.cu:
+//     S^T[key, row] = K_pair[256 x 576] . Q_tile[128 x 576]^T
+//     O^T[dim, row] += V_pair^T[512 x 256] . P^T[256 x 128]
+// with the running maximum and sum in fp32, P in fp16 (rounded once; with the
+// bf16 keys widened to fp16, which is exact, its 2^-12 is the largest error),
+// O^T in tensor memory, split by value dim over the two CTAs.
+//
+// What differs is the schedule.  The grid is one cluster per SM pair; cluster
+// c walks the steps from start[c] to start[c + 1] of the list of all tiles'
+// steps, so every pair works to the end whatever the lengths.  It runs as one
+// continuous pipeline over its segments (a segment: consecutive steps of one
+// tile): the ring of key chunks, the score buffers and all barrier phases
+// carry on over the border, the next tile's queries are loaded as soon as the
+// last S^T of the current one is done, and its first products are issued while
+// the softmax warps still read out the finished O^T.
+//
+// A tile that one cluster holds whole is normalised and stored directly;
+// otherwise the segment's partial goes to the workspace for shared_join_kernel.
+//
+// Roles (21 warps per CTA): warps 0-15 softmax, warp 16 MMA issue (even CTA)
+// or P^T hand-off (odd CTA), warps 17-19 the key ring, warp 20 the queries.
+// Every wait is bounded; after a timeout all of the cluster's rows are NaN.
+#include "shared.cuh"
+#include "kernels.h"
+#include "pair_common.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace mlav {
+namespace {
+
+constexpr int ROWS = SH_ROWS;       // query rows per pair: MMA N
+constexpr int HROWS = ROWS / 2;     // rows of the B operands a CTA holds
+constexpr int BN = SH_HALF;         // keys per CTA per step
+constexpr int SOFTMAX_WARPS = 16, MMA_WARP = 16, COPY_WARP = 17;
+constexpr int NCOPY = 3;            // copy warp k fills ring slot k
+constexpr int Q_WARP = COPY_WARP + NCOPY;
+constexpr int NWARPS = Q_WARP + 1;
+constexpr int NTHREADS = NWARPS * 32;
+constexpr int SM_THREADS = SOFTMAX_WARPS * 32;
+constexpr int CHUNK = BN * 128;          // 16 KB: 128 keys x 64 dims fp16
+constexpr int Q_CHUNK = HROWS * 128;     // 8 KB: 64 rows x 64 dims
+constexpr int Q_PLANES = 3;              // planes per query load
+constexpr int NSLOT = NCOPY;
+constexpr int OFF_Q = 0;
+constexpr int OFF_P = OFF_Q + 9 * Q_CHUNK;            // P^T [key half][128 keys][64 rows] fp16
+constexpr int OFF_RING = OFF_P + 2 * CHUNK;
+constexpr int OFF_ROPE = OFF_RING + NSLOT * 2 * CHUNK;
+constexpr int OFF_RED = OFF_ROPE + CHUNK;             // float [128 rows][4 quads]
+constexpr int OFF_XMAX = OFF_RED + ROWS * 4 * 4;      // float [2][128] the peer's row max of the step
+constexpr int OFF_XSUM = OFF_XMAX + 2 * ROWS * 4;     // float [128] the peer's row sums
+constexpr int OFF_M = OFF_XSUM + ROWS * 4;            // float [128] running row max (0: none yet)
+constexpr int OFF_A = OFF_M + ROWS * 4;               // float [128] rescale factor of the step
+constexpr int OFF_L = OFF_A + ROWS * 4;               // float [128] 1 / row sum (0: none)
+constexpr int OFF_ROW = OFF_L + ROWS * 4;             // int2 [128] request of the row (-1: not served), ancestor mask
+constexpr int OFF_MBAR = OFF_ROW + ROWS * 8;
+constexpr int NMBAR = 20;
+constexpr int OFF_MISC = OFF_MBAR + NMBAR * 8;        // tmem base, P-complete word, absent-unit word, abort flag
+constexpr int SMEM_TOTAL = OFF_MISC + 16;
+static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
+static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && OFF_ROPE % 1024 == 0,
+              "swizzled tiles need 1024-byte alignment");
+
+// mbarrier indices (same offsets in both CTAs)
+constexpr int MB_FULL = 0;     // [3] even CTA: ring slot landed in both CTAs (bytes of both)
+constexpr int MB_EMPTY = 3;    // [3] ring slot read by its MMAs (commit to both CTAs)
+constexpr int MB_RFULL = 6;    // even CTA: rope slot landed in both CTAs
+constexpr int MB_REMPTY = 7;   // rope slot read
+constexpr int MB_S = 8;        // [2] S^T buffer done
+constexpr int MB_P = 10;       // this CTA's softmax warps wrote their P^T and rescaled O^T
+constexpr int MB_PX = 11;      // the peer's half of this CTA's P^T landed (st.async bytes)
+constexpr int MB_PF = 12;      // even CTA: the odd CTA's P^T is complete (st.async word)
+constexpr int MB_OT = 13;      // O^T of a step done
+constexpr int MB_Q = 14;       // even CTA: both halves of a segment's queries landed
+constexpr int MB_QE = 15;      // the segment's last S^T is done: its queries can go
+constexpr int MB_X = 16;       // [2] the peer's row max of the step landed (st.async bytes)
+constexpr int MB_XS = 18;      // the peer's row sums landed (st.async bytes)
+constexpr int MB_DONE = 19;    // after an abort: every MMA issued is done
+
+constexpr int TMEM_COLS = 512;
+constexpr uint32_t TM_S = 256;                  // S^T buffer u at 256 + 128u; O^T tile t at 128t
+
+constexpr uint32_t IDESC_S = tc::idesc_f16(256, ROWS, 0, 0, 0);   // fp16, both K-major
+constexpr uint32_t IDESC_O = tc::idesc_f16(256, ROWS, 0, 1, 1);   // fp16, both MN-major
+
+constexpr int FEW_MOVED = 4;
+constexpr uint32_t ABSENT_BYTES = 4;   // the odd CTA's signal for a unit it has no half block for
+
+struct Segment {
+  SharedTile t;
+  int tile, sa, steps;   // steps sa .. sa + steps - 1 of the tile
+  bool first, whole;     // the cluster's first segment; the tile's only one
+};
+// The cluster's next segment at or after tile `tile`; false when there is none.
+__device__ __forceinline__ bool next_segment(const SharedParams& p, const SharedPos& from, const SharedPos& to, int tile,
+                                             Segment& s) {
+  for (; tile < to.tile || (tile == to.tile && to.step > 0); ++tile) {
+    const int4* rec = reinterpret_cast<const int4*>(p.tiles + tile);
+    const int4 a = __ldg(rec), b = __ldg(rec + 1), c = __ldg(rec + 2);
+    s.t = SharedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, 0};
+    s.tile = tile;
+    s.sa = tile == from.tile ? from.step : 0;
+    s.steps = (tile == to.tile ? to.step : s.t.steps) - s.sa;
+    s.first = tile == from.tile;
+    s.whole = s.t.nseg == 1;
+    if (s.steps > 0) return true;
+  }
+  return false;
+}
+
+// NaN for every row of the segment (a call that gave up).
+__device__ __forceinline__ void write_nan_segment(const SharedParams& p, const Segment& s, int cluster, uint32_t rank, int tid) {
+  const float nan = __int_as_float(0x7fc00000);
+  for (int i = tid; i < s.t.nrows * 256; i += NTHREADS) {
+    const int r = i >> 8, d = static_cast<int>(rank) * 256 + (i & 255);
+    if (s.whole) {
+      const size_t at = static_cast<size_t>(s.t.q_row0 + r) * D_V + d;
+      if (p.out_bf16) reinterpret_cast<uint16_t*>(p.out)[at] = 0x7fc0;
+      else reinterpret_cast<float*>(p.out)[at] = nan;
+      if (d == 0) p.lse[s.t.q_row0 + r] = nan;
+    } else if (d == 0) {
+      p.part_lse[static_cast<size_t>(part_slot(cluster, s.first)) * ROWS + r] = nan;
+    }
+  }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
+    partial_shared_kernel(const SharedParams p, const __grid_constant__ CUtensorMap tm_pair,
+                          const __grid_constant__ CUtensorMap tm_chunk, const __grid_constant__ CUtensorMap tm_q) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t rank = tc::cluster_rank();
+  const uint32_t peer = rank ^ 1u;
+  const int cluster = blockIdx.x >> 1;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int quad = warp & 3;            // TMEM lanes 32*quad .. +32 are this warp's
+  const int grp = warp >> 2;            // softmax: rows 32*grp .. +32
+
+  float* s_red = reinterpret_cast<float*>(smem + OFF_RED);
+  float* s_xmax = reinterpret_cast<float*>(smem + OFF_XMAX);
+  float* s_xsum = reinterpret_cast<float*>(smem + OFF_XSUM);
+  float* s_m = reinterpret_cast<float*>(smem + OFF_M);
+  float* s_a = reinterpret_cast<float*>(smem + OFF_A);
+  float* s_l = reinterpret_cast<float*>(smem + OFF_L);
+  int2* s_row = reinterpret_cast<int2*>(smem + OFF_ROW);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + OFF_MISC + 12);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t mbar0 = sbase + OFF_MBAR;
+  auto mbar = [&](int i) { return mbar0 + 8u * static_cast<uint32_t>(i); };
+
+  if (tid == 0) {
+    for (int i = 0; i < NMBAR; ++i) tc::mbar_init(mbar(i), i == MB_P ? SOFTMAX_WARPS : 1);
+    tc::mbar_fence_init();
+    *s_abort = 0;
+  }
+  if (warp == MMA_WARP) tc::tmem_alloc_pair<TMEM_COLS>(smem_u32(s_tmem));
+  tc::fence_before_sync();
+  __syncthreads();
+  // The peer's barriers exist and the pair's TMEM is allocated.
+  tc::cluster_sync_relaxed();
+  tc::fence_after_sync();
+  const uint32_t tmem = *s_tmem;
+  const uint32_t even_mbar0 = tc::peer_addr(mbar0, 0);   // the even CTA's barriers
+  const uint32_t peer_mbar0 = tc::peer_addr(mbar0, peer);
+  auto even_mbar = [&](int i) { return even_mbar0 + 8u * static_cast<uint32_t>(i); };
+  auto peer_mbar = [&](int i) { return peer_mbar0 + 8u * static_cast<uint32_t>(i); };
+  // Everything read from here on was written by the planning and packing kernels.
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  SharedPos from = p.start[cluster], to = p.start[cluster + 1];
+  if (sbase & 1023) {   // the swizzled tiles need it (uniform over the pair)
+    if (tid == 0) {
+      atomicOr(p.err, ERR_INTERNAL);
+      *s_abort = 1;
+    }
+    __syncthreads();
+    to = from;
+  }
+  Segment s;
+
+  if (warp >= COPY_WARP && warp < Q_WARP) {
+    // ========================= key chunk producers ==========================
+    // As in partial_pair.cu: unit n goes to slot n % 3, one warp per slot; the
+    // rope chunks go with slot 2; a half block the odd CTA does not have is
+    // signalled by ABSENT_BYTES, so that no CTA's barriers run ahead.
+    const int cw = warp - COPY_WARP;
+    const uint32_t absent_word = tc::peer_addr(smem_u32(s_tmem + 2), 0);
+    int n = 0, g0 = 0;   // units so far, steps of the segments before
+#pragma unroll 1
+    for (int tile = from.tile; next_segment(p, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps) {
+#pragma unroll 1
+      for (int f = 0; f < 2 * s.steps && !*s_abort; ++f) {
+        bool is_s;
+        int i;
+        phase_of(f, s.steps, is_s, i);
+        const int hb0 = 2 * (s.sa + i);
+        int count;
+#pragma unroll 1
+        for (int u = 0; u < 4; ++u, ++n) {
+          const int slot = n % NSLOT;
+          if (slot != cw) continue;
+          // S units: the own half block (the peer loads its own); O units:
+          // half block h in both CTAs.
+          const int h = is_s ? static_cast<int>(rank) : (u & 1);
+          const int pair_idx = is_s ? u : 2 * (u >> 1) + static_cast<int>(rank);
+          const bool mine = hb0 + h < s.t.halves;
+          const bool peers = is_s ? hb0 + static_cast<int>(peer) < s.t.halves : mine;
+          if (n >= NSLOT) wait_warp(mbar(MB_EMPTY + slot), static_cast<uint32_t>((n / NSLOT - 1) & 1), s_abort, p.err);
+          if (*s_abort) break;
+          if (rank == 0) {
+            if (lane == 0)
+              tc::mbar_arrive_expect(mbar(MB_FULL + slot), (mine ? 2 * CHUNK : 0) + (peers ? 2 * CHUNK : ABSENT_BYTES));
+            __syncwarp();
+          }
+          if (mine) {
+            tc::tma_load_3d_pair(sbase + OFF_RING + slot * 2 * CHUNK, &tm_pair, 0, half_base(s.t, hb0 + h, count), 2 * pair_idx,
+                                 even_mbar(MB_FULL + slot));
+          } else if (rank == 1) {
+            if (lane == 0) tc::st_async_b32(absent_word, 0, even_mbar(MB_FULL + slot));
+            __syncwarp();
+          }
+        }
+        if (*s_abort) break;
+        if (is_s && cw == NCOPY - 1) {
+          const int g = g0 + i;
+          const bool mine = hb0 + static_cast<int>(rank) < s.t.halves, peers = hb0 + static_cast<int>(peer) < s.t.halves;
+          if (g > 0) wait_warp(mbar(MB_REMPTY), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
+          if (*s_abort) break;
+          if (rank == 0) {
+            if (lane == 0) tc::mbar_arrive_expect(mbar(MB_RFULL), (mine ? CHUNK : 0) + (peers ? CHUNK : ABSENT_BYTES));
+            __syncwarp();
+          }
+          if (mine) {
+            tc::tma_load_3d_pair(sbase + OFF_ROPE, &tm_chunk, 0, half_base(s.t, hb0 + static_cast<int>(rank), count), 8,
+                                 even_mbar(MB_RFULL));
+          } else if (rank == 1) {
+            if (lane == 0) tc::st_async_b32(absent_word, 0, even_mbar(MB_RFULL));
+            __syncwarp();
+          }
+        }
+      }
+    }
+    // After an abort, copies already issued land within microseconds: wait
+    // far longer than that before the pair's shared memory can be released.
+    if (*s_abort) settle(1LL << 22);
+  } else if (warp == Q_WARP) {
+    // ============================== queries =================================
+    // Rows past the tile are the next tile's (or zeros past the batch): their
+    // columns of S^T and O^T are not stored.
+    int k = 0;
+#pragma unroll 1
+    for (int tile = from.tile; next_segment(p, from, to, tile, s); tile = s.tile + 1, ++k) {
+      if (k > 0) wait_warp(mbar(MB_QE), static_cast<uint32_t>((k - 1) & 1), s_abort, p.err);
+      if (*s_abort) break;
+      if (rank == 0) {
+        if (lane == 0) tc::mbar_arrive_expect(mbar(MB_Q), 2 * 9 * Q_CHUNK);
+        __syncwarp();
+      }
+#pragma unroll
+      for (int z = 0; z < 9; z += Q_PLANES)
+        tc::tma_load_3d_pair(sbase + OFF_Q + z * Q_CHUNK, &tm_q, 0, s.t.q_row0 + static_cast<int>(rank) * HROWS, z,
+                             even_mbar(MB_Q));
+    }
+    if (*s_abort) settle(1LL << 22);
+  } else if (warp == MMA_WARP && rank == 1) {
+    // =================== odd CTA: P^T complete -> even CTA ==================
+    uint32_t* s_word = s_tmem + 1;
+    const uint32_t even_word = tc::peer_addr(smem_u32(s_word), 0);
+    int g = 0;
+#pragma unroll 1
+    for (int tile = from.tile; next_segment(p, from, to, tile, s); tile = s.tile + 1) {
+#pragma unroll 1
+      for (int i = 0; i < s.steps; ++i, ++g) {
+        if (lane == 0) tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
+        __syncwarp();
+        wait_warp(mbar(MB_P), static_cast<uint32_t>(g & 1), s_abort, p.err);
+        wait_warp(mbar(MB_PX), static_cast<uint32_t>(g & 1), s_abort, p.err);
+        tc::fence_async_smem();   // the st.async bytes are read by the tensor core next
+        if (lane == 0) tc::st_async_b32(even_word, static_cast<uint32_t>(g), even_mbar(MB_PF));
+        __syncwarp();
+      }
+    }
+  } else if (warp == MMA_WARP) {
+    // ======================= MMA issuer (even CTA) ==========================
+    int n = 0, g0 = 0, k = 0;
+#pragma unroll 1
+    for (int tile = from.tile; next_segment(p, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
+      wait_warp(mbar(MB_Q), static_cast<uint32_t>(k & 1), s_abort, p.err);
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int f = 0; f < 2 * s.steps && !*s_abort; ++f) {
+        bool is_s;
+        int i;
+        phase_of(f, s.steps, is_s, i);
+        const int g = g0 + i;
+        if (is_s) {
+          const uint32_t d = tmem + TM_S + 128u * static_cast<uint32_t>(g & 1);
+#pragma unroll 1
+          for (int u = 0; u < 4; ++u, ++n) {
+            const int slot = n % NSLOT;
+            wait_warp(mbar(MB_FULL + slot), static_cast<uint32_t>((n / NSLOT) & 1), s_abort, p.err);
+            tc::fence_after_sync();
+            const uint32_t base = sbase + OFF_RING + slot * 2 * CHUNK;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const int c = 8 * u + kk;   // 16-dim step of the 576-dim contraction
+              const uint64_t a = tc::desc_sw128(base + (kk >> 2) * CHUNK + (kk & 3) * 32, 16, 1024);
+              const uint64_t bq = tc::desc_sw128(sbase + OFF_Q + (c >> 2) * Q_CHUNK + (c & 3) * 32, 16, 1024);
+              tc::mma_pair(d, a, bq, IDESC_S, c > 0);
+            }
+            tc::commit_pair(mbar(MB_EMPTY + slot));
+          }
+          wait_warp(mbar(MB_RFULL), static_cast<uint32_t>(g & 1), s_abort, p.err);
+          tc::fence_after_sync();
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t a = tc::desc_sw128(sbase + OFF_ROPE + kk * 32, 16, 1024);
+            const uint64_t bq = tc::desc_sw128(sbase + OFF_Q + 8 * Q_CHUNK + kk * 32, 16, 1024);
+            tc::mma_pair(d, a, bq, IDESC_S, 1);
+          }
+          tc::commit_pair(mbar(MB_REMPTY));
+          tc::commit_pair(mbar(MB_S + (g & 1)));
+          if (i == s.steps - 1) tc::commit_pair(mbar(MB_QE));
+        } else {
+          // P^T of the step: this CTA's softmax warps, the odd CTA's st.async
+          // bytes, and the odd CTA's word that its own half is complete.
+          if (lane == 0) {
+            tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
+            tc::mbar_arrive_expect(mbar(MB_PF), 4);
+          }
+          __syncwarp();
+          wait_warp(mbar(MB_P), static_cast<uint32_t>(g & 1), s_abort, p.err);
+          wait_warp(mbar(MB_PX), static_cast<uint32_t>(g & 1), s_abort, p.err);
+          wait_warp(mbar(MB_PF), static_cast<uint32_t>(g & 1), s_abort, p.err);
+          tc::fence_async_smem();
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int u = 0; u < 4; ++u, ++n) {
+            const int t = u >> 1, h = u & 1;
+            const int slot = n % NSLOT;
+            wait_warp(mbar(MB_FULL + slot), static_cast<uint32_t>((n / NSLOT) & 1), s_abort, p.err);
+            tc::fence_after_sync();
+            if (2 * (s.sa + i) + h < s.t.halves) {
+              const uint32_t base = sbase + OFF_RING + slot * 2 * CHUNK;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {   // 16-key steps of the key half
+                const uint64_t a = tc::desc_sw128(base + kk * 2048, CHUNK, 1024);
+                const uint64_t bp = tc::desc_sw128(sbase + OFF_P + h * CHUNK + kk * 2048, CHUNK, 1024);
+                tc::mma_pair(tmem + 128u * static_cast<uint32_t>(t), a, bp, IDESC_O, (i > 0 || h > 0 || kk > 0) ? 1u : 0u);
+              }
+            }
+            tc::commit_pair(mbar(MB_EMPTY + slot));
+          }
+          tc::commit_pair(mbar(MB_OT));
+        }
+      }
+    }
+    // After an abort: every MMA issued finishes before TMEM is freed.
+    if (__any_sync(0xffffffffu, *s_abort != 0)) {
+      tc::commit_pair(mbar(MB_DONE));
+      wait_drain(mbar(MB_DONE), 0, p.err);
+    }
+  } else {
+    // ============================= softmax =================================
+    // These warps never leave the loops early (they meet at named barriers);
+    // after an abort their waits return at once.
+    const int j = quad * 32 + lane;     // key of this thread = TMEM lane
+    const int c0 = grp * 32;            // pair rows c0 .. c0+31
+    const float scale2 = p.scale_log2;
+    const bool owner = quad == 0;       // lane l owns row c0 + l's running max
+    // This key's P^T row (key half = rank) in the CTA that holds the group's
+    // rows: a local store, or st.async into the peer with its MB_PX.
+    const bool p_local = (grp >> 1) == static_cast<int>(rank);
+    const uint32_t p_off = OFF_P + rank * CHUNK + j * 128;
+    const uint32_t p_peer = tc::peer_addr(sbase + p_off, peer);
+    const uint32_t xmax_peer = tc::peer_addr(sbase + OFF_XMAX, peer);
+    int g = 0, k = 0;   // steps and segments so far
+#pragma unroll 1
+    for (int tile = from.tile; next_segment(p, from, to, tile, s); tile = s.tile + 1, ++k) {
+      auto load_meta = [&](int step) {
+        int count;
+        const int hb = 2 * (s.sa + step) + static_cast<int>(rank);
+        if (step >= s.steps || hb >= s.t.halves) return META_MASKED;
+        const int base = half_base(s.t, hb, count);
+        return j < count ? __ldg(p.meta + base + j) : META_MASKED;
+      };
+      int meta = load_meta(0);
+      named_sync(1, SM_THREADS);   // the previous segment's rows are read
+      if (tid < ROWS) {
+        int2 row = make_int2(-1, 0);
+        if (tid < s.t.nrows) {
+          const int q = s.t.q_row0 + tid, b = q / p.R;
+          if (__ldg(p.own + b) > 0) row = make_int2(b, static_cast<int>(__ldg(p.anc + b * p.T + (q - b * p.R) / p.H)));
+        }
+        s_row[tid] = row;
+      }
+      named_sync(1, SM_THREADS);
+      float mrow = -INFINITY;
+      float lrun = 0.f;                   // row c0 + lane's sum over this warp's keys so far
+#pragma unroll 1
+      for (int it = 0; it < s.steps; ++it, ++g) {
+        // The group's rows that see this key (bit c: row c0 + c), decided
+        // while S^T is computed.
+        uint32_t vis = 0;
+        if (meta >= 0) {
+          const int m = meta & ~META_POISON;
+          if (m == META_SHARED) {
+            vis = 0xffffffffu;
+          } else {
+            const int b = m >> 6, d = (m & 63) - 2;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const int2 row = s_row[c0 + c];
+              const bool v = row.x == b && (d < 0 || ((static_cast<uint32_t>(row.y) >> d) & 1u));
+              vis |= (v ? 1u : 0u) << c;
+            }
+          }
+        }
+        const float visible = meta >= 0 && (meta & META_POISON) ? __int_as_float(0x7fc00000) : scale2;
+        meta = load_meta(it + 1);
+        const uint32_t sb = static_cast<uint32_t>(g & 1);
+        wait_warp(mbar(MB_S + sb), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
+        tc::fence_after_sync();
+        const uint32_t s_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + TM_S + 128u * sb + c0;
+        float x[32];
+        auto load_scores = [&]() { tc::tmem_ld32f(s_addr, x); };
+        auto mask_scores = [&]() {
+          if (vis == 0xffffffffu) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] *= visible;
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[c] = (vis >> c) & 1u ? x[c] * visible : -INFINITY;
+          }
+        };
+        load_scores();
+        tc::tmem_wait_ld();
+        mask_scores();
+        transpose_reduce32<false>(x, lane);
+        s_red[(c0 + lane) * 4 + quad] = x[0];
+        named_sync(1, SM_THREADS);
+        if (owner) {
+          const float4 q4 = *reinterpret_cast<const float4*>(s_red + (c0 + lane) * 4);
+          float bm = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
+          tc::st_async_b32(xmax_peer + (sb * ROWS + c0 + lane) * 4, __float_as_uint(bm), peer_mbar(MB_X + sb));
+          if (tid == 0) tc::mbar_arrive_expect(mbar(MB_X + sb), ROWS * 4);
+          wait_phase(mbar(MB_X + sb), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
+          bm = fmaxf(bm, s_xmax[sb * ROWS + c0 + lane]);
+          float alpha = 1.f;
+          if (bm > mrow) {
+            if (mrow != -INFINITY) alpha = ex2(mrow - bm);
+            mrow = bm;
+          }
+          s_m[c0 + lane] = mrow == -INFINITY ? 0.f : mrow;   // a fully masked row: p = ex2(-inf) = 0
+          s_a[c0 + lane] = alpha;
+        }
+        named_sync(1, SM_THREADS);
+        // Rows whose max moved (the same mask in every lane).
+        uint32_t moved_rows = 0;
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          const float4 a4 = *reinterpret_cast<const float4*>(s_a + c0 + c);
+          moved_rows |= (a4.x != 1.f ? 1u : 0u) << c | (a4.y != 1.f ? 1u : 0u) << (c + 1) |
+                        (a4.z != 1.f ? 1u : 0u) << (c + 2) | (a4.w != 1.f ? 1u : 0u) << (c + 3);
+        }
+        // O^T of the step before done: the P^T buffers (here and in the peer)
+        // are free and O^T can be rescaled.  (A segment's first step: the
+        // readout waited for it.)
+        if (it > 0) {
+          wait_warp(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
+          tc::fence_after_sync();
+        }
+        if (moved_rows != 0 && it > 0) {
+          const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
+          const int cnt = __popc(moved_rows);
+          if (cnt <= FEW_MOVED) {
+            uint32_t m = moved_rows;
+            for (int q = 0; q < cnt; ++q) {
+              const int c = __ffs(m) - 1;
+              m &= m - 1;
+              const float a = s_a[c0 + c];
+              const uint32_t v0 = tc::tmem_ld1(lane_base + c);
+              const uint32_t v1 = tc::tmem_ld1(lane_base + 128 + c);
+              tc::tmem_wait_ld();
+              tc::tmem_st1(lane_base + c, __float_as_uint(__uint_as_float(v0) * a));
+              tc::tmem_st1(lane_base + 128 + c, __float_as_uint(__uint_as_float(v1) * a));
+            }
+          } else {
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+              uint32_t v[32];
+              tc::tmem_ld32(lane_base + 128u * t, v);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * s_a[c0 + c]);
+              tc::tmem_st32(lane_base + 128u * t, v);
+            }
+          }
+          tc::tmem_wait_st();
+        }
+        load_scores();   // again, for P (registers were spent on the max)
+        tc::tmem_wait_ld();
+        mask_scores();
+        // This key's P^T for the group's 32 rows, eight rows (one 16-byte
+        // granule of the key's swizzled 128-byte row) at a time.
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 m0 = *reinterpret_cast<const float4*>(s_m + c0 + 8 * q);
+          const float4 m1 = *reinterpret_cast<const float4*>(s_m + c0 + 8 * q + 4);
+          const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+          uint32_t pk[4];
+#pragma unroll
+          for (int e = 0; e < 8; e += 2) {
+            const int c = 8 * q + e;
+            const float p0 = ex2(x[c] - mm[e]), p1 = ex2(x[c + 1] - mm[e + 1]);
+            x[c] = p0;
+            x[c + 1] = p1;
+            __half2 hh = __floats2half2_rn(p0, p1);
+            pk[e >> 1] = *reinterpret_cast<uint32_t*>(&hh);
+          }
+          const uint32_t gran = static_cast<uint32_t>((((grp & 1) * 4 + q) ^ (j & 7)) << 4);
+          const uint4 v = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          if (p_local) *reinterpret_cast<uint4*>(smem + p_off + gran) = v;
+          else tc::st_async_v4(p_peer + gran, v, peer_mbar(MB_PX));
+        }
+        // The step's row sums over this warp's 32 keys (lane l: row c0 + l),
+        // folded into the running sum after its rescale.
+        transpose_reduce32<true>(x, lane);
+        lrun = lrun * s_a[c0 + lane] + x[0];
+        tc::fence_async_smem();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(mbar(MB_P));
+      }
+      // ---- the segment's end: row sums, then O^T out of TMEM
+      wait_warp(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
+      tc::fence_after_sync();
+      s_red[(c0 + lane) * 4 + quad] = lrun;
+      named_sync(1, SM_THREADS);
+      const size_t part0 = static_cast<size_t>(part_slot(cluster, s.first)) * ROWS;
+      if (owner) {
+        const float4 q4 = *reinterpret_cast<const float4*>(s_red + (c0 + lane) * 4);
+        const float ls = (q4.x + q4.y) + (q4.z + q4.w);
+        tc::st_async_b32(tc::peer_addr(sbase + OFF_XSUM + (c0 + lane) * 4, peer), __float_as_uint(ls), peer_mbar(MB_XS));
+        if (tid == 0) tc::mbar_arrive_expect(mbar(MB_XS), ROWS * 4);
+        wait_phase(mbar(MB_XS), static_cast<uint32_t>(k & 1), s_abort, p.err);
+        // Both CTAs add the two halves in the same order.
+        const float lo = rank == 0 ? ls : s_xsum[c0 + lane];
+        const float hi = rank == 0 ? s_xsum[c0 + lane] : ls;
+        const float l = lo + hi;
+        const int r = c0 + lane;
+        const float nan = __int_as_float(0x7fc00000);
+        // A row that is not served, or saw a value outside fp16: NaN.
+        const bool lost = l != l || s_row[r].x < 0;
+        s_l[r] = lost ? nan : l > 0.f ? 1.f / l : 0.f;
+        if (r < s.t.nrows && (r >> 6) == static_cast<int>(rank)) {
+          const float lse = lost ? nan : l > 0.f ? (mrow + log2f(l)) * kLn2 : -INFINITY;
+          if (s.whole) p.lse[s.t.q_row0 + r] = lse;
+          else p.part_lse[part0 + r] = lse;
+        }
+      }
+      named_sync(1, SM_THREADS);
+      // Thread = value dim: each warp store covers 32 consecutive dims of a row.
+#pragma unroll 1
+      for (int t = 0; t < 2; ++t) {
+        uint32_t v[32];
+        tc::tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * t + c0, v);
+        tc::tmem_wait_ld();
+        const int dim = t * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const int r = c0 + c;
+          if (r >= s.t.nrows) continue;   // warp-uniform
+          const float inv = s_l[r];
+          const float o = inv == 0.f ? 0.f : __uint_as_float(v[c]) * inv;
+          if (!s.whole) {
+            p.part_o[(part0 + r) * D_V + dim] = o;
+          } else {
+            const size_t e = static_cast<size_t>(s.t.q_row0 + r) * D_V + dim;
+            if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(o);
+            else reinterpret_cast<float*>(p.out)[e] = o;
+          }
+        }
+      }
+      tc::fence_before_sync();   // the next segment's O^T overwrites these columns after MB_P
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  tc::fence_after_sync();
+  if (*s_abort != 0) {
+    const SharedPos end = p.start[cluster + 1];
+    for (int tile = from.tile; next_segment(p, from, end, tile, s); tile = s.tile + 1)
+      write_nan_segment(p, s, cluster, rank, tid);
+  }
+  // Neither CTA leaves while the peer may still write into its shared
+  // memory, signal its barriers or (even CTA) read its operands.
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  if (warp == MMA_WARP) tc::tmem_dealloc_pair<TMEM_COLS>(tmem);
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+}  // namespace
+
+cudaError_t make_shared_maps(SharedMaps* maps, void* k16, long long k_plane, void* q16, long long q_plane) {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+  if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) return e != cudaSuccess ? e : cudaErrorNotSupported;
+  const EncodeTiled encode = reinterpret_cast<EncodeTiled>(fn);
+  // Nine planes of rows of 64 fp16 (128 bytes), swizzled on the way in.
+  auto planes = [&](CUtensorMap* map, void* base, long long rows, cuuint32_t box_rows, cuuint32_t box_planes) {
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 9};
+    const cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(rows) * 128};
+    const cuuint32_t box[3] = {64, box_rows, box_planes}, estrides[3] = {1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, base, dims, strides, box, estrides, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  if (planes(&maps->pair, k16, k_plane, BN, 2) != CUDA_SUCCESS || planes(&maps->chunk, k16, k_plane, BN, 1) != CUDA_SUCCESS ||
+      planes(&maps->q, q16, q_plane, HROWS, Q_PLANES) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  return cudaSuccess;
+}
+
+cudaError_t partial_shared_prepare() {
+  cudaError_t e = cudaFuncSetAttribute(partial_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(partial_shared_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                              cudaSharedmemCarveoutMaxShared);
+}
+
+cudaError_t launch_partial_shared(const SharedParams& p, const SharedMaps& maps, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.clusters);
+  cfg.blockDim = dim3(NTHREADS);
+  cfg.dynamicSmemBytes = SMEM_TOTAL;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, partial_shared_kernel, p, maps.pair, maps.chunk, maps.q);
+}
+
+}  // namespace mlav
