@@ -25,8 +25,8 @@
 // A tile that one cluster holds whole is normalised and stored directly;
 // otherwise the segment's partial goes to the workspace for shared_join_kernel.
 //
-// Roles (21 warps per CTA): warps 0-15 softmax, warp 16 MMA issue (even CTA)
-// or P^T hand-off (odd CTA), warps 17-19 the key ring, warp 20 the queries.
+// Roles (20 warps per CTA): warps 0-15 softmax, warp 16 MMA issue (even CTA)
+// or P^T hand-off (odd CTA), warps 17-19 the key ring (17 the queries too).
 // Every wait is bounded; after a timeout all of the cluster's rows are NaN.
 #include "shared.cuh"
 #include "kernels.h"
@@ -43,8 +43,7 @@ constexpr int HROWS = ROWS / 2;     // rows of the B operands a CTA holds
 constexpr int BN = SH_HALF;         // keys per CTA per step
 constexpr int SOFTMAX_WARPS = 16, MMA_WARP = 16, COPY_WARP = 17;
 constexpr int NCOPY = 3;            // copy warp k fills ring slot k
-constexpr int Q_WARP = COPY_WARP + NCOPY;
-constexpr int NWARPS = Q_WARP + 1;
+constexpr int NWARPS = COPY_WARP + NCOPY;
 constexpr int NTHREADS = NWARPS * 32;
 constexpr int SM_THREADS = SOFTMAX_WARPS * 32;
 constexpr int CHUNK = BN * 128;          // 16 KB: 128 keys x 64 dims fp16
@@ -55,13 +54,11 @@ constexpr int OFF_Q = 0;
 constexpr int OFF_P = OFF_Q + 9 * Q_CHUNK;            // P^T [key half][128 keys][64 rows] fp16
 constexpr int OFF_RING = OFF_P + 2 * CHUNK;
 constexpr int OFF_ROPE = OFF_RING + NSLOT * 2 * CHUNK;
-constexpr int OFF_RED = OFF_ROPE + CHUNK;             // float [128 rows][4 quads]
-constexpr int OFF_XMAX = OFF_RED + ROWS * 4 * 4;      // float [2][128] the peer's row max of the step
-constexpr int OFF_XSUM = OFF_XMAX + 2 * ROWS * 4;     // float [128] the peer's row sums
-constexpr int OFF_M = OFF_XSUM + ROWS * 4;            // float [128] running row max (0: none yet)
-constexpr int OFF_A = OFF_M + ROWS * 4;               // float [128] rescale factor of the step
-constexpr int OFF_L = OFF_A + ROWS * 4;               // float [128] 1 / row sum (0: none)
-constexpr int OFF_ROW = OFF_L + ROWS * 4;             // int2 [128] request of the row (-1: not served), ancestor mask
+constexpr int OFF_RED = OFF_ROPE + CHUNK;             // float [2][128 rows][4 quads] this CTA's row maxima of the step
+constexpr int OFF_XRED = OFF_RED + 2 * ROWS * 4 * 4;  // the same of the peer (st.async)
+constexpr int OFF_XSUM = OFF_XRED + 2 * ROWS * 4 * 4; // float [128] the peer's row sums
+constexpr int OFF_M = OFF_XSUM + ROWS * 4;            // float [2][128] running row max (0: none yet); 1 / row sum at the end
+constexpr int OFF_ROW = OFF_M + 2 * ROWS * 4;             // int2 [128] request of the row (-1: not served), ancestor mask
 constexpr int OFF_MBAR = OFF_ROW + ROWS * 8;
 constexpr int NMBAR = 20;
 constexpr int OFF_MISC = OFF_MBAR + NMBAR * 8;        // tmem base, P-complete word, absent-unit word, abort flag
@@ -82,7 +79,7 @@ constexpr int MB_PF = 12;      // even CTA: the odd CTA's P^T is complete (st.as
 constexpr int MB_OT = 13;      // O^T of a step done
 constexpr int MB_Q = 14;       // even CTA: both halves of a segment's queries landed
 constexpr int MB_QE = 15;      // the segment's last S^T is done: its queries can go
-constexpr int MB_X = 16;       // [2] the peer's row max of the step landed (st.async bytes)
+constexpr int MB_X = 16;       // [2] the peer's row maxima of the step landed (st.async bytes)
 constexpr int MB_XS = 18;      // the peer's row sums landed (st.async bytes)
 constexpr int MB_DONE = 19;    // after an abort: every MMA issued is done
 
@@ -91,6 +88,11 @@ constexpr uint32_t TM_S = 256;                  // S^T buffer u at 256 + 128u; O
 
 constexpr uint32_t IDESC_S = tc::idesc_f16(256, ROWS, 0, 0, 0);   // fp16, both K-major
 constexpr uint32_t IDESC_O = tc::idesc_f16(256, ROWS, 0, 1, 1);   // fp16, both MN-major
+
+// Shared-memory descriptors (tc::desc_sw128): the low word is the address and
+// the leading offset, the high word (stride 1024 bytes, 128-byte swizzle) is one.
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3FFF) | (lbo >> 4) << 16; }
 
 constexpr int FEW_MOVED = 4;
 constexpr uint32_t ABSENT_BYTES = 4;   // the odd CTA's signal for a unit it has no half block for
@@ -145,11 +147,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   const int grp = warp >> 2;            // softmax: rows 32*grp .. +32
 
   float* s_red = reinterpret_cast<float*>(smem + OFF_RED);
-  float* s_xmax = reinterpret_cast<float*>(smem + OFF_XMAX);
+  float* s_xred = reinterpret_cast<float*>(smem + OFF_XRED);
   float* s_xsum = reinterpret_cast<float*>(smem + OFF_XSUM);
   float* s_m = reinterpret_cast<float*>(smem + OFF_M);
-  float* s_a = reinterpret_cast<float*>(smem + OFF_A);
-  float* s_l = reinterpret_cast<float*>(smem + OFF_L);
   int2* s_row = reinterpret_cast<int2*>(smem + OFF_ROW);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + OFF_MISC + 12);
@@ -186,16 +186,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   }
   Segment s;
 
-  if (warp >= COPY_WARP && warp < Q_WARP) {
+  if (warp >= COPY_WARP) {
     // ========================= key chunk producers ==========================
     // As in partial_pair.cu: unit n goes to slot n % 3, one warp per slot; the
     // rope chunks go with slot 2; a half block the odd CTA does not have is
     // signalled by ABSENT_BYTES, so that no CTA's barriers run ahead.
     const int cw = warp - COPY_WARP;
     const uint32_t absent_word = tc::peer_addr(smem_u32(s_tmem + 2), 0);
-    int n = 0, g0 = 0;   // units so far, steps of the segments before
+    int n = 0, g0 = 0, k = 0;   // units and segments so far, steps of the segments before
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps) {
+    for (int tile = from.tile; next_segment(p, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
+      if (cw == 0) {
+        // The tile's queries, once the last S^T of the segment before is done
+        // (its O^T units, already under way, come after it).  Rows past the
+        // tile are the next tile's (or zeros past the batch): their columns
+        // of S^T and O^T are not stored.
+        if (k > 0) wait_warp(mbar(MB_QE), static_cast<uint32_t>((k - 1) & 1), s_abort, p.err);
+        if (*s_abort) break;
+        if (rank == 0) {
+          if (lane == 0) tc::mbar_arrive_expect(mbar(MB_Q), 2 * 9 * Q_CHUNK);
+          __syncwarp();
+        }
+#pragma unroll
+        for (int z = 0; z < 9; z += Q_PLANES)
+          tc::tma_load_3d_pair(sbase + OFF_Q + z * Q_CHUNK, &tm_q, 0, s.t.q_row0 + static_cast<int>(rank) * HROWS, z,
+                               even_mbar(MB_Q));
+      }
 #pragma unroll 1
       for (int f = 0; f < 2 * s.steps && !*s_abort; ++f) {
         bool is_s;
@@ -251,25 +267,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     // After an abort, copies already issued land within microseconds: wait
     // far longer than that before the pair's shared memory can be released.
     if (*s_abort) settle(1LL << 22);
-  } else if (warp == Q_WARP) {
-    // ============================== queries =================================
-    // Rows past the tile are the next tile's (or zeros past the batch): their
-    // columns of S^T and O^T are not stored.
-    int k = 0;
-#pragma unroll 1
-    for (int tile = from.tile; next_segment(p, from, to, tile, s); tile = s.tile + 1, ++k) {
-      if (k > 0) wait_warp(mbar(MB_QE), static_cast<uint32_t>((k - 1) & 1), s_abort, p.err);
-      if (*s_abort) break;
-      if (rank == 0) {
-        if (lane == 0) tc::mbar_arrive_expect(mbar(MB_Q), 2 * 9 * Q_CHUNK);
-        __syncwarp();
-      }
-#pragma unroll
-      for (int z = 0; z < 9; z += Q_PLANES)
-        tc::tma_load_3d_pair(sbase + OFF_Q + z * Q_CHUNK, &tm_q, 0, s.t.q_row0 + static_cast<int>(rank) * HROWS, z,
-                             even_mbar(MB_Q));
-    }
-    if (*s_abort) settle(1LL << 22);
   } else if (warp == MMA_WARP && rank == 1) {
     // =================== odd CTA: P^T complete -> even CTA ==================
     uint32_t* s_word = s_tmem + 1;
@@ -308,27 +305,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const int slot = n % NSLOT;
             wait_warp(mbar(MB_FULL + slot), static_cast<uint32_t>((n / NSLOT) & 1), s_abort, p.err);
             tc::fence_after_sync();
-            const uint32_t base = sbase + OFF_RING + slot * 2 * CHUNK;
+            if (tc::elect_one()) {
+              const uint32_t a = desc_lo(sbase + OFF_RING + slot * 2 * CHUNK, 16);
+              const uint32_t bq = desc_lo(sbase + OFF_Q + u * 2 * Q_CHUNK, 16);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              const int c = 8 * u + kk;   // 16-dim step of the 576-dim contraction
-              const uint64_t a = tc::desc_sw128(base + (kk >> 2) * CHUNK + (kk & 3) * 32, 16, 1024);
-              const uint64_t bq = tc::desc_sw128(sbase + OFF_Q + (c >> 2) * Q_CHUNK + (c & 3) * 32, 16, 1024);
-              tc::mma_pair(d, a, bq, IDESC_S, c > 0);
+              for (int kk = 0; kk < 8; ++kk)   // 16-dim steps of the chunk pair
+                tc::mma_pair_one(d, a + (((kk >> 2) * CHUNK + (kk & 3) * 32) >> 4),
+                                 bq + (((kk >> 2) * Q_CHUNK + (kk & 3) * 32) >> 4), DESC_HI, IDESC_S, (u > 0 || kk > 0) ? 1u : 0u);
+              tc::commit_pair_one(mbar(MB_EMPTY + slot));
             }
-            tc::commit_pair(mbar(MB_EMPTY + slot));
+            __syncwarp();
           }
           wait_warp(mbar(MB_RFULL), static_cast<uint32_t>(g & 1), s_abort, p.err);
           tc::fence_after_sync();
+          if (tc::elect_one()) {
+            const uint32_t a = desc_lo(sbase + OFF_ROPE, 16), bq = desc_lo(sbase + OFF_Q + 8 * Q_CHUNK, 16);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t a = tc::desc_sw128(sbase + OFF_ROPE + kk * 32, 16, 1024);
-            const uint64_t bq = tc::desc_sw128(sbase + OFF_Q + 8 * Q_CHUNK + kk * 32, 16, 1024);
-            tc::mma_pair(d, a, bq, IDESC_S, 1);
+            for (int kk = 0; kk < 4; ++kk) tc::mma_pair_one(d, a + 2 * kk, bq + 2 * kk, DESC_HI, IDESC_S, 1);
+            tc::commit_pair_one(mbar(MB_REMPTY));
+            tc::commit_pair_one(mbar(MB_S + (g & 1)));
+            if (i == s.steps - 1) tc::commit_pair_one(mbar(MB_QE));
           }
-          tc::commit_pair(mbar(MB_REMPTY));
-          tc::commit_pair(mbar(MB_S + (g & 1)));
-          if (i == s.steps - 1) tc::commit_pair(mbar(MB_QE));
+          __syncwarp();
         } else {
           // P^T of the step: this CTA's softmax warps, the odd CTA's st.async
           // bytes, and the odd CTA's word that its own half is complete.
@@ -348,18 +346,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const int slot = n % NSLOT;
             wait_warp(mbar(MB_FULL + slot), static_cast<uint32_t>((n / NSLOT) & 1), s_abort, p.err);
             tc::fence_after_sync();
-            if (2 * (s.sa + i) + h < s.t.halves) {
-              const uint32_t base = sbase + OFF_RING + slot * 2 * CHUNK;
+            if (tc::elect_one()) {
+              if (2 * (s.sa + i) + h < s.t.halves) {
+                const uint32_t a = desc_lo(sbase + OFF_RING + slot * 2 * CHUNK, CHUNK);
+                const uint32_t bp = desc_lo(sbase + OFF_P + h * CHUNK, CHUNK);
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {   // 16-key steps of the key half
-                const uint64_t a = tc::desc_sw128(base + kk * 2048, CHUNK, 1024);
-                const uint64_t bp = tc::desc_sw128(sbase + OFF_P + h * CHUNK + kk * 2048, CHUNK, 1024);
-                tc::mma_pair(tmem + 128u * static_cast<uint32_t>(t), a, bp, IDESC_O, (i > 0 || h > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < 8; ++kk)   // 16-key steps of the key half
+                  tc::mma_pair_one(tmem + 128u * static_cast<uint32_t>(t), a + kk * (2048 >> 4), bp + kk * (2048 >> 4), DESC_HI,
+                                   IDESC_O, (i > 0 || h > 0 || kk > 0) ? 1u : 0u);
               }
+              tc::commit_pair_one(mbar(MB_EMPTY + slot));
+              if (u == 3) tc::commit_pair_one(mbar(MB_OT));
             }
-            tc::commit_pair(mbar(MB_EMPTY + slot));
+            __syncwarp();
           }
-          tc::commit_pair(mbar(MB_OT));
         }
       }
     }
@@ -370,43 +370,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     }
   } else {
     // ============================= softmax =================================
-    // These warps never leave the loops early (they meet at named barriers);
+    // The four warps of a row group (32 rows; a warp has 32 keys of each) meet
+    // at the group's named barrier; they never leave the loops early, and
     // after an abort their waits return at once.
     const int j = quad * 32 + lane;     // key of this thread = TMEM lane
     const int c0 = grp * 32;            // pair rows c0 .. c0+31
     const float scale2 = p.scale_log2;
-    const bool owner = quad == 0;       // lane l owns row c0 + l's running max
+    auto group_sync = [&]() { named_sync(1 + grp, 128); };
     // This key's P^T row (key half = rank) in the CTA that holds the group's
     // rows: a local store, or st.async into the peer with its MB_PX.
     const bool p_local = (grp >> 1) == static_cast<int>(rank);
     const uint32_t p_off = OFF_P + rank * CHUNK + j * 128;
     const uint32_t p_peer = tc::peer_addr(sbase + p_off, peer);
-    const uint32_t xmax_peer = tc::peer_addr(sbase + OFF_XMAX, peer);
+    const uint32_t red_off = ((c0 + lane) * 4 + quad) * 4;   // this warp's maximum of row c0 + lane
+    const uint32_t xred_peer = tc::peer_addr(sbase + OFF_XRED + red_off, peer);
     int g = 0, k = 0;   // steps and segments so far
 #pragma unroll 1
     for (int tile = from.tile; next_segment(p, from, to, tile, s); tile = s.tile + 1, ++k) {
+      // This CTA's half block of each step: h0, h0 + 2, ..  Its keys' meta
+      // words start at meta0 + 128 hb, those of the own range meta_gap behind.
+      const int h0 = 2 * s.sa + static_cast<int>(rank), np = prefix_halves(s.t);
+      const int prefix_len = s.t.prefix_len, own_len = s.t.own_len + np * BN;
+      const int* meta0 = p.meta + s.t.prefix_base + j;
+      const int meta_gap = s.t.own_base - np * BN - s.t.prefix_base;
+      const int nsteps = s.steps;
       auto load_meta = [&](int step) {
-        int count;
-        const int hb = 2 * (s.sa + step) + static_cast<int>(rank);
-        if (step >= s.steps || hb >= s.t.halves) return META_MASKED;
-        const int base = half_base(s.t, hb, count);
-        return j < count ? __ldg(p.meta + base + j) : META_MASKED;
+        const int key = (h0 + 2 * step) * BN;
+        const bool shared = key < np * BN;
+        if (step >= nsteps || key + j >= (shared ? prefix_len : own_len)) return META_MASKED;
+        return __ldg(meta0 + key + (shared ? 0 : meta_gap));
       };
       int meta = load_meta(0);
-      named_sync(1, SM_THREADS);   // the previous segment's rows are read
-      if (tid < ROWS) {
+      group_sync();   // the previous segment's rows are read
+      if (quad == 0) {
         int2 row = make_int2(-1, 0);
-        if (tid < s.t.nrows) {
-          const int q = s.t.q_row0 + tid, b = q / p.R;
+        if (c0 + lane < s.t.nrows) {
+          const int q = s.t.q_row0 + c0 + lane, b = q / p.R;
           if (__ldg(p.own + b) > 0) row = make_int2(b, static_cast<int>(__ldg(p.anc + b * p.T + (q - b * p.R) / p.H)));
         }
-        s_row[tid] = row;
+        s_row[c0 + lane] = row;
       }
-      named_sync(1, SM_THREADS);
-      float mrow = -INFINITY;
-      float lrun = 0.f;                   // row c0 + lane's sum over this warp's keys so far
+      group_sync();
+      float mrow = -INFINITY;             // row c0 + lane's running max, the same in the group's warps of both CTAs
+      float lrun = 0.f;                   // its sum over this warp's keys so far
 #pragma unroll 1
-      for (int it = 0; it < s.steps; ++it, ++g) {
+      for (int it = 0; it < nsteps; ++it, ++g) {
         // The group's rows that see this key (bit c: row c0 + c), decided
         // while S^T is computed.
         uint32_t vis = 0;
@@ -431,8 +439,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         tc::fence_after_sync();
         const uint32_t s_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + TM_S + 128u * sb + c0;
         float x[32];
-        auto load_scores = [&]() { tc::tmem_ld32f(s_addr, x); };
-        auto mask_scores = [&]() {
+        auto load_scores = [&]() {
+          tc::tmem_ld32f(s_addr, x);
+          tc::tmem_wait_ld();
           if (vis == 0xffffffffu) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) x[c] *= visible;
@@ -442,116 +451,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
         };
         load_scores();
-        tc::tmem_wait_ld();
-        mask_scores();
         transpose_reduce32<false>(x, lane);
-        s_red[(c0 + lane) * 4 + quad] = x[0];
-        named_sync(1, SM_THREADS);
-        if (owner) {
-          const float4 q4 = *reinterpret_cast<const float4*>(s_red + (c0 + lane) * 4);
-          float bm = fmaxf(fmaxf(q4.x, q4.y), fmaxf(q4.z, q4.w));
-          tc::st_async_b32(xmax_peer + (sb * ROWS + c0 + lane) * 4, __float_as_uint(bm), peer_mbar(MB_X + sb));
-          if (tid == 0) tc::mbar_arrive_expect(mbar(MB_X + sb), ROWS * 4);
-          wait_phase(mbar(MB_X + sb), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
-          bm = fmaxf(bm, s_xmax[sb * ROWS + c0 + lane]);
-          float alpha = 1.f;
+        // Every warp gives its 32 maxima to the group here and in the peer,
+        // and takes the maximum of the eight itself.
+        s_red[sb * ROWS * 4 + (c0 + lane) * 4 + quad] = x[0];
+        tc::st_async_b32(xred_peer + sb * ROWS * 16, __float_as_uint(x[0]), peer_mbar(MB_X + sb));
+        if (tid == 0) tc::mbar_arrive_expect(mbar(MB_X + sb), ROWS * 16);
+        load_scores();   // again, for P, while the peer's maxima arrive
+        group_sync();
+        wait_warp(mbar(MB_X + sb), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
+        float alpha = 1.f;
+        {
+          const float4 o4 = *reinterpret_cast<const float4*>(s_red + sb * ROWS * 4 + (c0 + lane) * 4);
+          const float4 p4 = *reinterpret_cast<const float4*>(s_xred + sb * ROWS * 4 + (c0 + lane) * 4);
+          const float bm = fmaxf(fmaxf(fmaxf(o4.x, o4.y), fmaxf(o4.z, o4.w)), fmaxf(fmaxf(p4.x, p4.y), fmaxf(p4.z, p4.w)));
           if (bm > mrow) {
             if (mrow != -INFINITY) alpha = ex2(mrow - bm);
             mrow = bm;
           }
-          s_m[c0 + lane] = mrow == -INFINITY ? 0.f : mrow;   // a fully masked row: p = ex2(-inf) = 0
-          s_a[c0 + lane] = alpha;
+          // A fully masked row: p = ex2(-inf - 0) = 0.  (The group's warps
+          // write the same values.)
+          s_m[sb * ROWS + c0 + lane] = mrow == -INFINITY ? 0.f : mrow;
         }
-        named_sync(1, SM_THREADS);
-        // Rows whose max moved (the same mask in every lane).
-        uint32_t moved_rows = 0;
+        __syncwarp();
+        // P^T for this key and the group's 32 rows, in fp16: weight 1 is
+        // exact, the others lose 2^-12 at most.
+        uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < 32; c += 4) {
-          const float4 a4 = *reinterpret_cast<const float4*>(s_a + c0 + c);
-          moved_rows |= (a4.x != 1.f ? 1u : 0u) << c | (a4.y != 1.f ? 1u : 0u) << (c + 1) |
-                        (a4.z != 1.f ? 1u : 0u) << (c + 2) | (a4.w != 1.f ? 1u : 0u) << (c + 3);
+        for (int q = 0; q < 8; ++q) {
+          const float4 m4 = *reinterpret_cast<const float4*>(s_m + sb * ROWS + c0 + 4 * q);
+          x[4 * q] = ex2(x[4 * q] - m4.x);
+          x[4 * q + 1] = ex2(x[4 * q + 1] - m4.y);
+          x[4 * q + 2] = ex2(x[4 * q + 2] - m4.z);
+          x[4 * q + 3] = ex2(x[4 * q + 3] - m4.w);
+          const __half2 lo = __floats2half2_rn(x[4 * q], x[4 * q + 1]), hi = __floats2half2_rn(x[4 * q + 2], x[4 * q + 3]);
+          pk[2 * q] = *reinterpret_cast<const uint32_t*>(&lo);
+          pk[2 * q + 1] = *reinterpret_cast<const uint32_t*>(&hi);
         }
+        // The step's row sums over this warp's 32 keys (lane l: row c0 + l).
+        transpose_reduce32<true>(x, lane);
+        lrun = lrun * alpha + x[0];
         // O^T of the step before done: the P^T buffers (here and in the peer)
         // are free and O^T can be rescaled.  (A segment's first step: the
         // readout waited for it.)
         if (it > 0) {
           wait_warp(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
           tc::fence_after_sync();
-        }
-        if (moved_rows != 0 && it > 0) {
-          const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
-          const int cnt = __popc(moved_rows);
-          if (cnt <= FEW_MOVED) {
-            uint32_t m = moved_rows;
-            for (int q = 0; q < cnt; ++q) {
-              const int c = __ffs(m) - 1;
-              m &= m - 1;
-              const float a = s_a[c0 + c];
-              const uint32_t v0 = tc::tmem_ld1(lane_base + c);
-              const uint32_t v1 = tc::tmem_ld1(lane_base + 128 + c);
-              tc::tmem_wait_ld();
-              tc::tmem_st1(lane_base + c, __float_as_uint(__uint_as_float(v0) * a));
-              tc::tmem_st1(lane_base + 128 + c, __float_as_uint(__uint_as_float(v1) * a));
-            }
-          } else {
+          const uint32_t moved_rows = __ballot_sync(0xffffffffu, alpha != 1.f);
+          if (moved_rows != 0) {
+            const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
+            const int cnt = __popc(moved_rows);
+            if (cnt <= FEW_MOVED) {
+              uint32_t m = moved_rows;
+              for (int q = 0; q < cnt; ++q) {
+                const int c = __ffs(m) - 1;
+                m &= m - 1;
+                const float a = __shfl_sync(0xffffffffu, alpha, c);
+                const uint32_t v0 = tc::tmem_ld1(lane_base + c);
+                const uint32_t v1 = tc::tmem_ld1(lane_base + 128 + c);
+                tc::tmem_wait_ld();
+                tc::tmem_st1(lane_base + c, __float_as_uint(__uint_as_float(v0) * a));
+                tc::tmem_st1(lane_base + 128 + c, __float_as_uint(__uint_as_float(v1) * a));
+              }
+            } else {
 #pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-              uint32_t v[32];
-              tc::tmem_ld32(lane_base + 128u * t, v);
-              tc::tmem_wait_ld();
+              for (int t = 0; t < 2; ++t) {
+                uint32_t v[32];
+                tc::tmem_ld32(lane_base + 128u * t, v);
+                tc::tmem_wait_ld();
 #pragma unroll
-              for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) * s_a[c0 + c]);
-              tc::tmem_st32(lane_base + 128u * t, v);
+                for (int c = 0; c < 32; ++c)
+                  v[c] = __float_as_uint(__uint_as_float(v[c]) * __shfl_sync(0xffffffffu, alpha, c));
+                tc::tmem_st32(lane_base + 128u * t, v);
+              }
             }
+            tc::tmem_wait_st();
           }
-          tc::tmem_wait_st();
         }
-        load_scores();   // again, for P (registers were spent on the max)
-        tc::tmem_wait_ld();
-        mask_scores();
-        // This key's P^T for the group's 32 rows, eight rows (one 16-byte
-        // granule of the key's swizzled 128-byte row) at a time.
+        // Eight rows are one 16-byte granule of the key's swizzled row.
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const float4 m0 = *reinterpret_cast<const float4*>(s_m + c0 + 8 * q);
-          const float4 m1 = *reinterpret_cast<const float4*>(s_m + c0 + 8 * q + 4);
-          const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-          uint32_t pk[4];
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const int c = 8 * q + e;
-            const float p0 = ex2(x[c] - mm[e]), p1 = ex2(x[c + 1] - mm[e + 1]);
-            x[c] = p0;
-            x[c + 1] = p1;
-            __half2 hh = __floats2half2_rn(p0, p1);
-            pk[e >> 1] = *reinterpret_cast<uint32_t*>(&hh);
-          }
           const uint32_t gran = static_cast<uint32_t>((((grp & 1) * 4 + q) ^ (j & 7)) << 4);
-          const uint4 v = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          const uint4 v = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
           if (p_local) *reinterpret_cast<uint4*>(smem + p_off + gran) = v;
           else tc::st_async_v4(p_peer + gran, v, peer_mbar(MB_PX));
         }
-        // The step's row sums over this warp's 32 keys (lane l: row c0 + l),
-        // folded into the running sum after its rescale.
-        transpose_reduce32<true>(x, lane);
-        lrun = lrun * s_a[c0 + lane] + x[0];
-        tc::fence_async_smem();
+        if (p_local) tc::fence_async_smem();   // (the peer's MMA warp fences the st.async bytes)
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(mbar(MB_P));
       }
-      // ---- the segment's end: row sums, then O^T out of TMEM
-      wait_warp(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
-      tc::fence_after_sync();
-      s_red[(c0 + lane) * 4 + quad] = lrun;
-      named_sync(1, SM_THREADS);
+      // ---- the segment's end: row sums over the group's warps, then the peer's
+      const int eb = (g & 1) * ROWS;   // the halves of s_red and s_m that the last step did not use
+      s_red[(eb + c0 + lane) * 4 + quad] = lrun;
+      group_sync();
+      float* s_l = s_m + eb;
       const size_t part0 = static_cast<size_t>(part_slot(cluster, s.first)) * ROWS;
-      if (owner) {
-        const float4 q4 = *reinterpret_cast<const float4*>(s_red + (c0 + lane) * 4);
+      if (quad == 0) {
+        const float4 q4 = *reinterpret_cast<const float4*>(s_red + (eb + c0 + lane) * 4);
         const float ls = (q4.x + q4.y) + (q4.z + q4.w);
         tc::st_async_b32(tc::peer_addr(sbase + OFF_XSUM + (c0 + lane) * 4, peer), __float_as_uint(ls), peer_mbar(MB_XS));
         if (tid == 0) tc::mbar_arrive_expect(mbar(MB_XS), ROWS * 4);
         wait_phase(mbar(MB_XS), static_cast<uint32_t>(k & 1), s_abort, p.err);
+        __syncwarp();
         // Both CTAs add the two halves in the same order.
         const float lo = rank == 0 ? ls : s_xsum[c0 + lane];
         const float hi = rank == 0 ? s_xsum[c0 + lane] : ls;
@@ -567,27 +569,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           else p.part_lse[part0 + r] = lse;
         }
       }
-      named_sync(1, SM_THREADS);
-      // Thread = value dim: each warp store covers 32 consecutive dims of a row.
+      group_sync();
+      // ---- O^T out of TMEM; thread = value dim, each warp store 32
+      // consecutive dims of a row.
+      wait_warp(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
+      tc::fence_after_sync();
+      const int rows = s.t.nrows - c0;
+      const size_t out0 = (s.whole ? static_cast<size_t>(s.t.q_row0) : part0) + c0;
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        uint32_t v[32];
-        tc::tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * t + c0, v);
+        float v[32];
+        tc::tmem_ld32f(tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * t + c0, v);
         tc::tmem_wait_ld();
-        const int dim = t * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const int r = c0 + c;
-          if (r >= s.t.nrows) continue;   // warp-uniform
-          const float inv = s_l[r];
-          const float o = inv == 0.f ? 0.f : __uint_as_float(v[c]) * inv;
-          if (!s.whole) {
-            p.part_o[(part0 + r) * D_V + dim] = o;
-          } else {
-            const size_t e = static_cast<size_t>(s.t.q_row0 + r) * D_V + dim;
-            if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16_rn(o);
-            else reinterpret_cast<float*>(p.out)[e] = o;
-          }
+        for (int q = 0; q < 8; ++q) {
+          const float4 i4 = *reinterpret_cast<const float4*>(s_l + c0 + 4 * q);
+          v[4 * q] = i4.x == 0.f ? 0.f : v[4 * q] * i4.x;
+          v[4 * q + 1] = i4.y == 0.f ? 0.f : v[4 * q + 1] * i4.y;
+          v[4 * q + 2] = i4.z == 0.f ? 0.f : v[4 * q + 2] * i4.z;
+          v[4 * q + 3] = i4.w == 0.f ? 0.f : v[4 * q + 3] * i4.w;
+        }
+        const size_t at = out0 * D_V + t * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
+        if (s.whole && p.out_bf16) {
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c < rows) o[c * D_V] = __float2bfloat16_rn(v[c]);
+        } else {
+          float* o = (s.whole ? reinterpret_cast<float*>(p.out) : p.part_o) + at;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c < rows) o[c * D_V] = v[c];
         }
       }
       tc::fence_before_sync();   // the next segment's O^T overwrites these columns after MB_P

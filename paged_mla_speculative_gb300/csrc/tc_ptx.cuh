@@ -186,6 +186,35 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
+// True in one lane of a converged warp, the same lane every time.  A run of
+// MMAs and their commit inside one such branch issue back to back.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred e;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "selp.u32 %0, 1, 0, e;\n}\n"
+      : "=r"(ok));
+  return ok != 0;
+}
+// For the elected lane: the same MMA and commit, issued by the calling thread.
+// Descriptors by their low words (address >> 4 and leading offset); `hi` is
+// the high word they share.
+__device__ __forceinline__ void mma_pair_one(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 a, b;\n"
+      "mov.b64 a, {%1, %3};\nmov.b64 b, {%2, %3};\n"
+      "setp.ne.b32 p, %5, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void commit_pair_one(uint32_t mbar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(mbar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
 // Arrive once on the mbarrier at this offset in both CTAs of the pair when
 // every MMA issued so far is done.
 __device__ __forceinline__ void commit_pair(uint32_t mbar) {
