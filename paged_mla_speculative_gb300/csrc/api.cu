@@ -113,13 +113,12 @@ size_t shared_layout(const mla_verify_plan* pl, mlav::SharedParams* p) {
   const size_t B = static_cast<size_t>(pl->max_batch), tiles = static_cast<size_t>(pl->max_tiles);
   p->base = take(2 * B + 1);
   p->source = take(B);
-  p->group_of = take(B);
   p->own = take(B);
   p->anc = reinterpret_cast<uint32_t*>(take(B * pl->T));
-  p->tile0 = take(B + 1);
+  p->tile0 = take(B);
   p->cost = take(tiles + 1);
   p->tiles = reinterpret_cast<mlav::SharedTile*>(take(tiles * sizeof(mlav::SharedTile) / 4));
-  p->start = reinterpret_cast<mlav::SharedPos*>(take(2 * (static_cast<size_t>(shared_clusters(pl)) + 1)));
+  p->share = reinterpret_cast<mlav::SharedShare*>(take(static_cast<size_t>(shared_clusters(pl)) * sizeof(mlav::SharedShare) / 4));
   p->totals = take(2);
   return at;
 }
@@ -942,7 +941,7 @@ int mla_verify_attn_shared(mla_verify_plan* pl, int batch, const void* q, const 
   p.part_o = pl->ws_o;
   p.part_lse = pl->ws_lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (mlav::launch_shared_plan(p, s) != cudaSuccess || mlav::launch_shared_pack(p, pl->num_sms, s) != cudaSuccess ||
+  if (mlav::launch_shared_prepare(p, pl->num_sms, s) != cudaSuccess ||
       mlav::launch_partial_shared(p, pl->sh_maps, s) != cudaSuccess || mlav::launch_shared_join(p, s) != cudaSuccess ||
       note_done(pl, s) != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;

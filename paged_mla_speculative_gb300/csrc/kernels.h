@@ -98,16 +98,15 @@ struct CompactArgs {
 };
 cudaError_t launch_compact_kv(const CompactArgs& a, cudaStream_t stream);
 
-// Attention of groups of requests that share their first rows: plan (and the
-// queries' widening), key pack, persistent attention, merge -- in this order,
-// each of the last three overlapping the tail of the one before.
+// Attention of groups of requests that share their first rows: the call's
+// layout with its packed keys and queries, the persistent attention, the merge
+// -- in this order, each of the last two overlapping the tail of the one before.
 struct SharedMaps {
   CUtensorMap pair, chunk, q;   // of the packed keys (two planes, one plane) and queries
 };
 cudaError_t make_shared_maps(SharedMaps* maps, void* k16, long long k_plane, void* q16, long long q_plane);
 cudaError_t partial_shared_prepare();
-cudaError_t launch_shared_plan(const SharedParams& p, cudaStream_t stream);
-cudaError_t launch_shared_pack(const SharedParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_shared_prepare(const SharedParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_partial_shared(const SharedParams& p, const SharedMaps& maps, cudaStream_t stream);
 cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream);
 

@@ -45,7 +45,6 @@ constexpr int SOFTMAX_WARPS = 16, MMA_WARP = 16, COPY_WARP = 17;
 constexpr int NCOPY = 3;            // copy warp k fills ring slot k
 constexpr int NWARPS = COPY_WARP + NCOPY;
 constexpr int NTHREADS = NWARPS * 32;
-constexpr int SM_THREADS = SOFTMAX_WARPS * 32;
 constexpr int CHUNK = BN * 128;          // 16 KB: 128 keys x 64 dims fp16
 constexpr int Q_CHUNK = HROWS * 128;     // 8 KB: 64 rows x 64 dims
 constexpr int Q_PLANES = 3;              // planes per query load
@@ -102,18 +101,24 @@ struct Segment {
   int tile, sa, steps;   // steps sa .. sa + steps - 1 of the tile
   bool first, whole;     // the cluster's first segment; the tile's only one
 };
+// (Plain loads of what the kernel before wrote, here and below: a read-only
+// load with an address known early may be moved above griddepcontrol.wait.)
+__device__ __forceinline__ SharedTile load_tile(const SharedTile* rec) {
+  const int4* q = reinterpret_cast<const int4*>(rec);
+  const int4 a = q[0], b = q[1], c = q[2];
+  return SharedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, 0};
+}
 // The cluster's next segment at or after tile `tile`; false when there is none.
-__device__ __forceinline__ bool next_segment(const SharedParams& p, const SharedPos& from, const SharedPos& to, int tile,
-                                             Segment& s) {
+__device__ __forceinline__ bool next_segment(const SharedParams& p, const SharedShare* share, const SharedPos& from,
+                                             const SharedPos& to, int tile, Segment& s) {
   for (; tile < to.tile || (tile == to.tile && to.step > 0); ++tile) {
-    const int4* rec = reinterpret_cast<const int4*>(p.tiles + tile);
-    const int4 a = __ldg(rec), b = __ldg(rec + 1), c = __ldg(rec + 2);
-    s.t = SharedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, 0};
-    s.tile = tile;
-    s.sa = tile == from.tile ? from.step : 0;
-    s.steps = (tile == to.tile ? to.step : s.t.steps) - s.sa;
     s.first = tile == from.tile;
-    s.whole = s.t.nseg == 1;
+    s.t = load_tile(s.first ? &share->first : p.tiles + tile);
+    s.tile = tile;
+    s.sa = s.first ? from.step : 0;
+    const bool ends = tile == to.tile;
+    s.steps = (ends ? to.step : s.t.steps) - s.sa;
+    s.whole = s.sa == 0 && !ends;
     if (s.steps > 0) return true;
   }
   return false;
@@ -173,9 +178,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   const uint32_t peer_mbar0 = tc::peer_addr(mbar0, peer);
   auto even_mbar = [&](int i) { return even_mbar0 + 8u * static_cast<uint32_t>(i); };
   auto peer_mbar = [&](int i) { return peer_mbar0 + 8u * static_cast<uint32_t>(i); };
-  // Everything read from here on was written by the planning and packing kernels.
+  // Everything read from here on was written by the kernel before.
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  SharedPos from = p.start[cluster], to = p.start[cluster + 1];
+  const SharedShare* share = p.share + cluster;
+  const int4 range = *reinterpret_cast<const int4*>(share);
+  const SharedPos from{range.x, range.y};
+  SharedPos to{range.z, range.w};
   if (sbase & 1023) {   // the swizzled tiles need it (uniform over the pair)
     if (tid == 0) {
       atomicOr(p.err, ERR_INTERNAL);
@@ -195,7 +203,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const uint32_t absent_word = tc::peer_addr(smem_u32(s_tmem + 2), 0);
     int n = 0, g0 = 0, k = 0;   // units and segments so far, steps of the segments before
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
+    for (int tile = from.tile; next_segment(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
       if (cw == 0) {
         // The tile's queries, once the last S^T of the segment before is done
         // (its O^T units, already under way, come after it).  Rows past the
@@ -273,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const uint32_t even_word = tc::peer_addr(smem_u32(s_word), 0);
     int g = 0;
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, from, to, tile, s); tile = s.tile + 1) {
+    for (int tile = from.tile; next_segment(p, share, from, to, tile, s); tile = s.tile + 1) {
 #pragma unroll 1
       for (int i = 0; i < s.steps; ++i, ++g) {
         if (lane == 0) tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
@@ -289,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     // ======================= MMA issuer (even CTA) ==========================
     int n = 0, g0 = 0, k = 0;
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
+    for (int tile = from.tile; next_segment(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
       wait_warp(mbar(MB_Q), static_cast<uint32_t>(k & 1), s_abort, p.err);
       tc::fence_after_sync();
 #pragma unroll 1
@@ -386,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const uint32_t xred_peer = tc::peer_addr(sbase + OFF_XRED + red_off, peer);
     int g = 0, k = 0;   // steps and segments so far
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, from, to, tile, s); tile = s.tile + 1, ++k) {
+    for (int tile = from.tile; next_segment(p, share, from, to, tile, s); tile = s.tile + 1, ++k) {
       // This CTA's half block of each step: h0, h0 + 2, ..  Its keys' meta
       // words start at meta0 + 128 hb, those of the own range meta_gap behind.
       const int h0 = 2 * s.sa + static_cast<int>(rank), np = prefix_halves(s.t);
@@ -398,7 +406,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const int key = (h0 + 2 * step) * BN;
         const bool shared = key < np * BN;
         if (step >= nsteps || key + j >= (shared ? prefix_len : own_len)) return META_MASKED;
-        return __ldg(meta0 + key + (shared ? 0 : meta_gap));
+        return meta0[key + (shared ? 0 : meta_gap)];
       };
       int meta = load_meta(0);
       group_sync();   // the previous segment's rows are read
@@ -406,7 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         int2 row = make_int2(-1, 0);
         if (c0 + lane < s.t.nrows) {
           const int q = s.t.q_row0 + c0 + lane, b = q / p.R;
-          if (__ldg(p.own + b) > 0) row = make_int2(b, static_cast<int>(__ldg(p.anc + b * p.T + (q - b * p.R) / p.H)));
+          if (p.own[b] > 0) row = make_int2(b, static_cast<int>(p.anc[b * p.T + (q - b * p.R) / p.H]));
         }
         s_row[c0 + lane] = row;
       }
@@ -611,8 +619,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   tc::fence_after_sync();
   if (*s_abort != 0) {
-    const SharedPos end = p.start[cluster + 1];
-    for (int tile = from.tile; next_segment(p, from, end, tile, s); tile = s.tile + 1)
+    const SharedPos end{range.z, range.w};
+    for (int tile = from.tile; next_segment(p, share, from, end, tile, s); tile = s.tile + 1)
       write_nan_segment(p, s, cluster, rank, tid);
   }
   // Neither CTA leaves while the peer may still write into its shared

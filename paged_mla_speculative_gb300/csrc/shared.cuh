@@ -19,6 +19,8 @@ constexpr int SH_TAIL = 128;       // zeroed keys behind the packed space: a hal
 // A tile's cost in steps is its steps plus this: what a segment costs beside
 // them (queries in, pipeline fill, last O^T, readout: ~10 us against ~5 us a step).
 constexpr int SH_SEGMENT_COST = 2;
+// What the merge of cut tiles costs, in steps (~7 us).
+constexpr int SH_JOIN_COST = 2;
 
 // Meta word of a packed key.
 constexpr int META_MASKED = -1;            // no row sees it
@@ -56,6 +58,13 @@ __device__ __forceinline__ int half_base(const SharedTile& t, int hb, int& count
 struct SharedPos {
   int tile, step;
 };
+// A cluster's share of the work, and its first tile (so that its kernel need
+// not wait for one load to make the next).
+struct SharedShare {
+  SharedPos from, to;
+  SharedTile first;
+};
+static_assert(sizeof(SharedShare) == 64, "four 16-byte loads");
 
 struct SharedParams {
   const uint16_t* q;            // bf16 [B * R, 576]
@@ -85,13 +94,12 @@ struct SharedParams {
   int* meta;                    // [k_plane]
   int* base;                    // [2 B + 1]: packed base of request b's shared part (its group's first request) and own part
   int* source;                  // [max(B, G)]: per group, the request whose table gives the shared rows
-  int* group_of;                // [B]
   int* own;                     // [B]: its own rows (>= T), 0 when it cannot be served
   uint32_t* anc;                // [B, T] ancestor masks
-  int* tile0;                   // [G + 1] first tile of each group
+  int* tile0;                   // [G] first tile of each group
   int* cost;                    // [max_tiles + 1] prefix sum of the tiles' costs
   SharedTile* tiles;            // [max_tiles]
-  SharedPos* start;             // [clusters + 1]
+  SharedShare* share;           // [clusters]
   int* totals;                  // [0] packed keys, [1] tiles
   float* part_o;                // [2 * clusters][128][512]
   float* part_lse;              // [2 * clusters][128]

@@ -1,17 +1,22 @@
-// Planning and packing of the shared-prefix verify attention.
+// Preparation of the shared-prefix verify attention, and the merge after it.
 //
-// shared_plan_kernel: CTA 0 lays out the call on the device (lengths are
-// device data): which requests can be served, each group's shared range and
-// each request's own range in the packed key space, the query-row tiles, and
-// the division of all tiles' steps over the attention kernel's clusters, even
-// to a step, so that one long prompt or many short ones fill the GPU alike.
-// The other CTAs widen the queries meanwhile (bf16 to fp16, planes of 64 dims).
-//
-// shared_pack_kernel: gathers each distinct row once -- shared rows once per
-// group, not once per request -- and widens it into fp16 planes of 64 dims,
-// which the attention kernel reads by TMA (any 128 consecutive keys are one
-// box).  Values that have no fp16 counterpart are packed as zero and marked in
-// the key's meta word, so that only rows that see the key are affected.
+// shared_prepare_kernel, three jobs side by side:
+//  * CTA 0 lays out the call on the device (lengths are device data): which
+//    requests can be served, each group's shared range and each request's own
+//    range in the packed key space, the query-row tiles, and the division of
+//    all tiles' steps over the attention kernel's clusters, even to a step, so
+//    that one long prompt or many short ones fill the GPU alike;
+//  * some CTAs widen the queries (bf16 to fp16, planes of 64 dims);
+//  * the others gather each distinct row once -- shared rows once per group,
+//    not once per request -- and widen it into fp16 planes of 64 dims, which
+//    the attention kernel reads by TMA (any 128 consecutive keys are one box).
+//    Values that have no fp16 counterpart are packed as zero and marked in the
+//    key's meta word, so that only rows that see the key are affected.
+//  The packers need the packed bases only: each scans the batch's lengths
+//  itself (about 2 us, in shared memory) instead of waiting for CTA 0, which
+//  took 7 us in a launch of its own.  Batches beyond SMALL requests are
+//  planned first and packed by a second launch that reads CTA 0's arrays.
+//  HBM and L2 are the bound of the packing: 1152 bytes read and written a row.
 //
 // shared_join_kernel: the LSE merge of the tiles that several clusters share.
 #include "shared.cuh"
@@ -25,11 +30,11 @@
 namespace mlav {
 namespace {
 
-constexpr int PLAN_THREADS = 1024;
-constexpr int PACK_THREADS = 256;
-constexpr int PACK_KEYS = 32;                                        // rows per CTA iteration
-constexpr int PER_THREAD = PACK_KEYS * ROW_CHUNKS / PACK_THREADS;    // 9 granules
-static_assert(PER_THREAD * PACK_THREADS == PACK_KEYS * ROW_CHUNKS, "even split");
+constexpr int THREADS = 256;
+constexpr int PACK_KEYS = 32;                                   // rows per CTA iteration
+constexpr int PER_THREAD = PACK_KEYS * ROW_CHUNKS / THREADS;    // 9 granules
+static_assert(PER_THREAD * THREADS == PACK_KEYS * ROW_CHUNKS, "even split");
+constexpr int SMALL = 512;     // requests, groups and tiles laid out in shared memory
 
 // Inclusive block scan; `all` receives the block's total.
 __device__ __forceinline__ int block_scan(int x, int* s_warp, int& all) {
@@ -42,15 +47,13 @@ __device__ __forceinline__ int block_scan(int x, int* s_warp, int& all) {
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  int w = s_warp[lane];
+  all = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += y;
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) x += all;
+    all += s_warp[w];
   }
-  all = __shfl_sync(0xffffffffu, w, 31);
-  const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
-  return x + (warp ? before : 0);
+  return x;
 }
 
 // Largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
@@ -64,30 +67,32 @@ __device__ __forceinline__ int last_not_above(const int* a, int n, int x) {
   return lo;
 }
 
-__device__ void plan_call(const SharedParams& p) {
-  __shared__ int s_warp[PLAN_THREADS / 32];
-  __shared__ int s_bad;
-  const int tid = threadIdx.x, B = p.batch;
-  if (tid == 0) s_bad = 0;
-  __syncthreads();
-  int bad = 0;
-  for (int g = tid; g < p.groups; g += PLAN_THREADS) {
-    if (p.group_indptr[g + 1] < p.group_indptr[g]) bad = 1;
-    if (g == 0 && (p.group_indptr[0] != 0 || p.group_indptr[p.groups] != B)) bad = 1;
-  }
-  if (bad) s_bad = 1;
-  for (int b = tid; b < max(B, p.groups); b += PLAN_THREADS) p.source[b] = INT_MAX;
-  __syncthreads();
-  // Groups that do not partition the batch: one group, no request served.
-  const bool groups_ok = s_bad == 0;
-  const int G = groups_ok ? p.groups : 1;
-  auto group_begin = [&](int g) { return groups_ok ? p.group_indptr[g] : (g ? B : 0); };
-  if (!groups_ok && tid == 0) atomicOr(p.err, ERR_INDPTR);
+// The groups of a call; when they do not partition the batch: one group, and
+// no request is served.
+struct Groups {
+  const int32_t* indptr;
+  int n, batch;
+  bool ok;
+  __device__ __forceinline__ int begin(int g) const { return ok ? indptr[g] : (g ? batch : 0); }
+  __device__ __forceinline__ int of(int b) const { return ok ? last_not_above(indptr, n, b) : 0; }
+};
 
-  // Requests: can each be served?
-  int errs = 0;
-  for (int b = tid; b < B; b += PLAN_THREADS) {
-    const int g = groups_ok ? last_not_above(p.group_indptr, G, b) : 0;
+// Own rows, packed bases and each group's source request, by the whole CTA;
+// returns the packed keys.  `report`: set the error bits of what cannot be served.
+__device__ __forceinline__ int scan_requests(const SharedParams& p, int* own, int* base, int* source, int* s_warp, Groups& grp,
+                                             bool report) {
+  const int tid = threadIdx.x, B = p.batch;
+  bool bad = false;
+  for (int g = tid; g < p.groups; g += THREADS) {
+    bad |= p.group_indptr[g + 1] < p.group_indptr[g];
+    source[g] = INT_MAX;
+  }
+  bad |= p.group_indptr[0] != 0 || p.group_indptr[p.groups] != B;
+  const bool groups_ok = __syncthreads_or(bad) == 0;
+  grp = Groups{p.group_indptr, groups_ok ? p.groups : 1, B, groups_ok};
+  int errs = groups_ok ? 0 : ERR_INDPTR;
+  for (int b = tid; b < B; b += THREADS) {
+    const int g = grp.of(b);
     const int n = p.kv_lens[b], ip0 = p.kv_indptr[b], ip1 = p.kv_indptr[b + 1], ipn = p.kv_indptr[B];
     const long long need = p.page_size == 1 ? n : (static_cast<long long>(n) + PAGE - 1) / PAGE;
     const int S = groups_ok ? p.shared_lens[g] : 0;
@@ -96,114 +101,153 @@ __device__ void plan_call(const SharedParams& p) {
     const bool ok = groups_ok && len_ok && ptr_ok;
     if (!len_ok) errs |= ERR_LEN;
     else if (!ptr_ok) errs |= ERR_INDPTR;
-    p.group_of[b] = g;
-    p.own[b] = ok ? n - S : 0;         // at least T
-    if (ok) atomicMin(p.source + g, b);
+    own[b] = ok ? n - S : 0;           // at least T
+    if (ok) atomicMin(source + g, b);
   }
-  if (errs) atomicOr(p.err, errs);
-  for (int i = tid; i < B * p.T; i += PLAN_THREADS)
-    p.anc[i] = ancestor_mask(p.draft_parent + static_cast<size_t>(i / p.T) * p.T, i % p.T, p.err);
+  if (report && errs) atomicOr(p.err, errs);
   __syncthreads();
-
-  // Packed bases, in request order.
   int before = 0;
-  for (int b0 = 0; b0 < B; b0 += PLAN_THREADS) {
+  for (int b0 = 0; b0 < B; b0 += THREADS) {
     const int b = b0 + tid;
-    int prefix = 0, own = 0;
+    int prefix = 0, mine = 0;
     if (b < B) {
-      const int g = p.group_of[b];
-      own = p.own[b];
-      if (b == group_begin(g) && __ldcg(p.source + g) != INT_MAX) prefix = p.shared_lens[g];
+      const int g = grp.of(b);
+      mine = own[b];
+      if (b == grp.begin(g) && *static_cast<volatile int*>(source + g) != INT_MAX) prefix = p.shared_lens[g];
     }
     int all;
-    const int end = before + block_scan(prefix + own, s_warp, all);
+    const int end = before + block_scan(prefix + mine, s_warp, all);
     if (b < B) {
-      p.base[2 * b] = end - own - prefix;
-      p.base[2 * b + 1] = end - own;
+      base[2 * b] = end - mine - prefix;
+      base[2 * b + 1] = end - mine;
     }
     before += all;
   }
-  if (tid == 0) {
-    p.base[2 * B] = before;
-    p.totals[0] = before;
-  }
+  if (tid == 0) base[2 * B] = before;
+  __syncthreads();
+  return before;
+}
+
+struct Layout {
+  int own[SMALL], base[2 * SMALL + 1], source[SMALL];
+};
+struct PlanLayout {
+  Layout l;
+  int tile0[SMALL], cost[SMALL + 1];
+};
+
+// CTA 0.  Arrays that others read go to the workspace; the ones used here
+// only, and those of a small call, are in shared memory.
+__device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int* s_warp) {
+  __shared__ int s_max;
+  const int tid = threadIdx.x, B = p.batch, lane = tid & 31;
+  if (tid == 0) s_max = 0;
+  int* own = small ? s.l.own : p.own;
+  int* base = small ? s.l.base : p.base;
+  Groups grp;
+  const int keys = scan_requests(p, own, base, small ? s.l.source : p.source, s_warp, grp, true);
+  for (int i = tid; i < B * p.T; i += THREADS)
+    p.anc[i] = ancestor_mask(p.draft_parent + static_cast<size_t>(i / p.T) * p.T, i % p.T, p.err);
+  if (small)
+    for (int b = tid; b < B; b += THREADS) p.own[b] = own[b];
   // Tiles of each group.
+  const int G = grp.n;
+  int* tile0 = small ? s.tile0 : p.tile0;
   int tiles = 0;
-  for (int g0 = 0; g0 < G; g0 += PLAN_THREADS) {
+  for (int g0 = 0; g0 < G; g0 += THREADS) {
     const int g = g0 + tid;
     int n = 0;
-    if (g < G) n = static_cast<int>((static_cast<long long>(group_begin(g + 1) - group_begin(g)) * p.R + SH_ROWS - 1) / SH_ROWS);
+    if (g < G) n = static_cast<int>((static_cast<long long>(grp.begin(g + 1) - grp.begin(g)) * p.R + SH_ROWS - 1) / SH_ROWS);
     int all;
     const int end = tiles + block_scan(n, s_warp, all);
-    if (g < G) p.tile0[g] = end - n;
+    if (g < G) tile0[g] = end - n;
     tiles += all;
   }
-  if (tid == 0) p.totals[1] = tiles;
+  if (tid == 0) {
+    p.totals[0] = keys;
+    p.totals[1] = tiles;
+  }
   __syncthreads();
   // Tile records and the prefix sum of their costs.
-  int cost = 0;
-  for (int t0 = 0; t0 < tiles; t0 += PLAN_THREADS) {
+  int* cost = tiles <= SMALL ? s.cost : p.cost;
+  int total = 0, most = 0;
+  for (int t0 = 0; t0 < tiles; t0 += THREADS) {
     const int t = t0 + tid;
     SharedTile rec{};
     int c = 0;
     if (t < tiles) {
-      const int g = last_not_above(p.tile0, G, t);
-      const int first = group_begin(g) * p.R, rows = group_begin(g + 1) * p.R - first;
-      const int off = (t - p.tile0[g]) * SH_ROWS;
+      const int g = last_not_above(tile0, G, t);
+      const int first = grp.begin(g) * p.R, rows = grp.begin(g + 1) * p.R - first;
+      const int off = (t - tile0[g]) * SH_ROWS;
       rec.q_row0 = first + off;
       rec.nrows = min(SH_ROWS, rows - off);
       rec.b0 = rec.q_row0 / p.R;
       const int b1 = (rec.q_row0 + rec.nrows - 1) / p.R;
-      rec.own_base = p.base[2 * rec.b0 + 1];
-      rec.own_len = p.base[2 * b1 + 1] + p.own[b1] - rec.own_base;
+      rec.own_base = base[2 * rec.b0 + 1];
+      rec.own_len = base[2 * b1 + 1] + own[b1] - rec.own_base;
       if (rec.own_len > 0) {       // some request of the tile is served
-        rec.prefix_base = p.base[2 * group_begin(g)];
+        rec.prefix_base = base[2 * grp.begin(g)];
         rec.prefix_len = p.shared_lens[g];
         rec.halves = prefix_halves(rec) + (rec.own_len + SH_HALF - 1) / SH_HALF;
         rec.steps = (rec.halves + 1) / 2;
         c = rec.steps + SH_SEGMENT_COST;
       }
     }
+    most = max(most, c);
     int all;
-    const int end = cost + block_scan(c, s_warp, all);
+    const int end = total + block_scan(c, s_warp, all);
     if (t < tiles) {
       p.tiles[t] = rec;
-      p.cost[t] = end - c;
+      cost[t] = end - c;
     }
-    cost += all;
+    total += all;
   }
-  if (tid == 0) p.cost[tiles] = cost;
+  for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (lane == 0) atomicMax(&s_max, most);
+  if (tid == 0) cost[tiles] = total;
   __syncthreads();
   // Even division over as many clusters as get two steps or more each.
   // Starts lie at least SH_SEGMENT_COST + 2 apart, so no used cluster is
-  // empty and no two start in one tile's leading cost.
-  const int used = max(1, min(p.clusters, cost / (SH_SEGMENT_COST + 2)));
-  for (int c = tid; c <= p.clusters; c += PLAN_THREADS) {
+  // empty and no two start in one tile's leading cost.  Where every tile can
+  // have a cluster of its own and the longest takes no more than an even
+  // share, cut tiles starting twice, and the merge, tiles stay whole.
+  int used = max(1, min(p.clusters, total / (SH_SEGMENT_COST + 2)));
+  const bool whole = tiles <= p.clusters && s_max <= total / p.clusters + SH_SEGMENT_COST + SH_JOIN_COST;
+  if (whole) used = tiles;
+  auto start = [&](int c) {
     SharedPos at{tiles, 0};
-    if (c < used && cost > 0) {
-      const int x = static_cast<int>(static_cast<long long>(cost) * c / used);
-      at.tile = last_not_above(p.cost, tiles, x);
-      at.step = max(0, x - p.cost[at.tile] - SH_SEGMENT_COST);
+    if (whole) {
+      at.tile = min(c, tiles);
+    } else if (c < used && total > 0) {
+      const int x = static_cast<int>(static_cast<long long>(total) * c / used);
+      at.tile = last_not_above(cost, tiles, x);
+      at.step = max(0, x - cost[at.tile] - SH_SEGMENT_COST);
     }
-    p.start[c] = at;
+    return at;
+  };
+  for (int c = tid; c < p.clusters; c += THREADS) {
+    SharedShare sh{};
+    sh.from = start(c);
+    sh.to = start(c + 1);
+    if (sh.from.tile < tiles) sh.first = p.tiles[sh.from.tile];
+    p.share[c] = sh;
   }
-  __syncthreads();
   // Which clusters hold each tile.
-  for (int t = tid; t < tiles; t += PLAN_THREADS) {
-    const int steps = p.tiles[t].steps;
-    if (steps == 0) continue;
+  for (int t = tid; t < tiles; t += THREADS) {
+    const int c = cost[t + 1] - cost[t];
+    if (c == 0) continue;
     // Last cluster that starts at or before step `step` of the tile.
     auto last_before = [&](int step) {
       int lo = 0, hi = used;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        const SharedPos s = p.start[mid];
-        if (s.tile < t || (s.tile == t && s.step <= step)) lo = mid;
+        const SharedPos at = start(mid);
+        if (at.tile < t || (at.tile == t && at.step <= step)) lo = mid;
         else hi = mid;
       }
       return lo;
     };
-    const int a = last_before(0), z = last_before(steps - 1);
+    const int a = last_before(0), z = last_before(c - SH_SEGMENT_COST - 1);
     p.tiles[t].seg0 = a;
     p.tiles[t].nseg = z - a + 1;
   }
@@ -218,7 +262,7 @@ __device__ __forceinline__ bool pack_rows(const uint16_t* src, const long long* 
   uint4 v[PER_THREAD];
 #pragma unroll
   for (int u = 0; u < PER_THREAD; ++u) {
-    const int e = threadIdx.x + u * PACK_THREADS;
+    const int e = threadIdx.x + u * THREADS;
     const int r = e / ROW_CHUNKS, c = e - r * ROW_CHUNKS;
     const long long row = s_row[r];
     v[u] = make_uint4(0, 0, 0, 0);
@@ -230,7 +274,7 @@ __device__ __forceinline__ bool pack_rows(const uint16_t* src, const long long* 
   bool any = false;
 #pragma unroll
   for (int u = 0; u < PER_THREAD; ++u) {
-    const int e = threadIdx.x + u * PACK_THREADS;
+    const int e = threadIdx.x + u * THREADS;
     const int r = e / ROW_CHUNKS, c = e - r * ROW_CHUNKS;
     bool bad = false;
     uint4 w = widen_bf16x8(v[u], bad);
@@ -250,56 +294,73 @@ __device__ __forceinline__ bool pack_rows(const uint16_t* src, const long long* 
   return any;
 }
 
-__global__ void __launch_bounds__(PLAN_THREADS) shared_plan_kernel(const SharedParams p) {
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (blockIdx.x == 0) {
-    plan_call(p);
-    return;
-  }
-  // Queries: 128 rows per CTA, nine granules per thread.
-  const long long rows = static_cast<long long>(p.batch) * p.R;
-  const long long row0 = static_cast<long long>(blockIdx.x - 1) * (PACK_KEYS * (PLAN_THREADS / PACK_THREADS));
-  bool bad = false;
-  uint4 v[PER_THREAD];
-#pragma unroll
-  for (int u = 0; u < PER_THREAD; ++u) {
-    const int e = threadIdx.x + u * PLAN_THREADS;
-    const long long row = row0 + e / ROW_CHUNKS;
-    v[u] = make_uint4(0, 0, 0, 0);
-    if (row < rows) v[u] = __ldg(reinterpret_cast<const uint4*>(p.q + row * D_QK) + e % ROW_CHUNKS);
-  }
-#pragma unroll
-  for (int u = 0; u < PER_THREAD; ++u) {
-    const int e = threadIdx.x + u * PLAN_THREADS;
-    const long long row = row0 + e / ROW_CHUNKS;
-    const int c = e % ROW_CHUNKS;
-    if (row < rows)
-      *reinterpret_cast<uint4*>(p.q16 + ((c >> 3) * p.q_plane + row) * 64 + (c & 7) * 8) = widen_bf16x8(v[u], bad);
-  }
-  report_range(bad, p.err);
-}
-
-__global__ void __launch_bounds__(PACK_THREADS, 4) shared_pack_kernel(const SharedParams p) {
+// `packers` CTAs (the last of the grid) gather keys, those before them widen
+// queries, CTA 0 plans; each job's CTAs may be none.
+__global__ void __launch_bounds__(THREADS, 4) shared_prepare_kernel(const SharedParams p, int plans, int packers) {
+  __shared__ PlanLayout s;
+  __shared__ int s_warp[THREADS / 32];
   __shared__ long long s_row[PACK_KEYS];
   __shared__ int s_meta[PACK_KEYS], s_bad[PACK_KEYS];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int total = p.totals[0], tid = threadIdx.x;
+  const bool small = p.batch <= SMALL && p.groups <= SMALL;
+  const int tid = threadIdx.x;
+  if (static_cast<int>(blockIdx.x) < plans) {
+    plan_call(p, s, small, s_warp);
+    return;
+  }
+  const int packer = static_cast<int>(blockIdx.x) - (static_cast<int>(gridDim.x) - packers);
+  if (packer < 0) {
+    // Queries: 32 rows per CTA, nine granules per thread.
+    const long long rows = static_cast<long long>(p.batch) * p.R;
+    const long long row0 = static_cast<long long>(static_cast<int>(blockIdx.x) - plans) * PACK_KEYS;
+    bool bad = false;
+    uint4 v[PER_THREAD];
+#pragma unroll
+    for (int u = 0; u < PER_THREAD; ++u) {
+      const int e = tid + u * THREADS;
+      const long long row = row0 + e / ROW_CHUNKS;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (row < rows) v[u] = __ldg(reinterpret_cast<const uint4*>(p.q + row * D_QK) + e % ROW_CHUNKS);
+    }
+#pragma unroll
+    for (int u = 0; u < PER_THREAD; ++u) {
+      const int e = tid + u * THREADS;
+      const long long row = row0 + e / ROW_CHUNKS;
+      const int c = e % ROW_CHUNKS;
+      if (row < rows)
+        *reinterpret_cast<uint4*>(p.q16 + ((c >> 3) * p.q_plane + row) * 64 + (c & 7) * 8) = widen_bf16x8(v[u], bad);
+    }
+    report_range(bad, p.err);
+    return;
+  }
+  int total;
+  Groups grp;
+  if (small) {
+    total = scan_requests(p, s.l.own, s.l.base, s.l.source, s_warp, grp, false);
+  } else {
+    total = p.totals[0];
+    grp = Groups{p.group_indptr, p.groups, p.batch, true};   // (no key of a group that is none is packed)
+  }
+  const int* own = small ? s.l.own : p.own;
+  const int* base = small ? s.l.base : p.base;
+  const int* source = small ? s.l.source : p.source;
   const int chunks = (total + SH_TAIL + PACK_KEYS - 1) / PACK_KEYS;
-  for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
+  for (int chunk = packer; chunk < chunks; chunk += packers) {
     const int key0 = chunk * PACK_KEYS, rows = min(PACK_KEYS, total + SH_TAIL - key0);
     if (tid < PACK_KEYS) {
       const int key = key0 + tid;
       long long row = -1;
       int meta = META_MASKED;
       if (key < total) {
-        const int part = last_not_above(p.base, 2 * p.batch, key);
-        int b = part >> 1, j = key - p.base[part];
+        const int part = last_not_above(base, 2 * p.batch, key);
+        int b = part >> 1, j = key - base[part];
         if (part & 1) {
-          j += p.kv_lens[b] - p.own[b];               // behind the shared rows
-          meta = meta_own(b, max(-1, j - (p.kv_lens[b] - p.T)));
+          const int n = p.kv_lens[b];
+          j += n - own[b];                            // behind the shared rows
+          meta = meta_own(b, max(-1, j - (n - p.T)));
         } else {
-          b = p.source[p.group_of[b]];
+          b = source[grp.of(b)];
           meta = META_SHARED;
         }
         const long long entry = p.kv_indices[p.kv_indptr[b] + (p.page_size == 1 ? j : j / PAGE)];
@@ -322,76 +383,90 @@ __global__ void __launch_bounds__(PACK_THREADS, 4) shared_pack_kernel(const Shar
 }
 
 // Rows of tiles that several clusters hold parts of (or none: no request of
-// the tile is served), one warp per row, four rows per CTA.
-constexpr int JOIN_ROWS = 4;
+// the tile is served): 128 threads per row, a float4 of each part per thread,
+// up to JOIN_FLIGHT parts loaded before any is used.  A row's parts were just
+// written and mostly come from L2; the launch and one round trip are the time.
+constexpr int JOIN_ROWS = 2;
+constexpr int JOIN_FLIGHT = 8;
+constexpr int JOIN_MAX = 4;    // parts per lane: clusters <= 32 * JOIN_MAX
 
-__global__ void __launch_bounds__(JOIN_ROWS * 32) shared_join_kernel(const SharedParams p) {
+__global__ void __launch_bounds__(JOIN_ROWS * 128) shared_join_kernel(const SharedParams p) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int tile = blockIdx.x / (SH_ROWS / JOIN_ROWS);
   if (tile >= p.totals[1]) return;
   const SharedTile t = p.tiles[tile];
-  const int lane = threadIdx.x & 31;
-  const int r = (blockIdx.x % (SH_ROWS / JOIN_ROWS)) * JOIN_ROWS + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, col = threadIdx.x & 127;
+  const int r = (blockIdx.x % (SH_ROWS / JOIN_ROWS)) * JOIN_ROWS + (threadIdx.x >> 7);
   if (t.nseg == 1 || r >= t.nrows) return;
   const int row = t.q_row0 + r;
   const float nan = __int_as_float(0x7fc00000);
-  float4 acc[4];
-#pragma unroll
-  for (int f = 0; f < 4; ++f) acc[f] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc = make_float4(nan, nan, nan, nan);
   float lse = nan;
   if (t.nseg > 1 && p.own[row / p.R] > 0) {
-    const SharedPos s0 = p.start[t.seg0];
-    auto slot = [&](int s) { return part_slot(t.seg0 + s, s > 0 || (s0.tile == tile && s0.step == 0)); };
-    float mx = -INFINITY, sum = 0.f;
+    // The first part is its cluster's first segment if the cluster starts
+    // with the tile; the others begin inside it, hence with it.
+    const SharedPos from = p.share[t.seg0].from;
+    const int slot0 = part_slot(t.seg0, from.tile == tile);
+    auto at = [&](int s) { return static_cast<size_t>(s ? part_slot(t.seg0 + s, true) : slot0) * SH_ROWS + r; };
+    float L[JOIN_MAX], mx = -INFINITY;
     bool any_nan = false;
-    for (int s = lane; s < t.nseg; s += 32) {
-      const float L = p.part_lse[static_cast<size_t>(slot(s)) * SH_ROWS + r];
-      any_nan |= L != L;
-      mx = fmaxf(mx, L);
+#pragma unroll
+    for (int k = 0; k < JOIN_MAX; ++k) {
+      L[k] = 32 * k + lane < t.nseg ? p.part_lse[at(32 * k + lane)] : -INFINITY;
+      any_nan |= L[k] != L[k];
+      mx = fmaxf(mx, L[k]);
     }
+    any_nan = __any_sync(0xffffffffu, any_nan);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    any_nan = __any_sync(0xffffffffu, any_nan);
-    const float base = mx == -INFINITY ? 0.f : mx;
-    for (int s = 0; s < t.nseg; ++s) {
-      const size_t at = static_cast<size_t>(slot(s)) * SH_ROWS + r;
-      const float w = ex2((p.part_lse[at] - base) * kLog2e);
-      sum += w;
-      if (w == 0.f) continue;
-      const float4* o = reinterpret_cast<const float4*>(p.part_o + at * D_V) + lane;
+    const float top = mx == -INFINITY ? 0.f : mx;
+    float sum = 0.f;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const float4 x = __ldcs(o + 32 * f);
-        acc[f].x += w * x.x;
-        acc[f].y += w * x.y;
-        acc[f].z += w * x.z;
-        acc[f].w += w * x.w;
+    for (int k = 0; k < JOIN_MAX; ++k) {
+      L[k] = ex2((L[k] - top) * kLog2e);
+      sum += L[k];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // Every key masked (bad slots): weight 0 everywhere.
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < JOIN_MAX; ++k) {
+      for (int s0 = 32 * k; s0 < min(t.nseg, 32 * k + 32); s0 += JOIN_FLIGHT) {
+        float4 x[JOIN_FLIGHT];
+#pragma unroll
+        for (int f = 0; f < JOIN_FLIGHT; ++f)
+          if (s0 + f < t.nseg) x[f] = __ldcs(reinterpret_cast<const float4*>(p.part_o + at(s0 + f) * D_V) + col);
+#pragma unroll
+        for (int f = 0; f < JOIN_FLIGHT; ++f) {
+          const float w = __shfl_sync(0xffffffffu, L[k], (s0 + f) & 31) * inv;
+          if (s0 + f >= t.nseg || w == 0.f) continue;   // (a part of weight 0 may hold anything)
+          acc.x += w * x[f].x;
+          acc.y += w * x[f].y;
+          acc.z += w * x[f].z;
+          acc.w += w * x[f].w;
+        }
       }
     }
-    // Every key masked (bad slots): weight 0 everywhere.
-    const float inv = any_nan ? nan : sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-    for (int f = 0; f < 4; ++f) acc[f] = make_float4(acc[f].x * inv, acc[f].y * inv, acc[f].z * inv, acc[f].w * inv);
-    lse = any_nan ? nan : sum > 0.f ? base + logf(sum) : -INFINITY;
-  } else {
-#pragma unroll
-    for (int f = 0; f < 4; ++f) acc[f] = make_float4(nan, nan, nan, nan);
-  }
-#pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    const size_t at = static_cast<size_t>(row) * D_V / 4 + lane + 32 * f;
-    if (p.out_bf16) {
-      __nv_bfloat162 lo = __floats2bfloat162_rn(acc[f].x, acc[f].y), hi = __floats2bfloat162_rn(acc[f].z, acc[f].w);
-      reinterpret_cast<uint2*>(p.out)[at] = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-    } else {
-      reinterpret_cast<float4*>(p.out)[at] = acc[f];
+    lse = sum > 0.f ? top + logf(sum) : -INFINITY;
+    if (any_nan) {
+      acc = make_float4(nan, nan, nan, nan);
+      lse = nan;
     }
   }
-  if (lane == 0) p.lse[row] = lse;
+  const size_t at = static_cast<size_t>(row) * (D_V / 4) + col;
+  if (p.out_bf16) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+    reinterpret_cast<uint2*>(p.out)[at] = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+  } else {
+    reinterpret_cast<float4*>(p.out)[at] = acc;
+  }
+  if (col == 0) p.lse[row] = lse;
 }
 
-cudaError_t launch(void (*kernel)(const SharedParams), long long grid, unsigned block, const SharedParams& p,
-                   cudaStream_t stream, bool overlap) {
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), long long grid, unsigned block, cudaStream_t stream, bool overlap, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(block);
@@ -401,25 +476,25 @@ cudaError_t launch(void (*kernel)(const SharedParams), long long grid, unsigned 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = overlap ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace
 
-cudaError_t launch_shared_plan(const SharedParams& p, cudaStream_t stream) {
+cudaError_t launch_shared_prepare(const SharedParams& p, int num_sms, cudaStream_t stream) {
   const long long rows = static_cast<long long>(p.batch) * p.R;
-  const int per_cta = PACK_KEYS * (PLAN_THREADS / PACK_THREADS);
-  return launch(shared_plan_kernel, 1 + (rows + per_cta - 1) / per_cta, PLAN_THREADS, p, stream, false);
-}
-
-cudaError_t launch_shared_pack(const SharedParams& p, int num_sms, cudaStream_t stream) {
+  const long long query_ctas = (rows + PACK_KEYS - 1) / PACK_KEYS;
   const long long most = static_cast<long long>(p.batch) * p.max_kv_len + SH_TAIL;
-  const long long chunks = (most + PACK_KEYS - 1) / PACK_KEYS;
-  return launch(shared_pack_kernel, std::min<long long>(chunks, 6LL * num_sms), PACK_THREADS, p, stream, true);
+  const int packers = static_cast<int>(std::min<long long>((most + PACK_KEYS - 1) / PACK_KEYS, 4LL * num_sms));
+  if (p.batch <= SMALL && p.groups <= SMALL)
+    return launch(shared_prepare_kernel, 1 + query_ctas + packers, THREADS, stream, false, p, 1, packers);
+  const cudaError_t e = launch(shared_prepare_kernel, 1 + query_ctas, THREADS, stream, false, p, 1, 0);
+  return e != cudaSuccess ? e : launch(shared_prepare_kernel, packers, THREADS, stream, true, p, 0, packers);
 }
 
 cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream) {
-  return launch(shared_join_kernel, static_cast<long long>(p.max_tiles) * (SH_ROWS / JOIN_ROWS), JOIN_ROWS * 32, p, stream, true);
+  if (p.clusters > 32 * JOIN_MAX) return cudaErrorInvalidValue;
+  return launch(shared_join_kernel, static_cast<long long>(p.max_tiles) * (SH_ROWS / JOIN_ROWS), JOIN_ROWS * 128, stream, true, p);
 }
 
 }  // namespace mlav
