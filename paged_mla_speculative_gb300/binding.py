@@ -133,8 +133,8 @@ def _check(status: int, what: str):
 
 
 def _stream_ptr(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:   # as torch.cuda.current_stream().cuda_stream, without building the object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -269,6 +269,9 @@ class Plan:
 
 
 def _expect(t: torch.Tensor, name: str, dtype, device=None, shape=None):
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.is_contiguous()
+            and (device is None or t.device == device) and (shape is None or t.shape == shape)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -290,10 +293,11 @@ def _expect_strided(t: torch.Tensor, name: str, dtype, device, shape):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    strides = [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], shape)]
-    if t.stride(-1) != 1 or any(s % 8 for s in strides):
+    *strides, last = t.stride()
+    strides = [s if n > 1 else 0 for s, n in zip(strides, shape)]
+    if last != 1 or sum(s % 8 for s in strides):
         raise ValueError(f"{name}'s last dim must be contiguous and its other strides multiples of 8")
     return strides
 

@@ -388,7 +388,7 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
     return MLA_VERIFY_ERR_CUDA;
   if (mlav::partial_mma_prepare() != cudaSuccess || mlav::partial_tc_prepare() != cudaSuccess ||
       mlav::partial_pair_prepare() != cudaSuccess || mlav::pack_kv_prepare() != cudaSuccess ||
-      mlav::partial_shared_prepare() != cudaSuccess)
+      mlav::partial_shared_prepare() != cudaSuccess || mlav::page_pool_prepare() != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
 
   mla_verify_plan* pl = new (std::nothrow) mla_verify_plan();
@@ -1041,7 +1041,7 @@ int mla_verify_fork_kv(mla_verify_plan* pl, int num_children, const int32_t* par
   a.child_lens = child_lens;
   a.ticket = reinterpret_cast<unsigned*>(pl->err) + kTicketWord;
   a.err = pl->err;
-  if (mlav::launch_fork_kv(a, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+  if (mlav::launch_fork_kv(a, pl->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
       note_done(pl, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
   return MLA_VERIFY_OK;
@@ -1068,7 +1068,8 @@ int mla_verify_free_kv(mla_verify_plan* pl, int batch, const int32_t* kv_indices
   a.free_count = free_count;
   a.page_bits = pl->page_bits;
   a.err = pl->err;
-  if (mlav::launch_free_kv(a, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+  const long long entries = batch * ceil_div(pl->max_kv_len, mlav::PAGE);
+  if (mlav::launch_free_kv(a, static_cast<int>(std::min<long long>(entries, INT32_MAX)), static_cast<cudaStream_t>(stream)) != cudaSuccess ||
       note_done(pl, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
   return MLA_VERIFY_OK;

@@ -154,7 +154,8 @@ struct ForkArgs {
   unsigned* ticket;                 // plan workspace, 0 between calls
   int* err;
 };
-cudaError_t launch_fork_kv(const ForkArgs& a, cudaStream_t stream);
+cudaError_t page_pool_prepare();
+cudaError_t launch_fork_kv(const ForkArgs& a, int num_sms, cudaStream_t stream);
 struct FreeArgs {
   const int32_t* kv_indices;
   const int32_t* kv_indptr;         // [batch + 1]
@@ -165,6 +166,7 @@ struct FreeArgs {
   unsigned* page_bits;              // plan workspace, one bit per page, 0 between calls
   int* err;
 };
-cudaError_t launch_free_kv(const FreeArgs& a, cudaStream_t stream);
+// `max_entries`: of the tables, as far as the host can tell.
+cudaError_t launch_free_kv(const FreeArgs& a, int max_entries, cudaStream_t stream);
 
 }  // namespace mlav

@@ -25,19 +25,27 @@
 // partial page outside the cache is copied as zeros.
 #include "common.cuh"
 #include "kernels.h"
+#include "tc_ptx.cuh"
 
 #include <cooperative_groups.h>
+
+#include <algorithm>
 
 namespace mlav {
 namespace {
 
 constexpr int FORK_THREADS = 256;
-constexpr int FORK_CHUNK = 4 * FORK_THREADS;                       // table entries per CTA
-constexpr int COPY_PER_THREAD = PAGE * ROW_CHUNKS / FORK_THREADS;  // 18 granules
+constexpr int FORK_CHUNK = 4 * FORK_THREADS;     // table entries per CTA
+// Partial pages are copied through shared memory by bulk copies, two pieces of
+// half a page in turn: the rows of a partial page are one run of bytes.
+constexpr int PIECE = PAGE / 2 * ROW_BYTES;
+constexpr int COPY_SMEM = 2 * PIECE;
+constexpr int COPY_CTAS_PER_SM = 3;
+constexpr long long COPY_LIMIT = 1LL << 31;      // cycles before a wait gives up
 
 // Rows and entries of child i, or zero entries with the error bit that says why.
 struct Child {
-  int parent, n;
+  int parent, n, ip0;
   long long total, fresh;   // entries, of them fresh
   int bad;
 };
@@ -49,10 +57,11 @@ __device__ __forceinline__ Child load_child(const ForkArgs& a, int i) {
     return c;
   }
   c.n = a.kv_lens[c.parent];
-  const long long p0 = a.kv_indptr[c.parent], p1 = a.kv_indptr[c.parent + 1], pn = a.kv_indptr[a.num_parents];
+  c.ip0 = a.kv_indptr[c.parent];
+  const long long p1 = a.kv_indptr[c.parent + 1], pn = a.kv_indptr[a.num_parents];
   if (c.n < 0 || static_cast<long long>(c.n) + a.extra > a.max_kv_len) {
     c.bad = ERR_LEN;
-  } else if (p0 < 0 || p1 > pn || p1 - p0 < (static_cast<long long>(c.n) + PAGE - 1) / PAGE) {
+  } else if (c.ip0 < 0 || p1 > pn || p1 - c.ip0 < (static_cast<long long>(c.n) + PAGE - 1) / PAGE) {
     c.bad = ERR_INDPTR;
   } else {
     c.total = (static_cast<long long>(c.n) + a.extra + PAGE - 1) / PAGE;
@@ -85,18 +94,83 @@ __device__ __forceinline__ Sums block_scan(Sums x, Sums* s_warp, Sums& all) {
   return x;
 }
 
-// grid (table chunks + layers, children).  Every CTA scans all children's
+// One thread: `bytes` from src to dst for each layer l0, l0 + step, .., in
+// pieces that alternate between the two buffers, so that one is filled while
+// the other is written out.
+__device__ __forceinline__ void copy_layers(const ForkArgs& a, uint8_t* buf, uint32_t mbar, long long from, long long to,
+                                            int bytes, int l0, int step) {
+  const int pieces = (bytes + PIECE - 1) / PIECE;
+  const int total = (a.num_layers - l0 + step - 1) / step * pieces;
+  auto piece = [&](int i, const uint8_t*& src, uint8_t*& dst, int& size) {
+    const int off = i % pieces * PIECE;
+    uint8_t* layer = reinterpret_cast<uint8_t*>(a.kv_cache + static_cast<long long>(l0 + i / pieces * step) * a.layer_stride);
+    src = layer + from * PAGE * ROW_BYTES + off;
+    dst = layer + to * PAGE * ROW_BYTES + off;
+    size = min(PIECE, bytes - off);
+  };
+  auto load = [&](int i) {
+    const uint8_t* src;
+    uint8_t* dst;
+    int size;
+    piece(i, src, dst, size);
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(mbar + 8 * (i & 1)), "r"(size) : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                     smem_u32(buf) + (i & 1) * PIECE),
+                 "l"(src), "r"(size), "r"(mbar + 8 * (i & 1))
+                 : "memory");
+  };
+  load(0);
+  for (int i = 0; i < total; ++i) {
+    if (i + 1 < total) {
+      // The other buffer is free once its last piece has been read out.
+      if (i) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+      load(i + 1);
+    }
+    // (Past the limit the error is set, and the copy in flight gets as long
+    // again before the shared memory it lands in is given up.)
+    const long long t0 = clock64();
+    bool late = false;
+    while (!tc::mbar_try(mbar + 8 * (i & 1), (i >> 1) & 1)) {
+      if (!late && clock64() - t0 > COPY_LIMIT) {
+        atomicOr(a.err, ERR_TIMEOUT);
+        late = true;
+      }
+      if (late && clock64() - t0 > 2 * COPY_LIMIT) break;
+    }
+    if (late) break;
+    const uint8_t* src;
+    uint8_t* dst;
+    int size;
+    piece(i, src, dst, size);
+    asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;\n" ::"l"(dst),
+                 "r"(smem_u32(buf) + (i & 1) * PIECE), "r"(size)
+                 : "memory");
+  }
+  asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+}
+
+// grid (table_parts + copy_parts, children).  Every CTA scans all children's
 // counts itself (a few loads per thread), which gives its child's offsets and
 // the capacity cut without a second launch; the last CTA to have read
-// free_count lowers it.
+// free_count lowers it.  Copy part k of a child takes layers k, k +
+// copy_parts, ..; as many parts as fill the SMs once, so that the scan (about
+// 3 us of dependent loads) is paid once per SM slot and not once per layer.
 __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a, int table_parts) {
+  extern __shared__ __align__(128) uint8_t s_copy[];
   __shared__ Sums s_warp[FORK_THREADS / 32];
   __shared__ Sums s_mine, s_fit;
+  __shared__ Child s_child;
   __shared__ unsigned long long s_last[2];
+  __shared__ __align__(8) uint64_t s_mbar[2];
   const int c = blockIdx.y, tid = threadIdx.x;
   const long long left = max(0, min(*a.free_count, a.num_pages));
   if (tid < 2) s_last[tid] = 0;
-  if (tid == 0) s_mine = Sums{0, 0};
+  if (tid == 0) {
+    tc::mbar_init(smem_u32(s_mbar), 1);
+    tc::mbar_init(smem_u32(s_mbar + 1), 1);
+    tc::mbar_fence_init();
+  }
   Sums before{0, 0};
   for (int base = 0; base < a.num_children; base += FORK_THREADS) {
     const int i = base + tid;
@@ -104,6 +178,7 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
     if (i < a.num_children) {
       const Child ch = load_child(a, i);
       x = Sums{ch.total, ch.fresh};
+      if (i == c) s_child = ch;
     }
     Sums all;
     const Sums own = x;
@@ -132,7 +207,7 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
       *a.free_count = static_cast<int32_t>(left - static_cast<long long>(s_last[1]));
     }
   }
-  const Child ch = load_child(a, c);
+  const Child ch = s_child;
   const bool fits = s_fit.total <= a.capacity && s_fit.fresh <= left;
   if (blockIdx.x == 0 && tid == 0) {
     if (ch.bad) atomicOr(a.err, ch.bad);
@@ -143,7 +218,7 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
   }
   if (!fits || ch.total == 0) return;
   const int full = ch.n / PAGE, partial = ch.n % PAGE;
-  const int32_t* held = a.kv_indices + a.kv_indptr[ch.parent];
+  const int32_t* held = a.kv_indices + ch.ip0;
   // The page at entry j >= full.
   auto fresh = [&](long long j) { return a.free_pages[left - 1 - (s_mine.fresh + j - full)]; };
 
@@ -167,22 +242,15 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
   if (partial == 0) return;
   const long long from = held[full], to = fresh(full);
   if (to < 0 || to >= a.num_pages) return;             // reported with the table
-  const bool src_ok = from >= 0 && from < a.num_pages;
-  if (!src_ok && tid == 0) atomicOr(a.err, ERR_SLOT);
-  uint16_t* layer = a.kv_cache + static_cast<long long>(blockIdx.x - table_parts) * a.layer_stride;
-  const uint4* src = reinterpret_cast<const uint4*>(layer + from * PAGE * D_QK);
-  uint4* dst = reinterpret_cast<uint4*>(layer + to * PAGE * D_QK);
-  uint4 v[COPY_PER_THREAD];
-#pragma unroll
-  for (int u = 0; u < COPY_PER_THREAD; ++u) {
-    const int e = tid + u * FORK_THREADS;
-    v[u] = make_uint4(0, 0, 0, 0);
-    if (src_ok && e < partial * ROW_CHUNKS) v[u] = src[e];
+  const int part = static_cast<int>(blockIdx.x) - table_parts, parts = static_cast<int>(gridDim.x) - table_parts;
+  if (from >= 0 && from < a.num_pages) {
+    if (tid == 0) copy_layers(a, s_copy, smem_u32(s_mbar), from, to, partial * ROW_BYTES, part, parts);
+    return;
   }
-#pragma unroll
-  for (int u = 0; u < COPY_PER_THREAD; ++u) {
-    const int e = tid + u * FORK_THREADS;
-    if (e < partial * ROW_CHUNKS) dst[e] = v[u];
+  if (tid == 0) atomicOr(a.err, ERR_SLOT);
+  for (int l = part; l < a.num_layers; l += parts) {   // no such page: zeros
+    uint4* dst = reinterpret_cast<uint4*>(a.kv_cache + static_cast<long long>(l) * a.layer_stride + to * PAGE * D_QK);
+    for (int e = tid; e < partial * ROW_CHUNKS; e += FORK_THREADS) dst[e] = make_uint4(0, 0, 0, 0);
   }
 }
 
@@ -190,7 +258,7 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
 // marks the page in a bit map), then the bit map read in order, so the pushed
 // pages ascend whatever order the counts fell in, and cleared for the next call.
 constexpr int FREE_THREADS = 1024;
-constexpr int FREE_CTAS = 8;
+constexpr int FREE_MAX_CTAS = 8;
 
 __global__ void __launch_bounds__(FREE_THREADS) free_kv_kernel(const FreeArgs a) {
   namespace cg = cooperative_groups;
@@ -278,22 +346,33 @@ __global__ void __launch_bounds__(FREE_THREADS) free_kv_kernel(const FreeArgs a)
 
 }  // namespace
 
-cudaError_t launch_fork_kv(const ForkArgs& a, cudaStream_t stream) {
+cudaError_t page_pool_prepare() {
+  return cudaFuncSetAttribute(fork_kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, COPY_SMEM);
+}
+
+cudaError_t launch_fork_kv(const ForkArgs& a, int num_sms, cudaStream_t stream) {
   const int entries = (a.max_kv_len + PAGE - 1) / PAGE;
   const int table_parts = (entries + FORK_CHUNK - 1) / FORK_CHUNK;
-  const dim3 grid(table_parts + a.num_layers, a.num_children);
-  fork_kv_kernel<<<grid, FORK_THREADS, 0, stream>>>(a, table_parts);
+  const int slots = COPY_CTAS_PER_SM * num_sms;
+  const int copy_parts = std::max(1, std::min(a.num_layers, slots / a.num_children));
+  const dim3 grid(table_parts + copy_parts, a.num_children);
+  fork_kv_kernel<<<grid, FORK_THREADS, COPY_SMEM, stream>>>(a, table_parts);
   return cudaGetLastError();
 }
 
-cudaError_t launch_free_kv(const FreeArgs& a, cudaStream_t stream) {
+cudaError_t launch_free_kv(const FreeArgs& a, int max_entries, cudaStream_t stream) {
+  // One CTA while it has at most four entries and four bit-map words per
+  // thread; the cluster's barriers cost about 1 us.
+  const long long work = std::max<long long>(max_entries, a.num_pages / 32);
+  int ctas = 1;
+  while (ctas < FREE_MAX_CTAS && work > 4LL * FREE_THREADS * ctas) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(FREE_CTAS);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(FREE_THREADS);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = FREE_CTAS;
+  attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
