@@ -10,7 +10,7 @@
 //     S^T[key, row] = K_pair[256 x 576] . Q_tile[128 x 576]^T
 //     O^T[dim, row] += V_pair^T[512 x 256] . P^T[256 x 128]
 // with the running maximum and sum in fp32, P in fp16 (rounded once; with the
-// bf16 keys widened to fp16, which is exact, its 2^-12 is the largest error),
+// bf16 keys widened to fp16, which is exact, its 2^-11 is the largest error),
 // O^T in tensor memory, split by value dim over the two CTAs.
 //
 // What differs is the schedule.  The grid is one cluster per SM pair; cluster
@@ -94,6 +94,54 @@ constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3FFF) | (lbo >> 4) << 16; }
 
 constexpr int FEW_MOVED = 4;
+// Bounded waits of a warp.  wait_own: for barriers that TMA, tcgen05.commit
+// and this CTA's threads complete; wait_peer: for those that the peer's
+// st.async complete, acquiring its stores into this CTA's shared memory.
+// (pair_common.cuh's waits acquire all memory at cluster scope, which drops
+// the SM's L1 lines, spilled registers among them, every step.)
+template <bool PEER>
+__device__ __forceinline__ void wait_bounded(uint32_t mbar, uint32_t parity, volatile int* abort, int* err) {
+  auto done = [&]() { return PEER ? tc::mbar_try_cluster_relaxed(mbar, parity) : tc::mbar_try(mbar, parity); };
+  if (!done()) {
+    const long long t0 = clock64();
+    while (!done()) {
+      if (*abort) break;
+      if (clock64() - t0 > WAIT_LIMIT) {
+        *abort = 1;
+        atomicOr(err, ERR_TIMEOUT);
+        break;
+      }
+    }
+  }
+  if (PEER) tc::fence_acquire_shared_cluster();
+  __syncwarp();
+}
+__device__ __forceinline__ void wait_own(uint32_t mbar, uint32_t parity, volatile int* abort, int* err) {
+  wait_bounded<false>(mbar, parity, abort, err);
+}
+__device__ __forceinline__ void wait_peer(uint32_t mbar, uint32_t parity, volatile int* abort, int* err) {
+  wait_bounded<true>(mbar, parity, abort, err);
+}
+
+// Row maxima (or sums) of a warp: lane t starts with eight rows' values over
+// its own keys, y[2i + e] of row 8i + 2 (t % 4) + e, and ends with the result
+// of row 16 b4 + 8 b3 + 2 (t % 4) + b2 (b: the bits of t).
+template <bool SUM>
+__device__ __forceinline__ float reduce_rows(float (&y)[8], int lane) {
+#pragma unroll
+  for (int w = 16, n = 4; n >= 1; w >>= 1, n >>= 1) {
+    const bool upper = (lane & w) != 0;
+#pragma unroll
+    for (int c = 0; c < n; ++c) {
+      const float send = upper ? y[c] : y[c + n];
+      const float keep = upper ? y[c + n] : y[c];
+      const float got = __shfl_xor_sync(0xffffffffu, send, w);
+      y[c] = SUM ? keep + got : fmaxf(keep, got);
+    }
+  }
+  return y[0];
+}
+
 constexpr uint32_t ABSENT_BYTES = 4;   // the odd CTA's signal for a unit it has no half block for
 
 struct Segment {
@@ -209,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         // (its O^T units, already under way, come after it).  Rows past the
         // tile are the next tile's (or zeros past the batch): their columns
         // of S^T and O^T are not stored.
-        if (k > 0) wait_warp(mbar(MB_QE), static_cast<uint32_t>((k - 1) & 1), s_abort, p.err);
+        if (k > 0) wait_own(mbar(MB_QE), static_cast<uint32_t>((k - 1) & 1), s_abort, p.err);
         if (*s_abort) break;
         if (rank == 0) {
           if (lane == 0) tc::mbar_arrive_expect(mbar(MB_Q), 2 * 9 * Q_CHUNK);
@@ -237,7 +285,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           const int pair_idx = is_s ? u : 2 * (u >> 1) + static_cast<int>(rank);
           const bool mine = hb0 + h < s.t.halves;
           const bool peers = is_s ? hb0 + static_cast<int>(peer) < s.t.halves : mine;
-          if (n >= NSLOT) wait_warp(mbar(MB_EMPTY + slot), static_cast<uint32_t>((n / NSLOT - 1) & 1), s_abort, p.err);
+          if (n >= NSLOT) wait_own(mbar(MB_EMPTY + slot), static_cast<uint32_t>((n / NSLOT - 1) & 1), s_abort, p.err);
           if (*s_abort) break;
           if (rank == 0) {
             if (lane == 0)
@@ -256,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (is_s && cw == NCOPY - 1) {
           const int g = g0 + i;
           const bool mine = hb0 + static_cast<int>(rank) < s.t.halves, peers = hb0 + static_cast<int>(peer) < s.t.halves;
-          if (g > 0) wait_warp(mbar(MB_REMPTY), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
+          if (g > 0) wait_own(mbar(MB_REMPTY), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
           if (*s_abort) break;
           if (rank == 0) {
             if (lane == 0) tc::mbar_arrive_expect(mbar(MB_RFULL), (mine ? CHUNK : 0) + (peers ? CHUNK : ABSENT_BYTES));
@@ -286,8 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       for (int i = 0; i < s.steps; ++i, ++g) {
         if (lane == 0) tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
         __syncwarp();
-        wait_warp(mbar(MB_P), static_cast<uint32_t>(g & 1), s_abort, p.err);
-        wait_warp(mbar(MB_PX), static_cast<uint32_t>(g & 1), s_abort, p.err);
+        wait_own(mbar(MB_P), static_cast<uint32_t>(g & 1), s_abort, p.err);
+        wait_peer(mbar(MB_PX), static_cast<uint32_t>(g & 1), s_abort, p.err);
         tc::fence_async_smem();   // the st.async bytes are read by the tensor core next
         if (lane == 0) tc::st_async_b32(even_word, static_cast<uint32_t>(g), even_mbar(MB_PF));
         __syncwarp();
@@ -298,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     int n = 0, g0 = 0, k = 0;
 #pragma unroll 1
     for (int tile = from.tile; next_segment(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
-      wait_warp(mbar(MB_Q), static_cast<uint32_t>(k & 1), s_abort, p.err);
+      wait_own(mbar(MB_Q), static_cast<uint32_t>(k & 1), s_abort, p.err);
       tc::fence_after_sync();
 #pragma unroll 1
       for (int f = 0; f < 2 * s.steps && !*s_abort; ++f) {
@@ -311,7 +359,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
           for (int u = 0; u < 4; ++u, ++n) {
             const int slot = n % NSLOT;
-            wait_warp(mbar(MB_FULL + slot), static_cast<uint32_t>((n / NSLOT) & 1), s_abort, p.err);
+            wait_own(mbar(MB_FULL + slot), static_cast<uint32_t>((n / NSLOT) & 1), s_abort, p.err);
             tc::fence_after_sync();
             if (tc::elect_one()) {
               const uint32_t a = desc_lo(sbase + OFF_RING + slot * 2 * CHUNK, 16);
@@ -324,7 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             }
             __syncwarp();
           }
-          wait_warp(mbar(MB_RFULL), static_cast<uint32_t>(g & 1), s_abort, p.err);
+          wait_own(mbar(MB_RFULL), static_cast<uint32_t>(g & 1), s_abort, p.err);
           tc::fence_after_sync();
           if (tc::elect_one()) {
             const uint32_t a = desc_lo(sbase + OFF_ROPE, 16), bq = desc_lo(sbase + OFF_Q + 8 * Q_CHUNK, 16);
@@ -343,16 +391,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             tc::mbar_arrive_expect(mbar(MB_PF), 4);
           }
           __syncwarp();
-          wait_warp(mbar(MB_P), static_cast<uint32_t>(g & 1), s_abort, p.err);
-          wait_warp(mbar(MB_PX), static_cast<uint32_t>(g & 1), s_abort, p.err);
-          wait_warp(mbar(MB_PF), static_cast<uint32_t>(g & 1), s_abort, p.err);
+          wait_own(mbar(MB_P), static_cast<uint32_t>(g & 1), s_abort, p.err);
+          wait_peer(mbar(MB_PX), static_cast<uint32_t>(g & 1), s_abort, p.err);
+          wait_peer(mbar(MB_PF), static_cast<uint32_t>(g & 1), s_abort, p.err);
           tc::fence_async_smem();
           tc::fence_after_sync();
 #pragma unroll 1
           for (int u = 0; u < 4; ++u, ++n) {
             const int t = u >> 1, h = u & 1;
             const int slot = n % NSLOT;
-            wait_warp(mbar(MB_FULL + slot), static_cast<uint32_t>((n / NSLOT) & 1), s_abort, p.err);
+            wait_own(mbar(MB_FULL + slot), static_cast<uint32_t>((n / NSLOT) & 1), s_abort, p.err);
             tc::fence_after_sync();
             if (tc::elect_one()) {
               if (2 * (s.sa + i) + h < s.t.halves) {
@@ -381,16 +429,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     // The four warps of a row group (32 rows; a warp has 32 keys of each) meet
     // at the group's named barrier; they never leave the loops early, and
     // after an abort their waits return at once.
-    const int j = quad * 32 + lane;     // key of this thread = TMEM lane
+    // A warp's 32 keys x 32 rows are spread over its lanes as MMA accumulators
+    // are: lane t holds keys t / 4 + 8k (k < 4) and, of each, rows 8i + 2 (t %
+    // 4) + e (i < 4, e < 2), so that a row's maximum and sum over the warp's
+    // keys take three operations in the lane and seven shuffles for all rows
+    // (with a key per lane they took 31), and P^T goes out by stmatrix.
     const int c0 = grp * 32;            // pair rows c0 .. c0+31
+    const int key = lane >> 2, pair = 2 * (lane & 3);
+    const int j = quad * 32 + lane;     // the key whose meta word this lane loads
+    // The row whose maximum and sum this lane ends up with.
+    const int row = c0 + (lane & 16) + (lane & 8) + pair + ((lane >> 2) & 1);
     const float scale2 = p.scale_log2;
     auto group_sync = [&]() { named_sync(1 + grp, 128); };
-    // This key's P^T row (key half = rank) in the CTA that holds the group's
-    // rows: a local store, or st.async into the peer with its MB_PX.
+    // P^T (key half = rank) goes to the CTA that holds the group's rows: by
+    // stmatrix here, or by st.async into the peer with its MB_PX.  Keys k * 8
+    // of the warp: + 1024 k bytes.
     const bool p_local = (grp >> 1) == static_cast<int>(rank);
-    const uint32_t p_off = OFF_P + rank * CHUNK + j * 128;
-    const uint32_t p_peer = tc::peer_addr(sbase + p_off, peer);
-    const uint32_t red_off = ((c0 + lane) * 4 + quad) * 4;   // this warp's maximum of row c0 + lane
+    const uint32_t p_warp = sbase + OFF_P + rank * CHUNK + quad * 32 * 128;
+    const uint32_t p_matrix = p_warp + (lane & 7) * 128 + ((((grp & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4);
+    const uint32_t p_peer = tc::peer_addr(p_warp + key * 128 + ((((grp & 1) * 4 + (lane & 3)) ^ key) << 4), peer);
+    const uint32_t red_off = (row * 4 + quad) * 4;   // this warp's maximum of the lane's row
     const uint32_t xred_peer = tc::peer_addr(sbase + OFF_XRED + red_off, peer);
     int g = 0, k = 0;   // steps and segments so far
 #pragma unroll 1
@@ -411,110 +469,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       int meta = load_meta(0);
       group_sync();   // the previous segment's rows are read
       if (quad == 0) {
-        int2 row = make_int2(-1, 0);
+        int2 of = make_int2(-1, 0);
         if (c0 + lane < s.t.nrows) {
           const int q = s.t.q_row0 + c0 + lane, b = q / p.R;
-          if (p.own[b] > 0) row = make_int2(b, static_cast<int>(p.anc[b * p.T + (q - b * p.R) / p.H]));
+          if (p.own[b] > 0) of = make_int2(b, static_cast<int>(p.anc[b * p.T + (q - b * p.R) / p.H]));
         }
-        s_row[c0 + lane] = row;
+        s_row[c0 + lane] = of;
       }
       group_sync();
-      float mrow = -INFINITY;             // row c0 + lane's running max, the same in the group's warps of both CTAs
+      float mrow = -INFINITY;             // the lane's row's running max, the same in the group's warps of both CTAs
       float lrun = 0.f;                   // its sum over this warp's keys so far
 #pragma unroll 1
       for (int it = 0; it < nsteps; ++it, ++g) {
-        // The group's rows that see this key (bit c: row c0 + c), decided
-        // while S^T is computed.
-        uint32_t vis = 0;
-        if (meta >= 0) {
-          const int m = meta & ~META_POISON;
-          if (m == META_SHARED) {
-            vis = 0xffffffffu;
-          } else {
-            const int b = m >> 6, d = (m & 63) - 2;
+        // Decided while S^T is computed: do all rows see all of the warp's
+        // keys?  If not, which: bit 8k + 2i + e for key k and row (i, e).
+        const bool plain = __all_sync(0xffffffffu, meta == META_SHARED);
+        uint32_t vis = 0, poison = 0;
+        if (!plain) {
+#pragma unroll 1
+          for (int k8 = 0; k8 < 4; ++k8) {
+            const int m = __shfl_sync(0xffffffffu, meta, key + 8 * k8);
+            if (m < 0) continue;
+            poison |= m & META_POISON ? 1u << k8 : 0u;
+            const int w = m & ~META_POISON, b = w >> 6, d = (w & 63) - 2;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const int2 row = s_row[c0 + c];
-              const bool v = row.x == b && (d < 0 || ((static_cast<uint32_t>(row.y) >> d) & 1u));
-              vis |= (v ? 1u : 0u) << c;
+            for (int c = 0; c < 8; ++c) {
+              const int2 r = s_row[c0 + 8 * (c >> 1) + pair + (c & 1)];
+              const bool v = w == META_SHARED || (r.x == b && (d < 0 || ((static_cast<uint32_t>(r.y) >> d) & 1u)));
+              vis |= (v ? 1u : 0u) << (8 * k8 + c);
             }
           }
         }
-        const float visible = meta >= 0 && (meta & META_POISON) ? __int_as_float(0x7fc00000) : scale2;
         meta = load_meta(it + 1);
         const uint32_t sb = static_cast<uint32_t>(g & 1);
-        wait_warp(mbar(MB_S + sb), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
+        wait_own(mbar(MB_S + sb), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
         tc::fence_after_sync();
+        // x[16 hh + 4 i + 2 h + e]: key 8 (2 hh + h), row (i, e).
         const uint32_t s_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + TM_S + 128u * sb + c0;
         float x[32];
-        auto load_scores = [&]() {
-          tc::tmem_ld32f(s_addr, x);
-          tc::tmem_wait_ld();
-          if (vis == 0xffffffffu) {
+        tc::tmem_ld16x32f(s_addr, x);
+        tc::tmem_ld16x32f(s_addr + (16u << 16), x + 16);
+        tc::tmem_wait_ld();
+        float mul = scale2;   // still to be applied to x
+        if (!plain || scale2 < 0.f) {
+          mul = 1.f;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] *= visible;
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) x[c] = (vis >> c) & 1u ? x[c] * visible : -INFINITY;
+          for (int n = 0; n < 32; ++n) {
+            const int k8 = 2 * (n >> 4) + ((n >> 1) & 1), c = 2 * ((n >> 2) & 3) + (n & 1);
+            const float v = (poison >> k8) & 1u ? __int_as_float(0x7fc00000) : x[n] * scale2;
+            x[n] = plain || ((vis >> (8 * k8 + c)) & 1u) ? v : -INFINITY;
           }
-        };
-        load_scores();
-        transpose_reduce32<false>(x, lane);
+        }
+        float y[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const int n = 4 * (c >> 1) + (c & 1);
+          y[c] = fmaxf(fmaxf(x[n], x[n + 2]), fmaxf(x[n + 16], x[n + 18]));
+        }
+        const float wmax = mul * reduce_rows<false>(y, lane);
         // Every warp gives its 32 maxima to the group here and in the peer,
         // and takes the maximum of the eight itself.
-        s_red[sb * ROWS * 4 + (c0 + lane) * 4 + quad] = x[0];
-        tc::st_async_b32(xred_peer + sb * ROWS * 16, __float_as_uint(x[0]), peer_mbar(MB_X + sb));
+        s_red[sb * ROWS * 4 + row * 4 + quad] = wmax;
+        tc::st_async_b32(xred_peer + sb * ROWS * 16, __float_as_uint(wmax), peer_mbar(MB_X + sb));
         if (tid == 0) tc::mbar_arrive_expect(mbar(MB_X + sb), ROWS * 16);
-        load_scores();   // again, for P, while the peer's maxima arrive
         group_sync();
-        wait_warp(mbar(MB_X + sb), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
+        wait_peer(mbar(MB_X + sb), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
         float alpha = 1.f;
         {
-          const float4 o4 = *reinterpret_cast<const float4*>(s_red + sb * ROWS * 4 + (c0 + lane) * 4);
-          const float4 p4 = *reinterpret_cast<const float4*>(s_xred + sb * ROWS * 4 + (c0 + lane) * 4);
+          const float4 o4 = *reinterpret_cast<const float4*>(s_red + sb * ROWS * 4 + row * 4);
+          const float4 p4 = *reinterpret_cast<const float4*>(s_xred + sb * ROWS * 4 + row * 4);
           const float bm = fmaxf(fmaxf(fmaxf(o4.x, o4.y), fmaxf(o4.z, o4.w)), fmaxf(fmaxf(p4.x, p4.y), fmaxf(p4.z, p4.w)));
           if (bm > mrow) {
             if (mrow != -INFINITY) alpha = ex2(mrow - bm);
             mrow = bm;
           }
           // A fully masked row: p = ex2(-inf - 0) = 0.  (The group's warps
-          // write the same values.)
-          s_m[sb * ROWS + c0 + lane] = mrow == -INFINITY ? 0.f : mrow;
+          // write the same values; the other half of s_m is free until the
+          // group has met again.)
+          s_m[sb * ROWS + row] = mrow == -INFINITY ? 0.f : mrow;
+          s_m[(sb ^ 1u) * ROWS + row] = alpha;
         }
         __syncwarp();
-        // P^T for this key and the group's 32 rows, in fp16: weight 1 is
-        // exact, the others lose 2^-12 at most.
-        uint32_t pk[16];
+        // P^T in fp16: weight 1 is exact (the fused product is off by an ulp
+        // of the score at most), the others lose 2^-11 at most.
+        uint32_t pk[16];   // word 4 k8 + i: rows (i, 0) and (i, 1) of key 8 k8
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 m4 = *reinterpret_cast<const float4*>(s_m + sb * ROWS + c0 + 4 * q);
-          x[4 * q] = ex2(x[4 * q] - m4.x);
-          x[4 * q + 1] = ex2(x[4 * q + 1] - m4.y);
-          x[4 * q + 2] = ex2(x[4 * q + 2] - m4.z);
-          x[4 * q + 3] = ex2(x[4 * q + 3] - m4.w);
-          const __half2 lo = __floats2half2_rn(x[4 * q], x[4 * q + 1]), hi = __floats2half2_rn(x[4 * q + 2], x[4 * q + 3]);
-          pk[2 * q] = *reinterpret_cast<const uint32_t*>(&lo);
-          pk[2 * q + 1] = *reinterpret_cast<const uint32_t*>(&hi);
+        for (int i = 0; i < 4; ++i) {
+          const float2 m2 = *reinterpret_cast<const float2*>(s_m + sb * ROWS + c0 + 8 * i + pair);
+          y[2 * i] = y[2 * i + 1] = 0.f;
+#pragma unroll
+          for (int k8 = 0; k8 < 4; ++k8) {
+            const int n = 16 * (k8 >> 1) + 4 * i + 2 * (k8 & 1);
+            const float p0 = ex2(fmaf(x[n], mul, -m2.x)), p1 = ex2(fmaf(x[n + 1], mul, -m2.y));
+            y[2 * i] += p0;
+            y[2 * i + 1] += p1;
+            const __half2 hh = __floats2half2_rn(p0, p1);
+            pk[4 * k8 + i] = *reinterpret_cast<const uint32_t*>(&hh);
+          }
         }
-        // The step's row sums over this warp's 32 keys (lane l: row c0 + l).
-        transpose_reduce32<true>(x, lane);
-        lrun = lrun * alpha + x[0];
+        // The step's row sums over this warp's 32 keys.
+        lrun = lrun * alpha + reduce_rows<true>(y, lane);
         // O^T of the step before done: the P^T buffers (here and in the peer)
         // are free and O^T can be rescaled.  (A segment's first step: the
         // readout waited for it.)
         if (it > 0) {
-          wait_warp(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
+          wait_own(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
           tc::fence_after_sync();
-          const uint32_t moved_rows = __ballot_sync(0xffffffffu, alpha != 1.f);
-          if (moved_rows != 0) {
+          const uint32_t moved = __ballot_sync(0xffffffffu, alpha != 1.f);   // by lane
+          if (moved != 0) {
             const uint32_t lane_base = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c0;
-            const int cnt = __popc(moved_rows);
+            const int cnt = __popc(moved);
             if (cnt <= FEW_MOVED) {
-              uint32_t m = moved_rows;
+              uint32_t m = moved;
               for (int q = 0; q < cnt; ++q) {
-                const int c = __ffs(m) - 1;
+                const int l = __ffs(m) - 1;
                 m &= m - 1;
-                const float a = __shfl_sync(0xffffffffu, alpha, c);
+                const int c = __shfl_sync(0xffffffffu, row, l) - c0;
+                const float a = __shfl_sync(0xffffffffu, alpha, l);
                 const uint32_t v0 = tc::tmem_ld1(lane_base + c);
                 const uint32_t v1 = tc::tmem_ld1(lane_base + 128 + c);
                 tc::tmem_wait_ld();
@@ -522,27 +593,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                 tc::tmem_st1(lane_base + 128 + c, __float_as_uint(__uint_as_float(v1) * a));
               }
             } else {
+              const float* s_alpha = s_m + (sb ^ 1u) * ROWS + c0;
 #pragma unroll 1
               for (int t = 0; t < 2; ++t) {
                 uint32_t v[32];
                 tc::tmem_ld32(lane_base + 128u * t, v);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  v[c] = __float_as_uint(__uint_as_float(v[c]) * __shfl_sync(0xffffffffu, alpha, c));
+                for (int q = 0; q < 8; ++q) {
+                  const float4 a4 = *reinterpret_cast<const float4*>(s_alpha + 4 * q);
+                  v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) * a4.x);
+                  v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) * a4.y);
+                  v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) * a4.z);
+                  v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) * a4.w);
+                }
                 tc::tmem_st32(lane_base + 128u * t, v);
               }
             }
             tc::tmem_wait_st();
           }
         }
-        // Eight rows are one 16-byte granule of the key's swizzled row.
+        // Eight rows (one i) are a 16-byte granule of the key's swizzled row.
+        if (p_local) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t gran = static_cast<uint32_t>((((grp & 1) * 4 + q) ^ (j & 7)) << 4);
-          const uint4 v = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-          if (p_local) *reinterpret_cast<uint4*>(smem + p_off + gran) = v;
-          else tc::st_async_v4(p_peer + gran, v, peer_mbar(MB_PX));
+          for (int k8 = 0; k8 < 4; ++k8) tc::stmatrix4(p_matrix + k8 * 1024, pk + 4 * k8);
+        } else {
+          // Lane t takes row granule t % 4 of its key from the four lanes
+          // that hold its row pairs (a 4 x 4 transpose, four shuffles a key):
+          // four 16-byte stores went out in half the time of sixteen words.
+          const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+          for (int k8 = 0; k8 < 4; ++k8) {
+            const uint32_t* w = pk + 4 * k8;
+            const uint32_t r01 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1);
+            const uint32_t r23 = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+            const uint32_t u0 = odd ? r01 : w[0], u1 = odd ? w[1] : r01, v0 = odd ? r23 : w[2], v1 = odd ? w[3] : r23;
+            const uint32_t g0 = __shfl_xor_sync(0xffffffffu, high ? u0 : v0, 2);
+            const uint32_t g1 = __shfl_xor_sync(0xffffffffu, high ? u1 : v1, 2);
+            tc::st_async_v4(p_peer + k8 * 1024, high ? make_uint4(g0, g1, v0, v1) : make_uint4(u0, u1, g0, g1), peer_mbar(MB_PX));
+          }
         }
         if (p_local) tc::fence_async_smem();   // (the peer's MMA warp fences the st.async bytes)
         tc::fence_before_sync();
@@ -551,22 +640,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       }
       // ---- the segment's end: row sums over the group's warps, then the peer's
       const int eb = (g & 1) * ROWS;   // the halves of s_red and s_m that the last step did not use
-      s_red[(eb + c0 + lane) * 4 + quad] = lrun;
+      s_red[(eb + row) * 4 + quad] = lrun;
       group_sync();
       float* s_l = s_m + eb;
       const size_t part0 = static_cast<size_t>(part_slot(cluster, s.first)) * ROWS;
       if (quad == 0) {
-        const float4 q4 = *reinterpret_cast<const float4*>(s_red + (eb + c0 + lane) * 4);
+        const float4 q4 = *reinterpret_cast<const float4*>(s_red + (eb + row) * 4);
         const float ls = (q4.x + q4.y) + (q4.z + q4.w);
-        tc::st_async_b32(tc::peer_addr(sbase + OFF_XSUM + (c0 + lane) * 4, peer), __float_as_uint(ls), peer_mbar(MB_XS));
+        tc::st_async_b32(tc::peer_addr(sbase + OFF_XSUM + row * 4, peer), __float_as_uint(ls), peer_mbar(MB_XS));
         if (tid == 0) tc::mbar_arrive_expect(mbar(MB_XS), ROWS * 4);
-        wait_phase(mbar(MB_XS), static_cast<uint32_t>(k & 1), s_abort, p.err);
-        __syncwarp();
+        wait_peer(mbar(MB_XS), static_cast<uint32_t>(k & 1), s_abort, p.err);
         // Both CTAs add the two halves in the same order.
-        const float lo = rank == 0 ? ls : s_xsum[c0 + lane];
-        const float hi = rank == 0 ? s_xsum[c0 + lane] : ls;
+        const float lo = rank == 0 ? ls : s_xsum[row];
+        const float hi = rank == 0 ? s_xsum[row] : ls;
         const float l = lo + hi;
-        const int r = c0 + lane;
+        const int r = row;
         const float nan = __int_as_float(0x7fc00000);
         // A row that is not served, or saw a value outside fp16: NaN.
         const bool lost = l != l || s_row[r].x < 0;
@@ -580,7 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       group_sync();
       // ---- O^T out of TMEM; thread = value dim, each warp store 32
       // consecutive dims of a row.
-      wait_warp(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
+      wait_own(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
       tc::fence_after_sync();
       const int rows = s.t.nrows - c0;
       const size_t out0 = (s.whole ? static_cast<size_t>(s.t.q_row0) : part0) + c0;

@@ -126,6 +126,22 @@ __device__ __forceinline__ void tmem_ld32f(uint32_t taddr, float (&r)[32]) {
         "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
+// 16 lanes x 32 columns, spread as MMA accumulators are: thread t gets, in
+// r[4i + 2h + e], lane t / 4 + 8h and column 8i + 2 (t % 4) + e (i < 4).
+__device__ __forceinline__ void tmem_ld16x32f(uint32_t taddr, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]), "=f"(r[8]),
+        "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+      : "r"(taddr));
+}
+// Four 8x8 matrices of 16-bit values from that spread: matrix k is word r[k]
+// of every thread; lane l gives the address of row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t* r) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};\n" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 // One TMEM column for the warp's 32 lanes.
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -269,6 +285,22 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t mbar, uint32_t parity)
       : "r"(mbar), "r"(parity)
       : "memory");
   return ok != 0;
+}
+// The same without the acquire, and an acquire fence at cluster scope for
+// shared memory alone.  An unrestricted acquire at cluster scope also drops
+// the SM's L1 lines.
+__device__ __forceinline__ bool mbar_try_cluster_relaxed(uint32_t mbar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p;\nmbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n"
+      "selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(mbar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void fence_acquire_shared_cluster() {
+  asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;\n" ::: "memory");
 }
 // Generic-proxy writes to this CTA's or the peer's shared memory become
 // visible to the tensor core.
