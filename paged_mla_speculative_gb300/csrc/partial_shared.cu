@@ -100,19 +100,21 @@ constexpr int FEW_MOVED = 4;
 // (pair_common.cuh's waits acquire all memory at cluster scope, which drops
 // the SM's L1 lines, spilled registers among them, every step.)
 template <bool PEER>
-__device__ __forceinline__ void wait_bounded(uint32_t mbar, uint32_t parity, volatile int* abort, int* err) {
-  auto done = [&]() { return PEER ? tc::mbar_try_cluster_relaxed(mbar, parity) : tc::mbar_try(mbar, parity); };
-  if (!done()) {
-    const long long t0 = clock64();
-    while (!done()) {
-      if (*abort) break;
-      if (clock64() - t0 > WAIT_LIMIT) {
-        *abort = 1;
-        atomicOr(err, ERR_TIMEOUT);
-        break;
-      }
+__device__ __noinline__ void wait_longer(uint32_t mbar, uint32_t parity, volatile int* abort, int* err) {
+  const long long t0 = clock64();
+  while (!(PEER ? tc::mbar_try_cluster_relaxed(mbar, parity) : tc::mbar_try(mbar, parity))) {
+    if (*abort) return;
+    if (clock64() - t0 > WAIT_LIMIT) {
+      *abort = 1;
+      atomicOr(err, ERR_TIMEOUT);
+      return;
     }
   }
+}
+template <bool PEER>
+__device__ __forceinline__ void wait_bounded(uint32_t mbar, uint32_t parity, volatile int* abort, int* err) {
+  if (!(PEER ? tc::mbar_try_cluster_relaxed(mbar, parity) : tc::mbar_try(mbar, parity)))
+    wait_longer<PEER>(mbar, parity, abort, err);
   if (PEER) tc::fence_acquire_shared_cluster();
   __syncwarp();
 }
@@ -484,8 +486,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         // Decided while S^T is computed: do all rows see all of the warp's
         // keys?  If not, which: bit 8k + 2i + e for key k and row (i, e).
         const bool plain = __all_sync(0xffffffffu, meta == META_SHARED);
-        uint32_t vis = 0, poison = 0;
+        uint32_t vis = 0xffffffffu, poison = 0;
         if (!plain) {
+          vis = 0;
 #pragma unroll 1
           for (int k8 = 0; k8 < 4; ++k8) {
             const int m = __shfl_sync(0xffffffffu, meta, key + 8 * k8);
@@ -514,10 +517,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         if (!plain || scale2 < 0.f) {
           mul = 1.f;
 #pragma unroll
-          for (int n = 0; n < 32; ++n) {
-            const int k8 = 2 * (n >> 4) + ((n >> 1) & 1), c = 2 * ((n >> 2) & 3) + (n & 1);
-            const float v = (poison >> k8) & 1u ? __int_as_float(0x7fc00000) : x[n] * scale2;
-            x[n] = plain || ((vis >> (8 * k8 + c)) & 1u) ? v : -INFINITY;
+          for (int k8 = 0; k8 < 4; ++k8) {
+            const float f = (poison >> k8) & 1u ? __int_as_float(0x7fc00000) : scale2;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              float& v = x[16 * (k8 >> 1) + 4 * (c >> 1) + 2 * (k8 & 1) + (c & 1)];
+              v = (vis >> (8 * k8 + c)) & 1u ? v * f : -INFINITY;
+            }
           }
         }
         float y[8];
@@ -595,19 +601,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             } else {
               const float* s_alpha = s_m + (sb ^ 1u) * ROWS + c0;
 #pragma unroll 1
-              for (int t = 0; t < 2; ++t) {
-                uint32_t v[32];
-                tc::tmem_ld32(lane_base + 128u * t, v);
+              for (int t = 0; t < 4; ++t) {   // 16 columns at a time
+                const uint32_t at = lane_base + 128u * (t >> 1) + 16u * (t & 1);
+                uint32_t v[16];
+                tc::tmem_ld16(at, v);
                 tc::tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                  const float4 a4 = *reinterpret_cast<const float4*>(s_alpha + 4 * q);
+                for (int q = 0; q < 4; ++q) {
+                  const float4 a4 = *reinterpret_cast<const float4*>(s_alpha + 16 * (t & 1) + 4 * q);
                   v[4 * q] = __float_as_uint(__uint_as_float(v[4 * q]) * a4.x);
                   v[4 * q + 1] = __float_as_uint(__uint_as_float(v[4 * q + 1]) * a4.y);
                   v[4 * q + 2] = __float_as_uint(__uint_as_float(v[4 * q + 2]) * a4.z);
                   v[4 * q + 3] = __float_as_uint(__uint_as_float(v[4 * q + 3]) * a4.w);
                 }
-                tc::tmem_st32(lane_base + 128u * t, v);
+                tc::tmem_st16(at, v);
               }
             }
             tc::tmem_wait_st();
