@@ -99,7 +99,7 @@ double fixed_us(int kernel) { return kernel == MLA_VERIFY_KERNEL_PAIR ? 20.0 : 1
 long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Clusters of the shared-prefix attention kernel: one per SM pair.
-int shared_clusters(const mla_verify_plan* pl) { return pl->num_sms / 2; }
+int shared_clusters(const mla_verify_plan* pl) { return std::min(pl->num_sms / 2, mlav::SH_MAX_CLUSTERS); }
 
 // The layout arrays of a shared-prefix call, one after another in the plan's
 // sh_layout; returns the 32-bit words they take.

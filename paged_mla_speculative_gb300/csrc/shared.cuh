@@ -29,6 +29,7 @@ constexpr int META_POISON = 1 << 30;       // holds a value outside fp16: rows t
 // own key of request b: draft -1 for a key before the drafts
 __host__ __device__ constexpr int meta_own(int b, int draft) { return b * 64 + 2 + draft; }
 constexpr int SH_MAX_BATCH = 1 << 24;
+constexpr int SH_MAX_CLUSTERS = 128;   // of the attention kernel (an SM pair each)
 
 struct SharedTile {
   int q_row0, nrows;        // query rows

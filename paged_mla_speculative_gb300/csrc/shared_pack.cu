@@ -1,7 +1,7 @@
 // Preparation of the shared-prefix verify attention, and the merge after it.
 //
 // shared_prepare_kernel, three jobs side by side:
-//  * CTA 0 lays out the call on the device (lengths are device data): which
+//  * CTA 0 (and 1, the ancestor masks) lays out the call on the device (lengths are device data): which
 //    requests can be served, each group's shared range and each request's own
 //    range in the packed key space, the query-row tiles, and the division of
 //    all tiles' steps over the attention kernel's clusters, even to a step, so
@@ -71,6 +71,7 @@ __device__ __forceinline__ int last_not_above(const int* a, int n, int x) {
 // no request is served.
 struct Groups {
   const int32_t* indptr;
+  const int32_t* shared_lens;
   int n, batch;
   bool ok;
   __device__ __forceinline__ int begin(int g) const { return ok ? indptr[g] : (g ? batch : 0); }
@@ -79,23 +80,35 @@ struct Groups {
 
 // Own rows, packed bases and each group's source request, by the whole CTA;
 // returns the packed keys.  `report`: set the error bits of what cannot be served.
-__device__ __forceinline__ int scan_requests(const SharedParams& p, int* own, int* base, int* source, int* s_warp, Groups& grp,
-                                             bool report) {
+// `indptr` and `lens`: copies of the groups' arrays to keep using, or the
+// arrays themselves.  (Beside the packers' loads a dependent load takes up to
+// 2 us: a small call makes one round of them and goes on in shared memory.)
+__device__ __forceinline__ int scan_requests(const SharedParams& p, int* own, int* base, int* source, int* indptr, int* lens,
+                                             int* s_warp, Groups& grp, bool report) {
   const int tid = threadIdx.x, B = p.batch;
   bool bad = false;
+  // The first round's loads go out before the groups are known.
+  int n = 0, ip0 = 0, ip1 = 0;
+  const int ipn = p.kv_indptr[B];
+  if (tid < B) n = p.kv_lens[tid], ip0 = p.kv_indptr[tid], ip1 = p.kv_indptr[tid + 1];
   for (int g = tid; g < p.groups; g += THREADS) {
-    bad |= p.group_indptr[g + 1] < p.group_indptr[g];
+    const int a = p.group_indptr[g], z = p.group_indptr[g + 1];
+    bad |= z < a || (g == 0 && a != 0) || (g == p.groups - 1 && z != B);
     source[g] = INT_MAX;
+    if (indptr) {
+      indptr[g] = a;
+      lens[g] = p.shared_lens[g];
+      if (g == p.groups - 1) indptr[g + 1] = z;
+    }
   }
-  bad |= p.group_indptr[0] != 0 || p.group_indptr[p.groups] != B;
   const bool groups_ok = __syncthreads_or(bad) == 0;
-  grp = Groups{p.group_indptr, groups_ok ? p.groups : 1, B, groups_ok};
+  grp = Groups{indptr ? indptr : p.group_indptr, indptr ? lens : p.shared_lens, groups_ok ? p.groups : 1, B, groups_ok};
   int errs = groups_ok ? 0 : ERR_INDPTR;
   for (int b = tid; b < B; b += THREADS) {
     const int g = grp.of(b);
-    const int n = p.kv_lens[b], ip0 = p.kv_indptr[b], ip1 = p.kv_indptr[b + 1], ipn = p.kv_indptr[B];
+    if (b >= THREADS) n = p.kv_lens[b], ip0 = p.kv_indptr[b], ip1 = p.kv_indptr[b + 1];
     const long long need = p.page_size == 1 ? n : (static_cast<long long>(n) + PAGE - 1) / PAGE;
-    const int S = groups_ok ? p.shared_lens[g] : 0;
+    const int S = groups_ok ? grp.shared_lens[g] : 0;
     const bool len_ok = n >= p.T && n <= p.max_kv_len && S >= 0 && S <= n - p.T;
     const bool ptr_ok = ip0 >= 0 && ip1 >= ip0 && ip1 <= ipn && static_cast<long long>(ip1) - ip0 == need;
     const bool ok = groups_ok && len_ok && ptr_ok;
@@ -113,7 +126,7 @@ __device__ __forceinline__ int scan_requests(const SharedParams& p, int* own, in
     if (b < B) {
       const int g = grp.of(b);
       mine = own[b];
-      if (b == grp.begin(g) && *static_cast<volatile int*>(source + g) != INT_MAX) prefix = p.shared_lens[g];
+      if (b == grp.begin(g) && *static_cast<volatile int*>(source + g) != INT_MAX) prefix = grp.shared_lens[g];
     }
     int all;
     const int end = before + block_scan(prefix + mine, s_warp, all);
@@ -129,12 +142,33 @@ __device__ __forceinline__ int scan_requests(const SharedParams& p, int* own, in
 }
 
 struct Layout {
-  int own[SMALL], base[2 * SMALL + 1], source[SMALL];
+  int own[SMALL], base[2 * SMALL + 1], source[SMALL], indptr[SMALL + 1], lens[SMALL];
 };
 struct PlanLayout {
   Layout l;
   int tile0[SMALL], cost[SMALL + 1];
+  SharedTile tiles[SMALL];
+  SharedPos start[SH_MAX_CLUSTERS + 1];
 };
+
+// CTA 1.  Ancestor masks: a warp holds a request's parents and walks them by
+// shuffles (walking them in global memory took a load per level).
+__device__ __forceinline__ void plan_ancestors(const SharedParams& p) {
+  const int lane = threadIdx.x & 31;
+  for (int b = threadIdx.x >> 5; b < p.batch; b += THREADS / 32) {
+    const int par = lane < p.T ? p.draft_parent[static_cast<size_t>(b) * p.T + lane] : -1;
+    if (par < -1 || par >= lane + (lane < p.T ? 0 : 1)) atomicOr(p.err, ERR_PARENT);
+    const int up = par >= lane ? -1 : par;
+    uint32_t mask = 1u << lane;
+    int cur = up;
+    for (int it = 1; it < p.T; ++it) {
+      if (cur >= 0) mask |= 1u << cur;
+      const int next = __shfl_sync(0xffffffffu, up, max(cur, 0));
+      cur = cur >= 0 ? next : -1;
+    }
+    if (lane < p.T) p.anc[static_cast<size_t>(b) * p.T + lane] = mask;
+  }
+}
 
 // CTA 0.  Arrays that others read go to the workspace; the ones used here
 // only, and those of a small call, are in shared memory.
@@ -145,9 +179,8 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
   int* own = small ? s.l.own : p.own;
   int* base = small ? s.l.base : p.base;
   Groups grp;
-  const int keys = scan_requests(p, own, base, small ? s.l.source : p.source, s_warp, grp, true);
-  for (int i = tid; i < B * p.T; i += THREADS)
-    p.anc[i] = ancestor_mask(p.draft_parent + static_cast<size_t>(i / p.T) * p.T, i % p.T, p.err);
+  const int keys = scan_requests(p, own, base, small ? s.l.source : p.source, small ? s.l.indptr : nullptr, s.l.lens, s_warp, grp,
+                                 true);
   if (small)
     for (int b = tid; b < B; b += THREADS) p.own[b] = own[b];
   // Tiles of each group.
@@ -170,6 +203,7 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
   __syncthreads();
   // Tile records and the prefix sum of their costs.
   int* cost = tiles <= SMALL ? s.cost : p.cost;
+  SharedTile* recs = tiles <= SMALL ? s.tiles : p.tiles;
   int total = 0, most = 0;
   for (int t0 = 0; t0 < tiles; t0 += THREADS) {
     const int t = t0 + tid;
@@ -187,7 +221,7 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
       rec.own_len = base[2 * b1 + 1] + own[b1] - rec.own_base;
       if (rec.own_len > 0) {       // some request of the tile is served
         rec.prefix_base = base[2 * grp.begin(g)];
-        rec.prefix_len = p.shared_lens[g];
+        rec.prefix_len = grp.shared_lens[g];
         rec.halves = prefix_halves(rec) + (rec.own_len + SH_HALF - 1) / SH_HALF;
         rec.steps = (rec.halves + 1) / 2;
         c = rec.steps + SH_SEGMENT_COST;
@@ -197,7 +231,7 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
     int all;
     const int end = total + block_scan(c, s_warp, all);
     if (t < tiles) {
-      p.tiles[t] = rec;
+      recs[t] = rec;
       cost[t] = end - c;
     }
     total += all;
@@ -214,7 +248,7 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
   int used = max(1, min(p.clusters, total / (SH_SEGMENT_COST + 2)));
   const bool whole = tiles <= p.clusters && s_max <= total / p.clusters + SH_SEGMENT_COST + SH_JOIN_COST;
   if (whole) used = tiles;
-  auto start = [&](int c) {
+  for (int c = tid; c <= p.clusters; c += THREADS) {
     SharedPos at{tiles, 0};
     if (whole) {
       at.tile = min(c, tiles);
@@ -223,61 +257,68 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
       at.tile = last_not_above(cost, tiles, x);
       at.step = max(0, x - cost[at.tile] - SH_SEGMENT_COST);
     }
-    return at;
-  };
+    s.start[c] = at;
+  }
+  __syncthreads();
   for (int c = tid; c < p.clusters; c += THREADS) {
     SharedShare sh{};
-    sh.from = start(c);
-    sh.to = start(c + 1);
-    if (sh.from.tile < tiles) sh.first = p.tiles[sh.from.tile];
+    sh.from = s.start[c];
+    sh.to = s.start[c + 1];
+    if (sh.from.tile < tiles) sh.first = recs[sh.from.tile];
     p.share[c] = sh;
   }
   // Which clusters hold each tile.
   for (int t = tid; t < tiles; t += THREADS) {
     const int c = cost[t + 1] - cost[t];
-    if (c == 0) continue;
-    // Last cluster that starts at or before step `step` of the tile.
-    auto last_before = [&](int step) {
-      int lo = 0, hi = used;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        const SharedPos at = start(mid);
-        if (at.tile < t || (at.tile == t && at.step <= step)) lo = mid;
-        else hi = mid;
-      }
-      return lo;
-    };
-    const int a = last_before(0), z = last_before(c - SH_SEGMENT_COST - 1);
-    p.tiles[t].seg0 = a;
-    p.tiles[t].nseg = z - a + 1;
+    SharedTile rec = recs[t];
+    if (c > 0) {
+      // Last cluster that starts at or before step `step` of the tile.
+      auto last_before = [&](int step) {
+        int lo = 0, hi = used;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          const SharedPos at = s.start[mid];
+          if (at.tile < t || (at.tile == t && at.step <= step)) lo = mid;
+          else hi = mid;
+        }
+        return lo;
+      };
+      rec.seg0 = whole ? t : last_before(0);
+      rec.nseg = whole ? 1 : last_before(c - SH_SEGMENT_COST - 1) - rec.seg0 + 1;
+    }
+    p.tiles[t] = rec;
   }
 }
 
-// 32 rows of a 576-wide bf16 array, row r at src + s_row[r] * 576 (negative:
-// zeros), widened into the planes at plane rows row0 .. row0 + rows - 1.  A
-// value outside fp16 is packed as zero and sets s_bad of its row; returns
-// whether this thread met one.
-__device__ __forceinline__ bool pack_rows(const uint16_t* src, const long long* s_row, int* s_bad, uint16_t* dst,
-                                          long long plane, long long row0, int rows) {
+struct Rows {
   uint4 v[PER_THREAD];
+};
+// Row r of 32 (each THREADS / 8 granules apart) at src + s_row[r] * 576, or
+// zeros where s_row is negative.
+__device__ __forceinline__ void load_rows(const uint16_t* src, const long long* s_row, Rows& x) {
 #pragma unroll
   for (int u = 0; u < PER_THREAD; ++u) {
     const int e = threadIdx.x + u * THREADS;
     const int r = e / ROW_CHUNKS, c = e - r * ROW_CHUNKS;
     const long long row = s_row[r];
-    v[u] = make_uint4(0, 0, 0, 0);
+    x.v[u] = make_uint4(0, 0, 0, 0);
     if (row >= 0)
       asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                   : "=r"(v[u].x), "=r"(v[u].y), "=r"(v[u].z), "=r"(v[u].w)
+                   : "=r"(x.v[u].x), "=r"(x.v[u].y), "=r"(x.v[u].z), "=r"(x.v[u].w)
                    : "l"(reinterpret_cast<const uint4*>(src + row * D_QK) + c));
   }
+}
+// Widened into the planes at plane rows row0 .. row0 + rows - 1.  A value
+// outside fp16 is packed as zero and sets s_bad of its row; returns whether
+// this thread met one.
+__device__ __forceinline__ bool store_rows(const Rows& x, int* s_bad, uint16_t* dst, long long plane, long long row0, int rows) {
   bool any = false;
 #pragma unroll
   for (int u = 0; u < PER_THREAD; ++u) {
     const int e = threadIdx.x + u * THREADS;
     const int r = e / ROW_CHUNKS, c = e - r * ROW_CHUNKS;
     bool bad = false;
-    uint4 w = widen_bf16x8(v[u], bad);
+    uint4 w = widen_bf16x8(x.v[u], bad);
     if (bad) {
       any = true;
       s_bad[r] = 1;
@@ -295,18 +336,19 @@ __device__ __forceinline__ bool pack_rows(const uint16_t* src, const long long* 
 }
 
 // `packers` CTAs (the last of the grid) gather keys, those before them widen
-// queries, CTA 0 plans; each job's CTAs may be none.
+// queries, the first `plans` (2 or 0) lay out the call.
 __global__ void __launch_bounds__(THREADS, 4) shared_prepare_kernel(const SharedParams p, int plans, int packers) {
   __shared__ PlanLayout s;
   __shared__ int s_warp[THREADS / 32];
-  __shared__ long long s_row[PACK_KEYS];
-  __shared__ int s_meta[PACK_KEYS], s_bad[PACK_KEYS];
+  __shared__ long long s_row[2][PACK_KEYS];
+  __shared__ int s_meta[2][PACK_KEYS], s_bad[2][PACK_KEYS];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const bool small = p.batch <= SMALL && p.groups <= SMALL;
   const int tid = threadIdx.x;
   if (static_cast<int>(blockIdx.x) < plans) {
-    plan_call(p, s, small, s_warp);
+    if (blockIdx.x == 0) plan_call(p, s, small, s_warp);
+    else plan_ancestors(p);
     return;
   }
   const int packer = static_cast<int>(blockIdx.x) - (static_cast<int>(gridDim.x) - packers);
@@ -337,48 +379,55 @@ __global__ void __launch_bounds__(THREADS, 4) shared_prepare_kernel(const Shared
   int total;
   Groups grp;
   if (small) {
-    total = scan_requests(p, s.l.own, s.l.base, s.l.source, s_warp, grp, false);
+    total = scan_requests(p, s.l.own, s.l.base, s.l.source, s.l.indptr, s.l.lens, s_warp, grp, false);
   } else {
     total = p.totals[0];
-    grp = Groups{p.group_indptr, p.groups, p.batch, true};   // (no key of a group that is none is packed)
+    grp = Groups{p.group_indptr, p.shared_lens, p.groups, p.batch, true};   // (no key of a group that is none is packed)
   }
   const int* own = small ? s.l.own : p.own;
   const int* base = small ? s.l.base : p.base;
   const int* source = small ? s.l.source : p.source;
   const int chunks = (total + SH_TAIL + PACK_KEYS - 1) / PACK_KEYS;
-  for (int chunk = packer; chunk < chunks; chunk += packers) {
-    const int key0 = chunk * PACK_KEYS, rows = min(PACK_KEYS, total + SH_TAIL - key0);
-    if (tid < PACK_KEYS) {
-      const int key = key0 + tid;
-      long long row = -1;
-      int meta = META_MASKED;
-      if (key < total) {
-        const int part = last_not_above(base, 2 * p.batch, key);
-        int b = part >> 1, j = key - base[part];
-        if (part & 1) {
-          const int n = p.kv_lens[b];
-          j += n - own[b];                            // behind the shared rows
-          meta = meta_own(b, max(-1, j - (n - p.T)));
-        } else {
-          b = source[grp.of(b)];
-          meta = META_SHARED;
-        }
-        const long long entry = p.kv_indices[p.kv_indptr[b] + (p.page_size == 1 ? j : j / PAGE)];
-        row = p.page_size == 1 ? entry : entry * PAGE + j % PAGE;
-        if (entry < 0 || row >= p.num_slots) {
-          atomicOr(p.err, ERR_SLOT);
-          row = -1;
-          meta = META_MASKED;
-        }
+  // The slot and meta word of each key of a chunk, by the first warp.
+  auto look_up = [&](int chunk, int buf) {
+    if (tid >= PACK_KEYS) return;
+    const int key = chunk * PACK_KEYS + tid;
+    long long row = -1;
+    int meta = META_MASKED;
+    if (key < total) {
+      const int part = last_not_above(base, 2 * p.batch, key);
+      int b = part >> 1, j = key - base[part];
+      if (part & 1) {
+        const int n = p.kv_lens[b];
+        j += n - own[b];                            // behind the shared rows
+        meta = meta_own(b, max(-1, j - (n - p.T)));
+      } else {
+        b = source[grp.of(b)];
+        meta = META_SHARED;
       }
-      s_row[tid] = row;
-      s_meta[tid] = meta;
-      s_bad[tid] = 0;
+      const long long entry = p.kv_indices[p.kv_indptr[b] + (p.page_size == 1 ? j : j / PAGE)];
+      row = p.page_size == 1 ? entry : entry * PAGE + j % PAGE;
+      if (entry < 0 || row >= p.num_slots) {
+        atomicOr(p.err, ERR_SLOT);
+        row = -1;
+        meta = META_MASKED;
+      }
     }
+    s_row[buf][tid] = row;
+    s_meta[buf][tid] = meta;
+    s_bad[buf][tid] = 0;
+  };
+  int buf = 0;
+  if (packer < chunks) look_up(packer, 0);
+  __syncthreads();
+  for (int chunk = packer; chunk < chunks; chunk += packers, buf ^= 1) {
+    const int key0 = chunk * PACK_KEYS, rows = min(PACK_KEYS, total + SH_TAIL - key0);
+    Rows x;
+    load_rows(p.kv, s_row[buf], x);
+    if (chunk + packers < chunks) look_up(chunk + packers, buf ^ 1);   // while the rows arrive
+    report_range(store_rows(x, s_bad[buf], p.k16, p.k_plane, key0, rows), p.err);
     __syncthreads();
-    report_range(pack_rows(p.kv, s_row, s_bad, p.k16, p.k_plane, key0, rows), p.err);
-    __syncthreads();
-    if (tid < rows) p.meta[key0 + tid] = s_meta[tid] | (s_bad[tid] ? META_POISON : 0);
+    if (tid < rows) p.meta[key0 + tid] = s_meta[buf][tid] | (s_bad[buf][tid] ? META_POISON : 0);
   }
 }
 
@@ -388,7 +437,7 @@ __global__ void __launch_bounds__(THREADS, 4) shared_prepare_kernel(const Shared
 // written and mostly come from L2; the launch and one round trip are the time.
 constexpr int JOIN_ROWS = 2;
 constexpr int JOIN_FLIGHT = 8;
-constexpr int JOIN_MAX = 4;    // parts per lane: clusters <= 32 * JOIN_MAX
+constexpr int JOIN_MAX = SH_MAX_CLUSTERS / 32;   // parts per lane
 
 __global__ void __launch_bounds__(JOIN_ROWS * 128) shared_join_kernel(const SharedParams p) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -482,18 +531,21 @@ cudaError_t launch(void (*kernel)(Args...), long long grid, unsigned block, cuda
 }  // namespace
 
 cudaError_t launch_shared_prepare(const SharedParams& p, int num_sms, cudaStream_t stream) {
+  if (p.clusters > SH_MAX_CLUSTERS) return cudaErrorInvalidValue;
   const long long rows = static_cast<long long>(p.batch) * p.R;
   const long long query_ctas = (rows + PACK_KEYS - 1) / PACK_KEYS;
   const long long most = static_cast<long long>(p.batch) * p.max_kv_len + SH_TAIL;
-  const int packers = static_cast<int>(std::min<long long>((most + PACK_KEYS - 1) / PACK_KEYS, 4LL * num_sms));
+  // Packers: what the query CTAs leave of one resident wave (four CTAs per
+  // SM), so that none starts when the others are done.
+  const long long wave = std::max(2LL * num_sms, 4LL * num_sms - 2 - query_ctas);
+  const int packers = static_cast<int>(std::min<long long>((most + PACK_KEYS - 1) / PACK_KEYS, wave));
   if (p.batch <= SMALL && p.groups <= SMALL)
-    return launch(shared_prepare_kernel, 1 + query_ctas + packers, THREADS, stream, false, p, 1, packers);
-  const cudaError_t e = launch(shared_prepare_kernel, 1 + query_ctas, THREADS, stream, false, p, 1, 0);
+    return launch(shared_prepare_kernel, 2 + query_ctas + packers, THREADS, stream, false, p, 2, packers);
+  const cudaError_t e = launch(shared_prepare_kernel, 2 + query_ctas, THREADS, stream, false, p, 2, 0);
   return e != cudaSuccess ? e : launch(shared_prepare_kernel, packers, THREADS, stream, true, p, 0, packers);
 }
 
 cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream) {
-  if (p.clusters > 32 * JOIN_MAX) return cudaErrorInvalidValue;
   return launch(shared_join_kernel, static_cast<long long>(p.max_tiles) * (SH_ROWS / JOIN_ROWS), JOIN_ROWS * 128, stream, true, p);
 }
 
