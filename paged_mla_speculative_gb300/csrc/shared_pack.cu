@@ -540,8 +540,8 @@ cudaError_t launch_shared_prepare(const SharedParams& p, int num_sms, cudaStream
   const long long wave = std::max(2LL * num_sms, 4LL * num_sms - 2 - query_ctas);
   const int packers = static_cast<int>(std::min<long long>((most + PACK_KEYS - 1) / PACK_KEYS, wave));
   if (p.batch <= SMALL && p.groups <= SMALL)
-    return launch(shared_prepare_kernel, 2 + query_ctas + packers, THREADS, stream, false, p, 2, packers);
-  const cudaError_t e = launch(shared_prepare_kernel, 2 + query_ctas, THREADS, stream, false, p, 2, 0);
+    return launch(shared_prepare_kernel, 2 + query_ctas + packers, THREADS, stream, true, p, 2, packers);
+  const cudaError_t e = launch(shared_prepare_kernel, 2 + query_ctas, THREADS, stream, true, p, 2, 0);
   return e != cudaSuccess ? e : launch(shared_prepare_kernel, packers, THREADS, stream, true, p, 0, packers);
 }
 
