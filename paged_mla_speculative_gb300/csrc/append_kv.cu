@@ -40,7 +40,8 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-// Granules read once by the whole call.
+// Granules read once by the whole call.  (Volatile, like the plain loads of
+// the rest: a read-only load could be moved above griddepcontrol.wait.)
 __device__ __forceinline__ uint4 load_once(const uint4* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
@@ -58,8 +59,8 @@ __device__ __forceinline__ Angles load_angles(const float* row, int g, bool halv
   Angles a;
   const float4* cs = reinterpret_cast<const float4*>(row);
   const int i = halves ? 2 * (g & 3) : g;
-  const float4 c0 = __ldg(cs + i), s0 = __ldg(cs + 8 + i);
-  const float4 c1 = halves ? __ldg(cs + i + 1) : c0, s1 = halves ? __ldg(cs + 8 + i + 1) : s0;
+  const float4 c0 = cs[i], s0 = cs[8 + i];
+  const float4 c1 = halves ? cs[i + 1] : c0, s1 = halves ? cs[8 + i + 1] : s0;
   a.c[0] = c0.x, a.c[1] = c0.y, a.c[2] = c0.z, a.c[3] = c0.w;
   a.c[4] = c1.x, a.c[5] = c1.y, a.c[6] = c1.z, a.c[7] = c1.w;
   a.s[0] = s0.x, a.s[1] = s0.y, a.s[2] = s0.z, a.s[3] = s0.w;
@@ -91,6 +92,7 @@ __device__ __forceinline__ uint4 rotate(uint4 v, const Angles& a, int g, bool ha
 }
 
 __global__ void __launch_bounds__(THREADS) append_kv_kernel(const AppendArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
   const int lane = threadIdx.x & 31, g = lane & 7;
   const int head_items = a.q_pe ? (a.heads + HEADS - 1) / HEADS : 0;
   const long long item = static_cast<long long>(blockIdx.x) * (THREADS / 32) + (threadIdx.x >> 5);
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(THREADS) append_kv_kernel(const AppendArgs a) 
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       x[u] = load_once(src + lane + 32 * u);
-      w[u] = __ldg(wsrc + lane + 32 * u);
+      w[u] = wsrc[lane + 32 * u];
     }
     if (lane < 8) r = load_once(src + NOPE_GRANULES + lane);
     const Angles ang = load_angles(a.cos_sin + pos * DR, g, halves);
@@ -176,8 +178,7 @@ cudaError_t launch_append_kv(const AppendArgs& a, cudaStream_t stream) {
   const long long items = a.num_tokens * (a.q_pe ? (a.heads + HEADS - 1) / HEADS + 1 : 1);
   const long long ctas = (items + THREADS / 32 - 1) / (THREADS / 32);
   if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-  append_kv_kernel<<<static_cast<unsigned>(ctas), THREADS, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_overlapping(append_kv_kernel, dim3(static_cast<unsigned>(ctas)), THREADS, 0, stream, 1, a);
 }
 
 }  // namespace mlav

@@ -9,6 +9,28 @@
 
 namespace mlav {
 
+// Launch with programmatic overlap: the kernel may
+// start while the one before it on the stream ends, and waits for it with
+// griddepcontrol.wait before it touches memory.  cluster: CTAs per cluster.
+template <typename... Args>
+cudaError_t launch_overlapping(void (*kernel)(Args...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
+                               unsigned cluster, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Split-KV partial kernel on warp-level mma.sync.
 int partial_mma_smem_bytes();
 cudaError_t partial_mma_prepare();

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
   __shared__ Child s_child;
   __shared__ unsigned long long s_last[2];
   __shared__ __align__(8) uint64_t s_mbar[2];
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
   const int c = blockIdx.y, tid = threadIdx.x;
   const long long left = max(0, min(*a.free_count, a.num_pages));
   if (tid < 2) s_last[tid] = 0;
@@ -261,6 +262,7 @@ constexpr int FREE_THREADS = 1024;
 constexpr int FREE_MAX_CTAS = 8;
 
 __global__ void __launch_bounds__(FREE_THREADS) free_kv_kernel(const FreeArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ int s_warp[FREE_THREADS / 32];
@@ -297,13 +299,15 @@ __global__ void __launch_bounds__(FREE_THREADS) free_kv_kernel(const FreeArgs a)
   }
   if (bad) atomicOr(a.err, bad);
   cluster.sync();
+  // (Volatile: the words were set by other SMs' atomics.)
+  const volatile unsigned* bits = a.page_bits;
   // This CTA's words of the bit map, in order: `per` consecutive ones per thread.
   const int words = (a.num_pages + 31) / 32;
   const int per = (words + ctas * FREE_THREADS - 1) / (ctas * FREE_THREADS);
   const long long w0 = (static_cast<long long>(rank) * FREE_THREADS + tid) * per;
   int mine = 0;
   for (int k = 0; k < per; ++k)
-    if (w0 + k < words) mine += __popc(__ldcg(a.page_bits + w0 + k));
+    if (w0 + k < words) mine += __popc(bits[w0 + k]);
   int x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(FREE_THREADS) free_kv_kernel(const FreeArgs a)
   if (mine)
     for (int k = 0; k < per; ++k) {
       if (w0 + k >= words) break;
-      unsigned w = __ldcg(a.page_bits + w0 + k);
+      unsigned w = bits[w0 + k];
       if (w) a.page_bits[w0 + k] = 0;
       while (w) {
         const int bit = __ffs(static_cast<int>(w)) - 1;
@@ -356,27 +360,16 @@ cudaError_t launch_fork_kv(const ForkArgs& a, int num_sms, cudaStream_t stream) 
   const int slots = COPY_CTAS_PER_SM * num_sms;
   const int copy_parts = std::max(1, std::min(a.num_layers, slots / a.num_children));
   const dim3 grid(table_parts + copy_parts, a.num_children);
-  fork_kv_kernel<<<grid, FORK_THREADS, COPY_SMEM, stream>>>(a, table_parts);
-  return cudaGetLastError();
+  return launch_overlapping(fork_kv_kernel, grid, FORK_THREADS, COPY_SMEM, stream, 1, a, table_parts);
 }
 
 cudaError_t launch_free_kv(const FreeArgs& a, int max_entries, cudaStream_t stream) {
   // One CTA while it has at most four entries and four bit-map words per
   // thread; the cluster's barriers cost about 1 us.
   const long long work = std::max<long long>(max_entries, a.num_pages / 32);
-  int ctas = 1;
+  unsigned ctas = 1;
   while (ctas < FREE_MAX_CTAS && work > 4LL * FREE_THREADS * ctas) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(FREE_THREADS);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, free_kv_kernel, a);
+  return launch_overlapping(free_kv_kernel, dim3(ctas), FREE_THREADS, 0, stream, ctas, a);
 }
 
 }  // namespace mlav

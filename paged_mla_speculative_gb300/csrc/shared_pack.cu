@@ -293,6 +293,15 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
 struct Rows {
   uint4 v[PER_THREAD];
 };
+// A granule that the call reads once.  (Volatile: a read-only load whose
+// address is known early could be moved above griddepcontrol.wait.)
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 // Row r of 32 (each THREADS / 8 granules apart) at src + s_row[r] * 576, or
 // zeros where s_row is negative.
 __device__ __forceinline__ void load_rows(const uint16_t* src, const long long* s_row, Rows& x) {
@@ -301,11 +310,7 @@ __device__ __forceinline__ void load_rows(const uint16_t* src, const long long* 
     const int e = threadIdx.x + u * THREADS;
     const int r = e / ROW_CHUNKS, c = e - r * ROW_CHUNKS;
     const long long row = s_row[r];
-    x.v[u] = make_uint4(0, 0, 0, 0);
-    if (row >= 0)
-      asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                   : "=r"(x.v[u].x), "=r"(x.v[u].y), "=r"(x.v[u].z), "=r"(x.v[u].w)
-                   : "l"(reinterpret_cast<const uint4*>(src + row * D_QK) + c));
+    x.v[u] = row >= 0 ? load_once(reinterpret_cast<const uint4*>(src + row * D_QK) + c) : make_uint4(0, 0, 0, 0);
   }
 }
 // Widened into the planes at plane rows row0 .. row0 + rows - 1.  A value
@@ -362,8 +367,7 @@ __global__ void __launch_bounds__(THREADS, 4) shared_prepare_kernel(const Shared
     for (int u = 0; u < PER_THREAD; ++u) {
       const int e = tid + u * THREADS;
       const long long row = row0 + e / ROW_CHUNKS;
-      v[u] = make_uint4(0, 0, 0, 0);
-      if (row < rows) v[u] = __ldg(reinterpret_cast<const uint4*>(p.q + row * D_QK) + e % ROW_CHUNKS);
+      v[u] = row < rows ? load_once(reinterpret_cast<const uint4*>(p.q + row * D_QK) + e % ROW_CHUNKS) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < PER_THREAD; ++u) {
@@ -514,24 +518,11 @@ __global__ void __launch_bounds__(JOIN_ROWS * 128) shared_join_kernel(const Shar
   if (col == 0) p.lse[row] = lse;
 }
 
-template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), long long grid, unsigned block, cudaStream_t stream, bool overlap, Args... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(block);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = overlap ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 }  // namespace
 
 cudaError_t launch_shared_prepare(const SharedParams& p, int num_sms, cudaStream_t stream) {
   if (p.clusters > SH_MAX_CLUSTERS) return cudaErrorInvalidValue;
+  auto grid = [](long long ctas) { return dim3(static_cast<unsigned>(ctas)); };
   const long long rows = static_cast<long long>(p.batch) * p.R;
   const long long query_ctas = (rows + PACK_KEYS - 1) / PACK_KEYS;
   const long long most = static_cast<long long>(p.batch) * p.max_kv_len + SH_TAIL;
@@ -540,13 +531,14 @@ cudaError_t launch_shared_prepare(const SharedParams& p, int num_sms, cudaStream
   const long long wave = std::max(2LL * num_sms, 4LL * num_sms - 2 - query_ctas);
   const int packers = static_cast<int>(std::min<long long>((most + PACK_KEYS - 1) / PACK_KEYS, wave));
   if (p.batch <= SMALL && p.groups <= SMALL)
-    return launch(shared_prepare_kernel, 2 + query_ctas + packers, THREADS, stream, true, p, 2, packers);
-  const cudaError_t e = launch(shared_prepare_kernel, 2 + query_ctas, THREADS, stream, true, p, 2, 0);
-  return e != cudaSuccess ? e : launch(shared_prepare_kernel, packers, THREADS, stream, true, p, 0, packers);
+    return launch_overlapping(shared_prepare_kernel, grid(2 + query_ctas + packers), THREADS, 0, stream, 1, p, 2, packers);
+  const cudaError_t e = launch_overlapping(shared_prepare_kernel, grid(2 + query_ctas), THREADS, 0, stream, 1, p, 2, 0);
+  return e != cudaSuccess ? e : launch_overlapping(shared_prepare_kernel, grid(packers), THREADS, 0, stream, 1, p, 0, packers);
 }
 
 cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream) {
-  return launch(shared_join_kernel, static_cast<long long>(p.max_tiles) * (SH_ROWS / JOIN_ROWS), JOIN_ROWS * 128, stream, true, p);
+  const unsigned ctas = static_cast<unsigned>(p.max_tiles) * (SH_ROWS / JOIN_ROWS);
+  return launch_overlapping(shared_join_kernel, dim3(ctas), JOIN_ROWS * 128, 0, stream, 1, p);
 }
 
 }  // namespace mlav
