@@ -37,6 +37,9 @@ reads); its pins are in tests/test_index_builder_pins.py.
 context-parallel split: one shard's partial over its keys and the reduce of
 the shards' partials (pins: tests/test_context_parallel_pins.py).  ``compact_ref.compact_kv``
 restates KV compaction into 64-row pages (pins: tests/test_compact_pins.py).
+``append_ref.append_kv`` restates the write of new tokens' rows and queries,
+``page_pool_ref.fork_kv`` / ``free_kv`` the branches of cached requests over
+counted pages (pins: tests/test_prompt_pins.py).
 
 Pins (tests/test_oracle_pins.py): pure-Python brute force on tiny inputs, a
 hand-derived closed-form fixture (tests/golden/), one-visible-key, identical
