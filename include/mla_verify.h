@@ -464,7 +464,7 @@ int mla_verify_compact_kv(mla_verify_plan* plan, int batch, const void* kv_src, 
  *   cos_sin      fp32 [max_pos][64].
  *   positions, slots  int32 [num_tokens].  Slot -1 marks a padding token:
  *                nothing of it is read or written.  The other slots are
- *                distinct (of two tokens with one slot either may be kept).
+ *                distinct (of two tokens with one slot a mixture stays).
  *   kv_cache     bf16 [num_slots][576], the plan's num_slots.
  *   q            bf16 [num_tokens][H][576], the plan's H.
  *
@@ -510,12 +510,14 @@ int mla_verify_append_kv(mla_verify_plan* plan, int64_t num_tokens, const void* 
  * The j-th fresh page of the call, in child order, is free_pages[free_count -
  * 1 - j]; free_count falls by the pages taken.  A parent may be forked any
  * number of times, or not at all; it keeps its own table.  The outputs must
- * not be the inputs.  num_parents and num_children in [1, max_batch].
+ * not be the inputs.  num_parents and num_children in [1, max_batch], and no
+ * more than 65535 children.
  * Device-side problems: a parent index out of range (MLA_VERIFY_DEV_BAD_POOL),
  * n outside [0, max_kv_len - extra_rows] (BAD_LEN) or a table that does not
  * hold n rows (BAD_INDPTR) gives the child length 0 and no entries; when the
  * stack or the capacity runs out the longest leading run of children that
- * fits is forked and later ones get none (CAPACITY); a page outside the cache
+ * fits is forked and later ones get none (CAPACITY; a free_count outside [0,
+ * num_slots / 64] counts as an empty stack and stays); a page outside the cache
  * stays in the table uncounted, its rows are copied as zeros (BAD_SLOT); a
  * held page whose count is not positive, or a fresh one whose count is not 0,
  * is reported (BAD_REF).

@@ -1012,7 +1012,7 @@ int mla_verify_fork_kv(mla_verify_plan* pl, int num_children, const int32_t* par
       !aligned16(child_indices) || !aligned16(child_indptr) || !aligned16(child_lens))
     return MLA_VERIFY_ERR_ALIGN;
   if (pl->page_size != mlav::PAGE) return MLA_VERIFY_ERR_SHAPE;
-  if (num_children < 1 || num_children > pl->max_batch || num_parents < 1 || num_parents > pl->max_batch)
+  if (num_children < 1 || num_children > std::min(pl->max_batch, 65535) || num_parents < 1 || num_parents > pl->max_batch)
     return MLA_VERIFY_ERR_BATCH;
   if (num_layers < 1 || layer_stride < 0 || layer_stride % 8 || extra_rows < 0 ||
       extra_rows > pl->max_kv_len || capacity < 0 || capacity > INT32_MAX)

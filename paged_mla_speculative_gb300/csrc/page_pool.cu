@@ -165,7 +165,9 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
   __shared__ __align__(8) uint64_t s_mbar[2];
   asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
   const int c = blockIdx.y, tid = threadIdx.x;
-  const long long left = max(0, min(*a.free_count, a.num_pages));
+  const int height = *a.free_count;
+  const bool height_ok = height >= 0 && height <= a.num_pages;
+  const long long left = height_ok ? height : 0;
   if (tid < 2) s_last[tid] = 0;
   if (tid == 0) {
     tc::mbar_init(smem_u32(s_mbar), 1);
@@ -205,7 +207,8 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
     const unsigned ctas = gridDim.x * gridDim.y;
     if (atomicAdd(a.ticket, 1u) == ctas - 1) {
       *a.ticket = 0;
-      *a.free_count = static_cast<int32_t>(left - static_cast<long long>(s_last[1]));
+      if (height_ok) *a.free_count = static_cast<int32_t>(left - static_cast<long long>(s_last[1]));
+      else atomicOr(a.err, ERR_CAPACITY);
     }
   }
   const Child ch = s_child;

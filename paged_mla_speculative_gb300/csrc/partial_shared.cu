@@ -156,7 +156,7 @@ struct Segment {
 __device__ __forceinline__ SharedTile load_tile(const SharedTile* rec) {
   const int4* q = reinterpret_cast<const int4*>(rec);
   const int4 a = q[0], b = q[1], c = q[2];
-  return SharedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, 0};
+  return SharedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {0, 0}};
 }
 // The cluster's next segment at or after tile `tile`; false when there is none.
 __device__ __forceinline__ bool next_segment(const SharedParams& p, const SharedShare* share, const SharedPos& from,

@@ -33,13 +33,12 @@ constexpr int SH_MAX_CLUSTERS = 128;   // of the attention kernel (an SM pair ea
 
 struct SharedTile {
   int q_row0, nrows;        // query rows
-  int b0;                   // request of the first row
   int prefix_base, prefix_len;
   int own_base, own_len;
   int halves;               // half blocks of the whole sequence
   int steps;                // (halves + 1) / 2
   int seg0, nseg;           // clusters seg0 .. seg0 + nseg - 1 hold its steps
-  int pad;
+  int pad[2];
 };
 static_assert(sizeof(SharedTile) == 48, "three 16-byte loads");
 

@@ -215,9 +215,8 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
       const int off = (t - tile0[g]) * SH_ROWS;
       rec.q_row0 = first + off;
       rec.nrows = min(SH_ROWS, rows - off);
-      rec.b0 = rec.q_row0 / p.R;
-      const int b1 = (rec.q_row0 + rec.nrows - 1) / p.R;
-      rec.own_base = base[2 * rec.b0 + 1];
+      const int b0 = rec.q_row0 / p.R, b1 = (rec.q_row0 + rec.nrows - 1) / p.R;
+      rec.own_base = base[2 * b0 + 1];
       rec.own_len = base[2 * b1 + 1] + own[b1] - rec.own_base;
       if (rec.own_len > 0) {       // some request of the tile is served
         rec.prefix_base = base[2 * grp.begin(g)];

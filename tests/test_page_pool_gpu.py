@@ -147,6 +147,22 @@ def test_what_does_not_fit_is_cut_and_reported():
         _free(plan, pool, kids)
 
 
+def test_a_stack_height_that_cannot_be():
+    pool = Pool(16, seed=16)
+    lens = [100, 64]
+    tables = [pool.request(n) for n in lens]
+    i, p = _tables(tables)
+    with _plan(pool) as plan:
+        for height in (-1, 17):
+            pool.push()
+            pool.d_count.fill_(height)
+            _, cp, cl = mb.fork_kv(plan, _i32([1, 0]), _i32(i), _i32(p), _i32(lens), pool.cache[0], pool.d_refs, pool.d_free,
+                                   pool.d_count)
+            # the child of full pages needs none of the stack
+            assert plan.get_error() == mb.DEV_CAPACITY and int(pool.d_count) == height
+            assert cp.tolist() == [0, 1, 1] and cl.tolist() == [64, 0]
+
+
 def test_bad_parents_lengths_tables_and_pages():
     pool = Pool(64, 2, seed=7)
     lens = [100, 200, 64, 90]

@@ -268,6 +268,25 @@ def test_rows_behind_the_batch_stay_as_they_were():
     G.assert_parity(out[:2].cpu().numpy(), lse[:2].cpu().numpy(), *G.oracle_full(inp))
 
 
+def test_rows_beyond_the_32_bit_offset():
+    """The same requests in the last rows of a cache of 2.4e9 elements."""
+    inp, gp, sl = make([3], [700], [30, 200, 5], 4, 16, seed=51)
+    ref = G.oracle_full(inp)
+    n, small = (1 << 22) + 64, inp.kv_cache.shape[0]
+    cache = torch.zeros(n, 576, dtype=torch.bfloat16, device="cuda")
+    cache[n - small:] = inp.kv_cache.cuda()
+    moved = dataclasses.replace(inp, kv_cache=cache, kv_indices=inp.kv_indices + (n - small))
+    with G.make_plan(moved) as plan:
+        o, l = run(plan, moved, gp, sl)
+        assert plan.get_error() == 0
+    G.assert_parity(o.cpu().numpy(), l.cpu().numpy(), *ref)
+
+
+def test_longest_trees_and_most_heads():
+    """32 drafts (every ancestor bit), 4096 query rows a request."""
+    check(make([2], [300], [40, 7], 32, 128, seed=52))
+
+
 def test_captured_and_replayed_with_other_lengths_and_groups():
     T, H = 4, 64
     cases = [make([3, 1], [300, 100], [10, 20, 30, 40], T, H, 64, seed=31, num_slots=8192),
