@@ -59,7 +59,7 @@ constexpr int OFF_XSUM = OFF_XRED + 2 * ROWS * 4 * 4; // float [128] the peer's 
 constexpr int OFF_M = OFF_XSUM + ROWS * 4;            // float [2][128] running row max (0: none yet); 1 / row sum at the end
 constexpr int OFF_ROW = OFF_M + 2 * ROWS * 4;             // int2 [128] request of the row (-1: not served), ancestor mask
 constexpr int OFF_MBAR = OFF_ROW + ROWS * 8;
-constexpr int NMBAR = 20;
+constexpr int NMBAR = 28;
 constexpr int OFF_MISC = OFF_MBAR + NMBAR * 8;        // tmem base, P-complete word, absent-unit word, abort flag
 constexpr int SMEM_TOTAL = OFF_MISC + 16;
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
@@ -78,9 +78,9 @@ constexpr int MB_PF = 12;      // even CTA: the odd CTA's P^T is complete (st.as
 constexpr int MB_OT = 13;      // O^T of a step done
 constexpr int MB_Q = 14;       // even CTA: both halves of a segment's queries landed
 constexpr int MB_QE = 15;      // the segment's last S^T is done: its queries can go
-constexpr int MB_X = 16;       // [2] the peer's row maxima of the step landed (st.async bytes)
-constexpr int MB_XS = 18;      // the peer's row sums landed (st.async bytes)
-constexpr int MB_DONE = 19;    // after an abort: every MMA issued is done
+constexpr int MB_X = 20;       // [2][4] the peer's row maxima of the step and row group landed (st.async bytes)
+constexpr int MB_XS = 16;      // the peer's row sums landed (st.async bytes)
+constexpr int MB_DONE = 17;    // after an abort: every MMA issued is done
 
 constexpr int TMEM_COLS = 512;
 constexpr uint32_t TM_S = 256;                  // S^T buffer u at 256 + 128u; O^T tile t at 128t
@@ -536,10 +536,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         // Every warp gives its 32 maxima to the group here and in the peer,
         // and takes the maximum of the eight itself.
         s_red[sb * ROWS * 4 + row * 4 + quad] = wmax;
-        tc::st_async_b32(xred_peer + sb * ROWS * 16, __float_as_uint(wmax), peer_mbar(MB_X + sb));
-        if (tid == 0) tc::mbar_arrive_expect(mbar(MB_X + sb), ROWS * 16);
+        tc::st_async_b32(xred_peer + sb * ROWS * 16, __float_as_uint(wmax), peer_mbar(MB_X + 4 * sb + grp));
+        if (quad == 0 && lane == 0) tc::mbar_arrive_expect(mbar(MB_X + 4 * sb + grp), 32 * 16);
         group_sync();
-        wait_peer(mbar(MB_X + sb), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
+        wait_peer(mbar(MB_X + 4 * sb + grp), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
         float alpha = 1.f;
         {
           const float4 o4 = *reinterpret_cast<const float4*>(s_red + sb * ROWS * 4 + row * 4);
@@ -573,8 +573,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             pk[4 * k8 + i] = *reinterpret_cast<const uint32_t*>(&hh);
           }
         }
-        // The step's row sums over this warp's 32 keys.
-        lrun = lrun * alpha + reduce_rows<true>(y, lane);
         // O^T of the step before done: the P^T buffers (here and in the peer)
         // are free and O^T can be rescaled.  (A segment's first step: the
         // readout waited for it.)
@@ -644,6 +642,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(mbar(MB_P));
+        // The step's row sums over this warp's 32 keys, off the way to O^T.
+        lrun = lrun * alpha + reduce_rows<true>(y, lane);
       }
       // ---- the segment's end: row sums over the group's warps, then the peer's
       const int eb = (g & 1) * ROWS;   // the halves of s_red and s_m that the last step did not use
