@@ -251,8 +251,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     // CTA's barriers run ahead.  S^T takes the first of its nine chunks from a
     // slot of its own, filled while O^T runs: its other slots are still on
     // their way then (three slots give a copy 768 cycles of MMAs to land in
-    // unnoticed, and it takes 1100 to 1400; with that chunk last and not first
-    // a step took 150 cycles more).
+    // unnoticed, and it takes 1100 to 1400).  16 requests on 65536 shared rows,
+    // trees of 16 drafts: 1658 us with the last chunk there, 1647 with the
+    // first and P's barriers armed a step ahead (the two not timed apart).
     const int cw = warp - COPY_WARP;
     const uint32_t absent_word = tc::peer_addr(smem_u32(s_tmem + 2), 0);
     int n = 0, g0 = 0, k = 0;   // units and segments so far, steps of the segments before
