@@ -52,8 +52,8 @@ constexpr int NSLOT = NCOPY;
 constexpr int OFF_Q = 0;
 constexpr int OFF_P = OFF_Q + 9 * Q_CHUNK;            // P^T [key half][128 keys][64 rows] fp16
 constexpr int OFF_RING = OFF_P + 2 * CHUNK;
-constexpr int OFF_LEAD = OFF_RING + NSLOT * 2 * CHUNK;
-constexpr int OFF_RED = OFF_LEAD + CHUNK;             // float [2][128 rows][4 quads] this CTA's row maxima of the step
+constexpr int OFF_ROPE = OFF_RING + NSLOT * 2 * CHUNK;
+constexpr int OFF_RED = OFF_ROPE + CHUNK;             // float [2][128 rows][4 quads] this CTA's row maxima of the step
 constexpr int OFF_XRED = OFF_RED + 2 * ROWS * 4 * 4;  // the same of the peer (st.async)
 constexpr int OFF_XSUM = OFF_XRED + 2 * ROWS * 4 * 4; // float [128] the peer's row sums
 constexpr int OFF_M = OFF_XSUM + ROWS * 4;            // float [2][128] running row max (0: none yet); 1 / row sum at the end
@@ -63,14 +63,14 @@ constexpr int NMBAR = 28;
 constexpr int OFF_MISC = OFF_MBAR + NMBAR * 8;        // tmem base, P-complete word, absent-unit word, abort flag
 constexpr int SMEM_TOTAL = OFF_MISC + 16;
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
-static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && OFF_LEAD % 1024 == 0,
+static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && OFF_ROPE % 1024 == 0,
               "swizzled tiles need 1024-byte alignment");
 
 // mbarrier indices (same offsets in both CTAs)
 constexpr int MB_FULL = 0;     // [3] even CTA: ring slot landed in both CTAs (bytes of both)
 constexpr int MB_EMPTY = 3;    // [3] ring slot read by its MMAs (commit to both CTAs)
-constexpr int MB_LFULL = 6;    // even CTA: lead slot landed in both CTAs
-constexpr int MB_LEMPTY = 7;   // lead slot read
+constexpr int MB_RFULL = 6;    // even CTA: rope slot landed in both CTAs
+constexpr int MB_REMPTY = 7;   // rope slot read
 constexpr int MB_S = 8;        // [2] S^T buffer done
 constexpr int MB_P = 10;       // this CTA's softmax warps wrote their P^T and rescaled O^T
 constexpr int MB_PX = 11;      // the peer's half of this CTA's P^T landed (st.async bytes)
@@ -246,14 +246,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 
   if (warp >= COPY_WARP) {
     // ========================= key chunk producers ==========================
-    // As in partial_pair.cu: unit n goes to slot n % 3, one warp per slot; a half
-    // block the odd CTA does not have is signalled by ABSENT_BYTES, so that no
-    // CTA's barriers run ahead.  S^T takes the first of its nine chunks from a
-    // slot of its own, filled while O^T runs: its other slots are still on
-    // their way then (three slots give a copy 768 cycles of MMAs to land in
-    // unnoticed, and it takes 1100 to 1400).  16 requests on 65536 shared rows,
-    // trees of 16 drafts: 1658 us with the last chunk there, 1647 with the
-    // first and P's barriers armed a step ahead (the two not timed apart).
+    // As in partial_pair.cu: unit n goes to slot n % 3, one warp per slot; the
+    // rope chunks go with slot 2; a half block the odd CTA does not have is
+    // signalled by ABSENT_BYTES, so that no CTA's barriers run ahead.
     const int cw = warp - COPY_WARP;
     const uint32_t absent_word = tc::peer_addr(smem_u32(s_tmem + 2), 0);
     int n = 0, g0 = 0, k = 0;   // units and segments so far, steps of the segments before
@@ -282,24 +277,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         phase_of(f, s.steps, is_s, i);
         const int hb0 = 2 * (s.sa + i);
         int count;
-        if (is_s && cw == NCOPY - 1) {
-          // The lead chunk: dims 0..63 of the own half block.
-          const int g = g0 + i;
-          const bool mine = hb0 + static_cast<int>(rank) < s.t.halves, peers = hb0 + static_cast<int>(peer) < s.t.halves;
-          if (g > 0) wait_own(mbar(MB_LEMPTY), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
-          if (*s_abort) break;
-          if (rank == 0) {
-            if (lane == 0) tc::mbar_arrive_expect(mbar(MB_LFULL), (mine ? CHUNK : 0) + (peers ? CHUNK : ABSENT_BYTES));
-            __syncwarp();
-          }
-          if (mine) {
-            tc::tma_load_3d_pair(sbase + OFF_LEAD, &tm_chunk, 0, half_base(s.t, hb0 + static_cast<int>(rank), count), 0,
-                                 even_mbar(MB_LFULL));
-          } else if (rank == 1) {
-            if (lane == 0) tc::st_async_b32(absent_word, 0, even_mbar(MB_LFULL));
-            __syncwarp();
-          }
-        }
 #pragma unroll 1
         for (int u = 0; u < 4; ++u, ++n) {
           const int slot = n % NSLOT;
@@ -307,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           // S units: the own half block (the peer loads its own); O units:
           // half block h in both CTAs.
           const int h = is_s ? static_cast<int>(rank) : (u & 1);
-          const int chunk = is_s ? 1 + 2 * u : 4 * (u >> 1) + 2 * static_cast<int>(rank);
+          const int pair_idx = is_s ? u : 2 * (u >> 1) + static_cast<int>(rank);
           const bool mine = hb0 + h < s.t.halves;
           const bool peers = is_s ? hb0 + static_cast<int>(peer) < s.t.halves : mine;
           if (n >= NSLOT) wait_own(mbar(MB_EMPTY + slot), static_cast<uint32_t>((n / NSLOT - 1) & 1), s_abort, p.err);
@@ -318,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             __syncwarp();
           }
           if (mine) {
-            tc::tma_load_3d_pair(sbase + OFF_RING + slot * 2 * CHUNK, &tm_pair, 0, half_base(s.t, hb0 + h, count), chunk,
+            tc::tma_load_3d_pair(sbase + OFF_RING + slot * 2 * CHUNK, &tm_pair, 0, half_base(s.t, hb0 + h, count), 2 * pair_idx,
                                  even_mbar(MB_FULL + slot));
           } else if (rank == 1) {
             if (lane == 0) tc::st_async_b32(absent_word, 0, even_mbar(MB_FULL + slot));
@@ -326,6 +303,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
         }
         if (*s_abort) break;
+        if (is_s && cw == NCOPY - 1) {
+          const int g = g0 + i;
+          const bool mine = hb0 + static_cast<int>(rank) < s.t.halves, peers = hb0 + static_cast<int>(peer) < s.t.halves;
+          if (g > 0) wait_own(mbar(MB_REMPTY), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
+          if (*s_abort) break;
+          if (rank == 0) {
+            if (lane == 0) tc::mbar_arrive_expect(mbar(MB_RFULL), (mine ? CHUNK : 0) + (peers ? CHUNK : ABSENT_BYTES));
+            __syncwarp();
+          }
+          if (mine) {
+            tc::tma_load_3d_pair(sbase + OFF_ROPE, &tm_chunk, 0, half_base(s.t, hb0 + static_cast<int>(rank), count), 8,
+                                 even_mbar(MB_RFULL));
+          } else if (rank == 1) {
+            if (lane == 0) tc::st_async_b32(absent_word, 0, even_mbar(MB_RFULL));
+            __syncwarp();
+          }
+        }
       }
     }
     // After an abort, copies already issued land within microseconds: wait
@@ -352,11 +346,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   } else if (warp == MMA_WARP) {
     // ======================= MMA issuer (even CTA) ==========================
     int n = 0, g0 = 0, k = 0;
-    if (lane == 0) {
-      tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
-      tc::mbar_arrive_expect(mbar(MB_PF), 4);
-    }
-    __syncwarp();
 #pragma unroll 1
     for (int tile = from.tile; next_segment(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
       wait_own(mbar(MB_Q), static_cast<uint32_t>(k & 1), s_abort, p.err);
@@ -369,15 +358,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const int g = g0 + i;
         if (is_s) {
           const uint32_t d = tmem + TM_S + 128u * static_cast<uint32_t>(g & 1);
-          wait_own(mbar(MB_LFULL), static_cast<uint32_t>(g & 1), s_abort, p.err);
-          tc::fence_after_sync();
-          if (tc::elect_one()) {
-            const uint32_t a = desc_lo(sbase + OFF_LEAD, 16), bq = desc_lo(sbase + OFF_Q, 16);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) tc::mma_pair_one(d, a + 2 * kk, bq + 2 * kk, DESC_HI, IDESC_S, kk > 0 ? 1u : 0u);
-            tc::commit_pair_one(mbar(MB_LEMPTY));
-          }
-          __syncwarp();
 #pragma unroll 1
           for (int u = 0; u < 4; ++u, ++n) {
             const int slot = n % NSLOT;
@@ -385,22 +365,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             tc::fence_after_sync();
             if (tc::elect_one()) {
               const uint32_t a = desc_lo(sbase + OFF_RING + slot * 2 * CHUNK, 16);
-              const uint32_t bq = desc_lo(sbase + OFF_Q + (1 + 2 * u) * Q_CHUNK, 16);
+              const uint32_t bq = desc_lo(sbase + OFF_Q + u * 2 * Q_CHUNK, 16);
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)   // 16-dim steps of the chunk pair
                 tc::mma_pair_one(d, a + (((kk >> 2) * CHUNK + (kk & 3) * 32) >> 4),
-                                 bq + (((kk >> 2) * Q_CHUNK + (kk & 3) * 32) >> 4), DESC_HI, IDESC_S, 1);
+                                 bq + (((kk >> 2) * Q_CHUNK + (kk & 3) * 32) >> 4), DESC_HI, IDESC_S, (u > 0 || kk > 0) ? 1u : 0u);
               tc::commit_pair_one(mbar(MB_EMPTY + slot));
-              if (u == 3) {
-                tc::commit_pair_one(mbar(MB_S + (g & 1)));
-                if (i == s.steps - 1) tc::commit_pair_one(mbar(MB_QE));
-              }
             }
             __syncwarp();
           }
+          wait_own(mbar(MB_RFULL), static_cast<uint32_t>(g & 1), s_abort, p.err);
+          tc::fence_after_sync();
+          if (tc::elect_one()) {
+            const uint32_t a = desc_lo(sbase + OFF_ROPE, 16), bq = desc_lo(sbase + OFF_Q + 8 * Q_CHUNK, 16);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) tc::mma_pair_one(d, a + 2 * kk, bq + 2 * kk, DESC_HI, IDESC_S, 1);
+            tc::commit_pair_one(mbar(MB_REMPTY));
+            tc::commit_pair_one(mbar(MB_S + (g & 1)));
+            if (i == s.steps - 1) tc::commit_pair_one(mbar(MB_QE));
+          }
+          __syncwarp();
         } else {
           // P^T of the step: this CTA's softmax warps, the odd CTA's st.async
           // bytes, and the odd CTA's word that its own half is complete.
+          if (lane == 0) {
+            tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
+            tc::mbar_arrive_expect(mbar(MB_PF), 4);
+          }
+          __syncwarp();
           wait_own(mbar(MB_P), static_cast<uint32_t>(g & 1), s_abort, p.err);
           wait_peer(mbar(MB_PX), static_cast<uint32_t>(g & 1), s_abort, p.err);
           wait_peer(mbar(MB_PF), static_cast<uint32_t>(g & 1), s_abort, p.err);
@@ -422,12 +414,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
                                    IDESC_O, (i > 0 || h > 0 || kk > 0) ? 1u : 0u);
               }
               tc::commit_pair_one(mbar(MB_EMPTY + slot));
-              if (u == 3) {
-                tc::commit_pair_one(mbar(MB_OT));
-                // The next step's barriers, off the way from P^T to O^T.
-                tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
-                tc::mbar_arrive_expect(mbar(MB_PF), 4);
-              }
+              if (u == 3) tc::commit_pair_one(mbar(MB_OT));
             }
             __syncwarp();
           }
