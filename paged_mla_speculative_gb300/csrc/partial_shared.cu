@@ -9,8 +9,8 @@
 // exchange between the two CTAs of a pair are those of partial_pair.cu:
 //     S^T[key, row] = K_pair[256 x 576] . Q_tile[128 x 576]^T
 //     O^T[dim, row] += V_pair^T[512 x 256] . P^T[256 x 128]
-// with the running maximum and sum in fp32, P in fp16 (rounded once; with the
-// bf16 keys widened to fp16, which is exact, its 2^-11 is the largest error),
+// with the running maximum and sum in fp32, P in fp16 (rounded once, 2^-11 of
+// every weight down to 2^-29 of the row's largest; see P_SHIFT),
 // O^T in tensor memory, split by value dim over the two CTAs.
 //
 // What differs is the schedule.  The grid is one cluster per SM pair; cluster
@@ -56,7 +56,7 @@ constexpr int OFF_ROPE = OFF_RING + NSLOT * 2 * CHUNK;
 constexpr int OFF_RED = OFF_ROPE + CHUNK;             // float [2][128 rows][4 quads] this CTA's row maxima of the step
 constexpr int OFF_XRED = OFF_RED + 2 * ROWS * 4 * 4;  // the same of the peer (st.async)
 constexpr int OFF_XSUM = OFF_XRED + 2 * ROWS * 4 * 4; // float [128] the peer's row sums
-constexpr int OFF_M = OFF_XSUM + ROWS * 4;            // float [2][128] running row max (0: none yet); 1 / row sum at the end
+constexpr int OFF_M = OFF_XSUM + ROWS * 4;            // float [2][128] running row max less P_SHIFT (0: none yet); 1 / row sum at the end
 constexpr int OFF_ROW = OFF_M + 2 * ROWS * 4;             // int2 [128] request of the row (-1: not served), ancestor mask
 constexpr int OFF_MBAR = OFF_ROW + ROWS * 8;
 constexpr int NMBAR = 28;
@@ -94,6 +94,14 @@ constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3FFF) | (lbo >> 4) << 16; }
 
 constexpr int FEW_MOVED = 4;
+
+// Weights are taken relative to 2^-P_SHIFT of the row's largest, so the
+// largest is 2^15 in fp16.  Relative to the largest itself, those below 2^-14
+// of it would be subnormal and those below 2^-25 zero, though the fp32 row sum
+// counts them: where one key without value led by 17 nats, the outputs were
+// 16 % too small.  The shift moves that to 2^-29 and 2^-40 and costs nothing
+// per score: row sums and O^T carry the same factor.
+constexpr float P_SHIFT = 15.f, P_LARGEST = 32768.f;
 // Bounded waits of a warp.  wait_own: for barriers that TMA, tcgen05.commit
 // and this CTA's threads complete; wait_peer: for those that the peer's
 // st.async complete, acquiring its stores into this CTA's shared memory.
@@ -479,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         s_row[c0 + lane] = of;
       }
       group_sync();
-      float mrow = -INFINITY;             // the lane's row's running max, the same in the group's warps of both CTAs
+      float mrow = -INFINITY;             // the lane's row's running max less P_SHIFT, the same in the group's warps of both CTAs
       float lrun = 0.f;                   // its sum over this warp's keys so far
 #pragma unroll 1
       for (int it = 0; it < nsteps; ++it, ++g) {
@@ -544,7 +552,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         {
           const float4 o4 = *reinterpret_cast<const float4*>(s_red + sb * ROWS * 4 + row * 4);
           const float4 p4 = *reinterpret_cast<const float4*>(s_xred + sb * ROWS * 4 + row * 4);
-          const float bm = fmaxf(fmaxf(fmaxf(o4.x, o4.y), fmaxf(o4.z, o4.w)), fmaxf(fmaxf(p4.x, p4.y), fmaxf(p4.z, p4.w)));
+          const float top = fmaxf(fmaxf(fmaxf(o4.x, o4.y), fmaxf(o4.z, o4.w)), fmaxf(fmaxf(p4.x, p4.y), fmaxf(p4.z, p4.w)));
+          // (Scores beyond 2^24 may round the difference to 16 or more, which
+          // fp16 does not hold: no shift there.)
+          float bm = top - P_SHIFT;
+          if (top - bm > P_SHIFT + 0.5f) bm = top;
           if (bm > mrow) {
             if (mrow != -INFINITY) alpha = ex2(mrow - bm);
             mrow = bm;
@@ -556,8 +568,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           s_m[(sb ^ 1u) * ROWS + row] = alpha;
         }
         __syncwarp();
-        // P^T in fp16: weight 1 is exact (the fused product is off by an ulp
-        // of the score at most), the others lose 2^-11 at most.
+        // P^T in fp16: the largest weight, 2^15, is exact (the fused product is
+        // off by an ulp of the score at most), those from 2^-14 on lose 2^-11
+        // at most, smaller ones 2^-25 (2^-40 of the largest).
         uint32_t pk[16];   // word 4 k8 + i: rows (i, 0) and (i, 1) of key 8 k8
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -667,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const bool lost = l != l || s_row[r].x < 0;
         s_l[r] = lost ? nan : l > 0.f ? 1.f / l : 0.f;
         if (r < s.t.nrows && (r >> 6) == static_cast<int>(rank)) {
-          const float lse = lost ? nan : l > 0.f ? (mrow + log2f(l)) * kLn2 : -INFINITY;
+          const float lse = lost ? nan : l > 0.f ? ((mrow + P_SHIFT) + log2f(l / P_LARGEST)) * kLn2 : -INFINITY;
           if (s.whole) p.lse[s.t.q_row0 + r] = lse;
           else p.part_lse[part0 + r] = lse;
         }

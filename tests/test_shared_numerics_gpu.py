@@ -1,0 +1,60 @@
+"""Numerics of the shared-prefix verify attention where the weights of a row
+span more than fp16 does, against the fp64 oracle, by relative error.
+
+Tolerance of an output whose value parts are all positive: P^T is rounded to
+fp16 once (2^-11 of each weight, and all equal weights alike); the scores here
+are exact, their exponents lose 2^-20 at most, and the fp32 sums of a cluster's
+few thousand keys less than 2^-14.
+"""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+from paged_mla_speculative_gb300 import binding as mb
+from tests import gpu_util as G
+from tests.test_shared_gpu import make, run
+
+pytestmark = pytest.mark.gpu
+
+REL = 2.0 ** -11 + 2.0 ** -14
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_mla_speculative_gb300 import build
+    build.build()
+
+
+def _one_dim_scores(shared, sink, others, q0, T=4, H=16, seed=60):
+    """Two requests whose scores come from rope dim 0 alone: the first shared
+    key has `sink` there and a value part of zeros, every other key `others`
+    and values in [0.5, 1.5); head h of every draft has q0[h]."""
+    inp, gp, sl = make([2], [shared], [9, 40], T, H, seed=seed, spike_frac=0.0)
+    g = torch.Generator().manual_seed(seed)
+    cache = torch.zeros_like(inp.kv_cache)
+    cache[:, :512] = (0.5 + torch.rand(cache.shape[0], 512, generator=g)).to(torch.bfloat16)
+    cache[:, 512] = others
+    first = int(inp.kv_indices[0])
+    cache[first] = 0
+    cache[first, 512] = sink
+    q = torch.zeros_like(inp.q)
+    q[..., 512] = torch.tensor(q0, dtype=torch.float32).to(torch.bfloat16)
+    return dataclasses.replace(inp, q=q, kv_cache=cache), gp, sl
+
+
+@pytest.mark.parametrize("shared", [600, 40000])     # a whole tile; parts of one merged
+def test_a_dominant_key_without_value(shared):
+    """One key up to 17.4 nats ahead (its weight is 2^25 times another's) holds
+    no value: the output is what the others' small weights add up to."""
+    case = _one_dim_scores(shared, 15.0625, 0.0, [16.0 - 0.5 * h for h in range(16)])
+    with G.make_plan(case[0]) as plan:
+        out, lse = run(plan, *case)
+        assert plan.get_error() == 0
+    ro, rl = G.oracle_full(case[0])
+    assert ro.min() > 0
+    assert (np.abs(out.double().cpu().numpy() - ro) <= REL * ro).all()
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= 2.0 ** -16 * np.maximum(1, np.abs(rl))).all()
