@@ -102,6 +102,8 @@ constexpr int FEW_MOVED = 4;
 // 16 % too small.  The shift moves that to 2^-29 and 2^-40 and costs nothing
 // per score: row sums and O^T carry the same factor.
 constexpr float P_SHIFT = 15.f, P_LARGEST = 32768.f;
+// Scores (as powers of two) up to which half an ulp is a quarter at most.
+constexpr float FUSED_LIMIT = 8388608.f;
 // Bounded waits of a warp.  wait_own: for barriers that TMA, tcgen05.commit
 // and this CTA's threads complete; wait_peer: for those that the peer's
 // st.async complete, acquiring its stores into this CTA's shared memory.
@@ -568,9 +570,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           s_m[(sb ^ 1u) * ROWS + row] = alpha;
         }
         __syncwarp();
-        // P^T in fp16: the largest weight, 2^15, is exact (the fused product is
-        // off by an ulp of the score at most), those from 2^-14 on lose 2^-11
-        // at most, smaller ones 2^-25 (2^-40 of the largest).
+        // The fused product below is exact, the maximum a rounded one, half an
+        // ulp of the score away at most.  Weights and row sum share whatever it
+        // is, but where it is 1 and more the largest weight would leave fp16:
+        // there the scores are rounded as the maximum was.  (All warps of the
+        // group decide alike: they hold the same maxima.)
+        if (__any_sync(0xffffffffu, fabsf(mrow) > FUSED_LIMIT)) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] *= mul;
+          mul = 1.f;
+        }
+        // P^T in fp16: the largest weight is 2^15, those from 2^-14 on lose
+        // 2^-11 at most, smaller ones 2^-25 (2^-40 of the largest).
         uint32_t pk[16];   // word 4 k8 + i: rows (i, 0) and (i, 1) of key 8 k8
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

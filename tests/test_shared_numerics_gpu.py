@@ -58,3 +58,17 @@ def test_a_dominant_key_without_value(shared):
     assert ro.min() > 0
     assert (np.abs(out.double().cpu().numpy() - ro) <= REL * ro).all()
     assert (np.abs(lse.double().cpu().numpy() - rl) <= 2.0 ** -16 * np.maximum(1, np.abs(rl))).all()
+
+
+@pytest.mark.parametrize("sink,others", [(59904.0, 0.0), (0.0, 59904.0), (59904.0, 59904.0), (59904.0, -59904.0)])
+def test_scores_beyond_the_exactness_of_fp32(sink, others):
+    """Scores up to 3e8: every weight is 1 or 0, of the smallest query 2^-40."""
+    q0 = [s * v for v in (59904.0, 40192.0, 3008.0, 520.0, 260.0, 130.0, 65.0, 2.0 ** -16) for s in (1.0, -1.0)]
+    case = _one_dim_scores(300, sink, others, q0)
+    with G.make_plan(case[0]) as plan:
+        out, lse = run(plan, *case)
+        assert plan.get_error() == 0
+    ro, rl = G.oracle_full(case[0])
+    assert (np.abs(out.double().cpu().numpy() - ro) <= REL * np.abs(ro)).all()
+    # the scaled score is rounded in units of log2 and again as lse
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= 2.0 ** -21 * np.maximum(1, np.abs(rl)) + 2.0 ** -16).all()
