@@ -225,11 +225,18 @@ int mla_verify_plan_set_profile_events(mla_verify_plan* plan, void* after_pack,
  * on use the tags 2^32 - 2, 2^32 - 1, 2^32, .. (the epoch and the tags are
  * 64-bit: they do not wrap); every result must stay exact.  The value is
  * written by a pageable host copy: not for a call under stream capture.
+ * MLA_VERIFY_FAULT_EVEN_GIVES_UP / _ODD_GIVES_UP (mla_verify_attn_shared):
+ * that CTA of every pair with two steps or more stops in its second one, as
+ * after a wait that ran out; its peer's waits run out (about a second), the
+ * pair's rows come out NaN, MLA_VERIFY_DEV_TIMEOUT is set and the context
+ * stays usable.
  * MLA_VERIFY_OK, or MLA_VERIFY_ERR_ARG for an unknown fault.
  */
 #define MLA_VERIFY_FAULT_NONE         0
 #define MLA_VERIFY_FAULT_SKIP_PACK    1
 #define MLA_VERIFY_FAULT_EPOCH_NEAR_WRAP 2
+#define MLA_VERIFY_FAULT_EVEN_GIVES_UP 3
+#define MLA_VERIFY_FAULT_ODD_GIVES_UP 4
 int mla_verify_plan_inject_fault(mla_verify_plan* plan, int fault);
 
 /* Bytes of device workspace the plan holds (partials, packed key blocks,

@@ -30,6 +30,8 @@ PACK_NONE = 4
 FAULT_NONE = 0
 FAULT_SKIP_PACK = 1
 FAULT_EPOCH_NEAR_WRAP = 2
+FAULT_EVEN_GIVES_UP = 3
+FAULT_ODD_GIVES_UP = 4
 MAX_NSPLIT = 32
 
 DEV_BAD_SLOT = 1

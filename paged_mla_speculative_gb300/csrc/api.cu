@@ -541,7 +541,8 @@ int mla_verify_plan_get_pack_mode(const mla_verify_plan* pl, int batch) {
 int mla_verify_plan_inject_fault(mla_verify_plan* pl, int fault) {
   if (!pl) return MLA_VERIFY_ERR_NULL;
   if (fault != MLA_VERIFY_FAULT_NONE && fault != MLA_VERIFY_FAULT_SKIP_PACK &&
-      fault != MLA_VERIFY_FAULT_EPOCH_NEAR_WRAP)
+      fault != MLA_VERIFY_FAULT_EPOCH_NEAR_WRAP && fault != MLA_VERIFY_FAULT_EVEN_GIVES_UP &&
+      fault != MLA_VERIFY_FAULT_ODD_GIVES_UP)
     return MLA_VERIFY_ERR_ARG;
   pl->fault = fault;
   return MLA_VERIFY_OK;
@@ -932,6 +933,8 @@ int mla_verify_attn_shared(mla_verify_plan* pl, int batch, const void* q, const 
   p.lse = lse;
   p.out_bf16 = pl->out_dtype == MLA_VERIFY_OUT_BF16;
   p.err = pl->err;
+  p.fault_rank = pl->fault == MLA_VERIFY_FAULT_EVEN_GIVES_UP ? 0 : pl->fault == MLA_VERIFY_FAULT_ODD_GIVES_UP ? 1 : -1;
+  pl->fault = MLA_VERIFY_FAULT_NONE;
   p.q16 = static_cast<uint16_t*>(pl->st_q);
   p.q_plane = 1LL * pl->max_batch * pl->R;
   p.k16 = static_cast<uint16_t*>(pl->packed);

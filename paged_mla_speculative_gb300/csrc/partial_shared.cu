@@ -27,7 +27,9 @@
 //
 // Roles (20 warps per CTA): warps 0-15 softmax, warp 16 MMA issue (even CTA)
 // or P^T hand-off (odd CTA), warps 17-19 the key ring (17 the queries too).
-// Every wait is bounded; after a timeout all of the cluster's rows are NaN.
+// Every wait is bounded.  A CTA whose wait runs out arms and sends nothing any
+// more, so its peer's waits run out too or its peer is done; the two tell each
+// other at the end, and all of the cluster's rows are NaN.
 #include "shared.cuh"
 #include "kernels.h"
 #include "pair_common.cuh"
@@ -60,8 +62,8 @@ constexpr int OFF_M = OFF_XSUM + ROWS * 4;            // float [2][128] running 
 constexpr int OFF_ROW = OFF_M + 2 * ROWS * 4;             // int2 [128] request of the row (-1: not served), ancestor mask
 constexpr int OFF_MBAR = OFF_ROW + ROWS * 8;
 constexpr int NMBAR = 28;
-constexpr int OFF_MISC = OFF_MBAR + NMBAR * 8;        // tmem base, P-complete word, absent-unit word, abort flag
-constexpr int SMEM_TOTAL = OFF_MISC + 16;
+constexpr int OFF_MISC = OFF_MBAR + NMBAR * 8;        // tmem base, P-complete word, absent-unit word, abort flag, the peer's
+constexpr int SMEM_TOTAL = OFF_MISC + 32;
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
 static_assert(OFF_P % 1024 == 0 && OFF_RING % 1024 == 0 && OFF_ROPE % 1024 == 0,
               "swizzled tiles need 1024-byte alignment");
@@ -154,6 +156,9 @@ __device__ __forceinline__ float reduce_rows(float (&y)[8], int lane) {
   return y[0];
 }
 
+// Testing: the ring unit before which SharedParams::fault_rank's CTA gives up
+// (the first of a second step's O^T, so that a step of scores is done).
+constexpr int SH_FAULT_UNIT = 12;
 constexpr uint32_t ABSENT_BYTES = 4;   // the odd CTA's signal for a unit it has no half block for
 
 struct Segment {
@@ -184,19 +189,18 @@ __device__ __forceinline__ bool next_segment(const SharedParams& p, const Shared
   return false;
 }
 
-// NaN for every row of the segment (a call that gave up).
+// NaN for every row of the segment (a pair that gave up), in the places that
+// this CTA's readout writes: value dims 256 t + 128 rank .., lse of its 64 rows.
 __device__ __forceinline__ void write_nan_segment(const SharedParams& p, const Segment& s, int cluster, uint32_t rank, int tid) {
   const float nan = __int_as_float(0x7fc00000);
+  const size_t row0 = s.whole ? static_cast<size_t>(s.t.q_row0) : static_cast<size_t>(part_slot(cluster, s.first)) * ROWS;
   for (int i = tid; i < s.t.nrows * 256; i += NTHREADS) {
-    const int r = i >> 8, d = static_cast<int>(rank) * 256 + (i & 255);
-    if (s.whole) {
-      const size_t at = static_cast<size_t>(s.t.q_row0 + r) * D_V + d;
-      if (p.out_bf16) reinterpret_cast<uint16_t*>(p.out)[at] = 0x7fc0;
-      else reinterpret_cast<float*>(p.out)[at] = nan;
-      if (d == 0) p.lse[s.t.q_row0 + r] = nan;
-    } else if (d == 0) {
-      p.part_lse[static_cast<size_t>(part_slot(cluster, s.first)) * ROWS + r] = nan;
-    }
+    const int r = i >> 8, c = i & 255;
+    const size_t at = (row0 + r) * D_V + (c >> 7) * 256 + rank * 128 + (c & 127);
+    if (!s.whole) p.part_o[at] = nan;
+    else if (p.out_bf16) reinterpret_cast<uint16_t*>(p.out)[at] = 0x7fc0;
+    else reinterpret_cast<float*>(p.out)[at] = nan;
+    if (c == 0 && (r >> 6) == static_cast<int>(rank)) (s.whole ? p.lse : p.part_lse)[row0 + r] = nan;
   }
 }
 
@@ -225,7 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   if (tid == 0) {
     for (int i = 0; i < NMBAR; ++i) tc::mbar_init(mbar(i), i == MB_P ? SOFTMAX_WARPS : 1);
     tc::mbar_fence_init();
-    *s_abort = 0;
+    s_abort[0] = s_abort[1] = 0;
   }
   if (warp == MMA_WARP) tc::tmem_alloc_pair<TMEM_COLS>(smem_u32(s_tmem));
   tc::fence_before_sync();
@@ -298,6 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           const bool mine = hb0 + h < s.t.halves;
           const bool peers = is_s ? hb0 + static_cast<int>(peer) < s.t.halves : mine;
           if (n >= NSLOT) wait_own(mbar(MB_EMPTY + slot), static_cast<uint32_t>((n / NSLOT - 1) & 1), s_abort, p.err);
+          if (n == SH_FAULT_UNIT && p.fault_rank == static_cast<int>(rank)) *s_abort = 1;   // (testing)
           if (*s_abort) break;
           if (rank == 0) {
             if (lane == 0)
@@ -332,22 +337,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
       }
     }
-    // After an abort, copies already issued land within microseconds: wait
-    // far longer than that before the pair's shared memory can be released.
-    if (*s_abort) settle(1LL << 22);
   } else if (warp == MMA_WARP && rank == 1) {
     // =================== odd CTA: P^T complete -> even CTA ==================
     uint32_t* s_word = s_tmem + 1;
     const uint32_t even_word = tc::peer_addr(smem_u32(s_word), 0);
     int g = 0;
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, share, from, to, tile, s); tile = s.tile + 1) {
+    for (int tile = from.tile; next_segment(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1) {
 #pragma unroll 1
-      for (int i = 0; i < s.steps; ++i, ++g) {
+      for (int i = 0; i < s.steps && !*s_abort; ++i, ++g) {
         if (lane == 0) tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
         __syncwarp();
         wait_own(mbar(MB_P), static_cast<uint32_t>(g & 1), s_abort, p.err);
         wait_peer(mbar(MB_PX), static_cast<uint32_t>(g & 1), s_abort, p.err);
+        if (*s_abort) break;
         tc::fence_async_smem();   // the st.async bytes are read by the tensor core next
         if (lane == 0) tc::st_async_b32(even_word, static_cast<uint32_t>(g), even_mbar(MB_PF));
         __syncwarp();
@@ -398,6 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         } else {
           // P^T of the step: this CTA's softmax warps, the odd CTA's st.async
           // bytes, and the odd CTA's word that its own half is complete.
+          if (*s_abort) break;
           if (lane == 0) {
             tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
             tc::mbar_arrive_expect(mbar(MB_PF), 4);
@@ -430,11 +434,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           }
         }
       }
-    }
-    // After an abort: every MMA issued finishes before TMEM is freed.
-    if (__any_sync(0xffffffffu, *s_abort != 0)) {
-      tc::commit_pair(mbar(MB_DONE));
-      wait_drain(mbar(MB_DONE), 0, p.err);
     }
   } else {
     // ============================= softmax =================================
@@ -493,6 +492,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       float lrun = 0.f;                   // its sum over this warp's keys so far
 #pragma unroll 1
       for (int it = 0; it < nsteps; ++it, ++g) {
+        // After an abort no barrier may be armed before its last phase is over,
+        // and no bytes sent that nobody arms for.
+        const bool alive = *s_abort == 0;
         // Decided while S^T is computed: do all rows see all of the warp's
         // keys?  If not, which: bit 8k + 2i + e for key k and row (i, e).
         const bool plain = __all_sync(0xffffffffu, meta == META_SHARED);
@@ -546,8 +548,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         // Every warp gives its 32 maxima to the group here and in the peer,
         // and takes the maximum of the eight itself.
         s_red[sb * ROWS * 4 + row * 4 + quad] = wmax;
-        tc::st_async_b32(xred_peer + sb * ROWS * 16, __float_as_uint(wmax), peer_mbar(MB_X + 4 * sb + grp));
-        if (quad == 0 && lane == 0) tc::mbar_arrive_expect(mbar(MB_X + 4 * sb + grp), 32 * 16);
+        if (alive) {
+          tc::st_async_b32(xred_peer + sb * ROWS * 16, __float_as_uint(wmax), peer_mbar(MB_X + 4 * sb + grp));
+          if (quad == 0 && lane == 0) tc::mbar_arrive_expect(mbar(MB_X + 4 * sb + grp), 32 * 16);
+        }
         group_sync();
         wait_peer(mbar(MB_X + 4 * sb + grp), static_cast<uint32_t>((g >> 1) & 1), s_abort, p.err);
         float alpha = 1.f;
@@ -659,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             const uint32_t u0 = odd ? r01 : w[0], u1 = odd ? w[1] : r01, v0 = odd ? r23 : w[2], v1 = odd ? w[3] : r23;
             const uint32_t g0 = __shfl_xor_sync(0xffffffffu, high ? u0 : v0, 2);
             const uint32_t g1 = __shfl_xor_sync(0xffffffffu, high ? u1 : v1, 2);
-            tc::st_async_v4(p_peer + k8 * 1024, high ? make_uint4(g0, g1, v0, v1) : make_uint4(u0, u1, g0, g1), peer_mbar(MB_PX));
+            if (alive) tc::st_async_v4(p_peer + k8 * 1024, high ? make_uint4(g0, g1, v0, v1) : make_uint4(u0, u1, g0, g1), peer_mbar(MB_PX));
           }
         }
         if (p_local) tc::fence_async_smem();   // (the peer's MMA warp fences the st.async bytes)
@@ -678,8 +682,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (quad == 0) {
         const float4 q4 = *reinterpret_cast<const float4*>(s_red + (eb + row) * 4);
         const float ls = (q4.x + q4.y) + (q4.z + q4.w);
-        tc::st_async_b32(tc::peer_addr(sbase + OFF_XSUM + row * 4, peer), __float_as_uint(ls), peer_mbar(MB_XS));
-        if (tid == 0) tc::mbar_arrive_expect(mbar(MB_XS), ROWS * 4);
+        if (*s_abort == 0) {
+          tc::st_async_b32(tc::peer_addr(sbase + OFF_XSUM + row * 4, peer), __float_as_uint(ls), peer_mbar(MB_XS));
+          if (tid == 0) tc::mbar_arrive_expect(mbar(MB_XS), ROWS * 4);
+        }
         wait_peer(mbar(MB_XS), static_cast<uint32_t>(k & 1), s_abort, p.err);
         // Both CTAs add the two halves in the same order.
         const float lo = rank == 0 ? ls : s_xsum[row];
@@ -736,16 +742,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   tc::fence_before_sync();
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  tc::fence_after_sync();
-  if (*s_abort != 0) {
-    const SharedPos end{range.z, range.w};
-    for (int tile = from.tile; next_segment(p, share, from, end, tile, s); tile = s.tile + 1)
-      write_nan_segment(p, s, cluster, rank, tid);
-  }
+  if (tid == 0 && s_abort[0] != 0) tc::st_cluster_b32(tc::peer_addr(smem_u32(s_tmem + 4), peer), 1);
   // Neither CTA leaves while the peer may still write into its shared
   // memory, signal its barriers or (even CTA) read its operands.
   tc::cluster_sync();
   tc::fence_after_sync();
+  if (s_abort[0] != 0 || s_abort[1] != 0) {   // the same in both CTAs
+    // Copies and stores under way land within microseconds: far longer than
+    // that.  And every MMA issued is done before tensor memory is freed.
+    settle(1LL << 22);
+    if (warp == MMA_WARP) {
+      if (rank == 0) tc::commit_pair(mbar(MB_DONE));
+      wait_drain(mbar(MB_DONE), 0, p.err);
+    }
+    const SharedPos end{range.z, range.w};
+    for (int tile = from.tile; next_segment(p, share, from, end, tile, s); tile = s.tile + 1)
+      write_nan_segment(p, s, cluster, rank, tid);
+    tc::cluster_sync();
+    tc::fence_after_sync();
+  }
   if (warp == MMA_WARP) tc::tmem_dealloc_pair<TMEM_COLS>(tmem);
 }
 

@@ -86,6 +86,7 @@ struct SharedParams {
   float* lse;                   // [B * R]
   int out_bf16;
   int* err;
+  int fault_rank;               // testing: the CTA of each pair that gives up in mid-call, -1 for none
   // Workspace.
   uint16_t* q16;                // fp16 [9][q_plane rows][64]
   long long q_plane;            // rows per plane
