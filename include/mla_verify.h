@@ -476,7 +476,8 @@ int mla_verify_compact_kv(mla_verify_plan* plan, int batch, const void* kv_src, 
  *   q            bf16 [num_tokens][H][576], the plan's H.
  *
  * Strides count elements and are multiples of 8 (16 bytes); 0 repeats a
- * vector.  Norm and rotation run in fp32 and are rounded to bf16 once.  A
+ * vector.  Norm and rotation run in fp32 (the sum of squares in other units
+ * where it would leave fp32's range) and are rounded to bf16 once.  A
  * slot outside the cache (MLA_VERIFY_DEV_BAD_SLOT) or a position outside the
  * table (MLA_VERIFY_DEV_BAD_POS) sets its bit and nothing of that token is
  * written.  num_tokens may be 0 and is not bounded by the plan's max_batch.
