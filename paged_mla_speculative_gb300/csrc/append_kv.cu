@@ -40,13 +40,15 @@ __device__ __forceinline__ uint32_t pack(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h);
 }
-// Granules read once by the whole call.  (Volatile, like the plain loads of
-// the rest: a read-only load could be moved above griddepcontrol.wait.)
+// Granules read once by the whole call.  (No read-only load: those are for
+// memory that nothing writes while the kernel runs, and this one is launched
+// while the kernel before it may still write its inputs.)
 __device__ __forceinline__ uint4 load_once(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return v;
 }
 

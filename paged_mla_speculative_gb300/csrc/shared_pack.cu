@@ -292,13 +292,15 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
 struct Rows {
   uint4 v[PER_THREAD];
 };
-// A granule that the call reads once.  (Volatile: a read-only load whose
-// address is known early could be moved above griddepcontrol.wait.)
+// A granule that the call reads once.  (No read-only load: those are for
+// memory that nothing writes while the kernel runs, and this one is launched
+// while the kernel before it may still write its inputs.)
 __device__ __forceinline__ uint4 load_once(const uint4* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return v;
 }
 // Row r of 32 (each THREADS / 8 granules apart) at src + s_row[r] * 576, or
