@@ -24,6 +24,7 @@
 // A page id outside the cache is reported (ERR_SLOT) and touches nothing; a
 // partial page outside the cache is copied as zeros.
 #include "common.cuh"
+#include "copy_ring.h"
 #include "kernels.h"
 #include "tc_ptx.cuh"
 
@@ -94,61 +95,45 @@ __device__ __forceinline__ Sums block_scan(Sums x, Sums* s_warp, Sums& all) {
   return x;
 }
 
-// One thread: `bytes` from src to dst for each layer l0, l0 + step, .., in
-// pieces that alternate between the two buffers, so that one is filled while
-// the other is written out.
-__device__ __forceinline__ void copy_layers(const ForkArgs& a, uint8_t* buf, uint32_t mbar, long long from, long long to,
-                                            int bytes, int l0, int step) {
-  const int pieces = (bytes + PIECE - 1) / PIECE;
-  const int total = (a.num_layers - l0 + step - 1) / step * pieces;
-  auto piece = [&](int i, const uint8_t*& src, uint8_t*& dst, int& size) {
-    const int off = i % pieces * PIECE;
-    uint8_t* layer = reinterpret_cast<uint8_t*>(a.kv_cache + static_cast<long long>(l0 + i / pieces * step) * a.layer_stride);
-    src = layer + from * PAGE * ROW_BYTES + off;
-    dst = layer + to * PAGE * ROW_BYTES + off;
+// The copy of `bytes` from page `from` to page `to` in each layer l0, l0 +
+// step, .., by one thread: the pieces of copy_through_two.
+struct LayerCopy {
+  const ForkArgs& a;
+  uint32_t buf, mbar;
+  long long from, to;
+  int bytes, l0, step;
+
+  __device__ __forceinline__ int pieces() const { return (bytes + PIECE - 1) / PIECE; }   // of a layer
+  __device__ __forceinline__ int total() const { return (a.num_layers - l0 + step - 1) / step * pieces(); }
+  // Piece i's first byte in the layer's page `page`, and its size.
+  __device__ __forceinline__ uint8_t* at(int i, long long page, int& size) const {
+    const int off = i % pieces() * PIECE;
     size = min(PIECE, bytes - off);
-  };
-  auto load = [&](int i) {
-    const uint8_t* src;
-    uint8_t* dst;
+    return reinterpret_cast<uint8_t*>(a.kv_cache + static_cast<long long>(l0 + i / pieces() * step) * a.layer_stride) +
+           page * PAGE * ROW_BYTES + off;
+  }
+  __device__ __forceinline__ void load(int i) {
     int size;
-    piece(i, src, dst, size);
+    const uint8_t* src = at(i, from, size);
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(mbar + 8 * (i & 1)), "r"(size) : "memory");
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                     smem_u32(buf) + (i & 1) * PIECE),
+                     buf + (i & 1) * PIECE),
                  "l"(src), "r"(size), "r"(mbar + 8 * (i & 1))
                  : "memory");
-  };
-  load(0);
-  for (int i = 0; i < total; ++i) {
-    if (i + 1 < total) {
-      // The other buffer is free once its last piece has been read out.
-      if (i) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
-      load(i + 1);
-    }
-    // (Past the limit the error is set, and the copy in flight gets as long
-    // again before the shared memory it lands in is given up.)
-    const long long t0 = clock64();
-    bool late = false;
-    while (!tc::mbar_try(mbar + 8 * (i & 1), (i >> 1) & 1)) {
-      if (!late && clock64() - t0 > COPY_LIMIT) {
-        atomicOr(a.err, ERR_TIMEOUT);
-        late = true;
-      }
-      if (late && clock64() - t0 > 2 * COPY_LIMIT) break;
-    }
-    if (late) break;
-    const uint8_t* src;
-    uint8_t* dst;
+  }
+  __device__ __forceinline__ bool landed(int i) { return tc::mbar_try(mbar + 8 * (i & 1), (i >> 1) & 1); }
+  __device__ __forceinline__ void store(int i) {
     int size;
-    piece(i, src, dst, size);
+    uint8_t* dst = at(i, to, size);
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\ncp.async.bulk.commit_group;\n" ::"l"(dst),
-                 "r"(smem_u32(buf) + (i & 1) * PIECE), "r"(size)
+                 "r"(buf + (i & 1) * PIECE), "r"(size)
                  : "memory");
   }
-  asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
-}
+  __device__ __forceinline__ void drain() { asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory"); }
+  __device__ __forceinline__ long long now() { return clock64(); }
+  __device__ __forceinline__ void late() { atomicOr(a.err, ERR_TIMEOUT); }
+};
 
 // grid (table_parts + copy_parts, children).  Every CTA scans all children's
 // counts itself (a few loads per thread), which gives its child's offsets and
@@ -248,7 +233,11 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
   if (to < 0 || to >= a.num_pages) return;             // reported with the table
   const int part = static_cast<int>(blockIdx.x) - table_parts, parts = static_cast<int>(gridDim.x) - table_parts;
   if (from >= 0 && from < a.num_pages) {
-    if (tid == 0) copy_layers(a, s_copy, smem_u32(s_mbar), from, to, partial * ROW_BYTES, part, parts);
+    if (tid == 0) {
+      LayerCopy copy{a, smem_u32(s_copy), smem_u32(s_mbar), from, to, partial * ROW_BYTES, part, parts};
+      copy_through_two(copy, copy.total(), COPY_LIMIT);
+      asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+    }
     return;
   }
   if (tid == 0) atomicOr(a.err, ERR_SLOT);
