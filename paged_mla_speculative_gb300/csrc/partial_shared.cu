@@ -189,6 +189,10 @@ __device__ __forceinline__ bool next_segment(const SharedParams& p, const Shared
   return false;
 }
 
+__device__ __forceinline__ void st_peer(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;\n" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+
 // NaN for every row of the segment (a pair that gave up), in the places that
 // this CTA's readout writes: value dims 256 t + 128 rank .., lse of its 64 rows.
 __device__ __forceinline__ void write_nan_segment(const SharedParams& p, const Segment& s, int cluster, uint32_t rank, int tid) {
@@ -742,7 +746,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   tc::fence_before_sync();
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  if (tid == 0 && s_abort[0] != 0) tc::st_cluster_b32(tc::peer_addr(smem_u32(s_tmem + 4), peer), 1);
+  if (tid == 0 && s_abort[0] != 0) st_peer(tc::peer_addr(smem_u32(s_tmem + 4), peer), 1);
   // Neither CTA leaves while the peer may still write into its shared
   // memory, signal its barriers or (even CTA) read its operands.
   tc::cluster_sync();
