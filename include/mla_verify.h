@@ -240,7 +240,11 @@ int mla_verify_plan_set_profile_events(mla_verify_plan* plan, void* after_pack,
 int mla_verify_plan_inject_fault(mla_verify_plan* plan, int fault);
 
 /* Bytes of device workspace the plan holds (partials, packed key blocks,
- * pack hand-off flags, error word). */
+ * pack hand-off flags, error word; and for mla_verify_attn_shared a 128-key
+ * block, 4 bytes per key of max_batch * max_kv_len and, if more than the
+ * partials of mla_verify_attn, two partials of 128 rows for each SM pair that
+ * a call can keep busy: 40 MB at most on 152 SMs; for mla_verify_free_kv a
+ * bit per page). */
 size_t mla_verify_plan_workspace_bytes(const mla_verify_plan* plan);
 
 /*

@@ -61,19 +61,20 @@ struct mla_verify_plan {
   cudaStream_t aux;
   // TMA descriptors of `packed` for the CTA-pair kernel.
   mlav::PackMaps pack_maps;
-  unsigned* page_bits;    // page_size 64: one bit per page of the cache (free_kv)
   // mla_verify_attn_shared: its packed keys and queries use `packed` and
   // `st_q`, its partials ws_o and ws_lse; meta words and the call's layout
-  // have their own memory.
+  // lie behind the packed keys.
   bool shared_ok;         // the packed key space has 32-bit positions
   long long k_plane;      // keys it holds
   int max_tiles;
   int* sh_meta;
   int* sh_layout;
+  unsigned* page_bits;    // free_kv, page_size 64: one bit per page of the cache, behind the error word
+  int sh_cut;             // clusters that can share a call's tiles
   mlav::SharedMaps sh_maps;
 };
 
-// The 256 bytes at mla_verify_plan::err: the error word, and fork_kv's ticket.
+// The first 256 bytes at mla_verify_plan::err: the error word, and fork_kv's ticket.
 constexpr int kTicketWord = 16;
 
 namespace {
@@ -100,6 +101,19 @@ long long ceil_div(long long a, long long b) { return (a + b - 1) / b; }
 
 // Clusters of the shared-prefix attention kernel: one per SM pair.
 int shared_clusters(const mla_verify_plan* pl) { return std::min(pl->num_sms / 2, mlav::SH_MAX_CLUSTERS); }
+
+// Clusters that can share the work of one of the plan's shared-prefix calls
+// (the kernel gives each SH_SEGMENT_COST + 2 steps at least), by an upper
+// bound of a call's cost: a tile's keys are at most its requests' own and
+// shared ones, in half blocks of which two may be ragged, and a request's
+// rows are in (R - 1) / SH_ROWS + 2 tiles at most.  1: no tile is ever cut.
+int shared_cut_clusters(const mla_verify_plan* pl) {
+  const long long B = pl->max_batch, R = pl->R;
+  const long long tiles = std::min(ceil_div(B * R, mlav::SH_ROWS) + B, B * ceil_div(R, mlav::SH_ROWS));
+  const double keys = static_cast<double>(B) * pl->max_kv_len * static_cast<double>((R - 1) / mlav::SH_ROWS + 2);
+  const double cost = static_cast<double>(tiles) * (1.5 + mlav::SH_SEGMENT_COST) + keys / (2 * mlav::SH_HALF);
+  return static_cast<int>(std::clamp(cost / (mlav::SH_SEGMENT_COST + 2), 1.0, static_cast<double>(shared_clusters(pl))));
+}
 
 // The layout arrays of a shared-prefix call, one after another in the plan's
 // sh_layout; returns the 32-bit words they take.
@@ -312,8 +326,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 
 void free_all(mla_verify_plan* p) {
   void* bufs[] = {p->ws_o, p->ws_lse, p->err, p->st_q, p->st_idx, p->st_indptr,
-                  p->st_lens, p->st_parent, p->st_out, p->st_lse, p->packed, p->pack_sync,
-                  p->page_bits, p->sh_meta, p->sh_layout};
+                  p->st_lens, p->st_parent, p->st_out, p->st_lse, p->packed, p->pack_sync};
   for (void* b : bufs)
     if (b) cudaFree(b);
 }
@@ -416,17 +429,24 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
   cap = std::max(cap, std::min(1LL * max_batch * std::min<long long>(mlav::MAX_NSPLIT, max_blocks),
                                std::max(floor_rs, std::min<long long>(mlav::MAX_NSPLIT, max_blocks))));
   pl->ws_capacity = cap;
-  // The shared-prefix kernel's partials: two tiles per cluster.
+  pl->pack_blocks = static_cast<int>(ceil_div(max_kv_len, 128));
+  pl->k_plane = (static_cast<long long>(max_batch) * pl->pack_blocks + 1) * 128;
+  pl->max_tiles = static_cast<int>(std::min<long long>(ceil_div(1LL * max_batch * pl->R, mlav::SH_ROWS) + max_batch, INT32_MAX));
+  pl->shared_ok = pl->k_plane <= INT32_MAX && 1LL * max_batch * pl->R <= INT32_MAX / 2 && max_batch < mlav::SH_MAX_BATCH;
+  // The shared-prefix kernel's partials: two tiles per cluster, where any are cut.
+  pl->sh_cut = pl->shared_ok ? shared_cut_clusters(pl) : 1;
   const size_t rows = std::max(static_cast<size_t>(cap) * pl->R,
-                               static_cast<size_t>(2 * shared_clusters(pl)) * mlav::SH_ROWS);
+                               pl->sh_cut > 1 ? static_cast<size_t>(2 * pl->sh_cut) * mlav::SH_ROWS : 0);
   const size_t out_elt = out_dtype == MLA_VERIFY_OUT_BF16 ? 2 : 4;
   const long long idx_per_req = page_size == 1 ? max_kv_len : ceil_div(max_kv_len, mlav::PAGE);
   pl->st_idx_cap = idx_per_req * max_batch;
   const size_t qrows = static_cast<size_t>(max_batch) * pl->R;
 
+  const size_t err_bytes = 256 + (page_size == mlav::PAGE ? static_cast<size_t>(ceil_div(num_slots / mlav::PAGE, 32)) * 4 : 0);
+
   bool ok = cudaMalloc(&pl->ws_o, rows * mlav::D_V * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&pl->ws_lse, rows * sizeof(float)) == cudaSuccess &&
-            cudaMalloc(&pl->err, 256) == cudaSuccess &&
+            cudaMalloc(&pl->err, err_bytes) == cudaSuccess &&
             cudaMalloc(&pl->st_q, qrows * mlav::ROW_BYTES) == cudaSuccess &&
             cudaMalloc(&pl->st_idx, static_cast<size_t>(pl->st_idx_cap) * 4) == cudaSuccess &&
             cudaMalloc(&pl->st_indptr, static_cast<size_t>(max_batch + 1) * 4) == cudaSuccess &&
@@ -434,30 +454,24 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
             cudaMalloc(&pl->st_parent, static_cast<size_t>(max_batch) * num_drafts * 4) == cudaSuccess &&
             cudaMalloc(&pl->st_out, qrows * mlav::D_V * out_elt) == cudaSuccess &&
             cudaMalloc(&pl->st_lse, qrows * sizeof(float)) == cudaSuccess;
-  pl->pack_blocks = static_cast<int>(ceil_div(max_kv_len, 128));
   // One block more than the requests': the tail of the shared-prefix call's
   // packed keys.
   const size_t packed_bytes =
       (static_cast<size_t>(max_batch) * pl->pack_blocks + 1) * mlav::packed_block_bytes();
-  pl->k_plane = (static_cast<long long>(max_batch) * pl->pack_blocks + 1) * 128;
-  pl->max_tiles = static_cast<int>(std::min<long long>(ceil_div(1LL * max_batch * pl->R, mlav::SH_ROWS) + max_batch, INT32_MAX));
-  pl->shared_ok = pl->k_plane <= INT32_MAX && 1LL * max_batch * pl->R <= INT32_MAX / 2 && max_batch < mlav::SH_MAX_BATCH;
-  ok = ok && cudaMalloc(&pl->packed, packed_bytes) == cudaSuccess;
+  // Behind it, in the same allocation, the shared-prefix call's meta words and layout.
+  mlav::SharedParams layout{};
+  const size_t shared_bytes = pl->shared_ok ? (static_cast<size_t>(pl->k_plane) + shared_layout(pl, &layout)) * 4 : 0;
+  ok = ok && cudaMalloc(&pl->packed, packed_bytes + shared_bytes) == cudaSuccess;
   ok = ok && mlav::make_pack_maps(&pl->pack_maps, pl->packed, packed_bytes) == cudaSuccess;
   const size_t sync_bytes =
       mlav::PACK_SYNC_HEADER * sizeof(unsigned) +
       static_cast<size_t>(max_batch) * pl->pack_blocks * 32 * sizeof(unsigned long long);
   ok = ok && cudaMalloc(&pl->pack_sync, sync_bytes) == cudaSuccess;
   pl->pack_sync_bytes = sync_bytes;
-  const size_t bit_bytes = page_size == mlav::PAGE ? static_cast<size_t>(ceil_div(num_slots / mlav::PAGE, 32)) * 4 : 0;
-  ok = ok && (!bit_bytes || cudaMalloc(&pl->page_bits, bit_bytes) == cudaSuccess);
-  size_t shared_bytes = 0;
-  if (pl->shared_ok) {
-    mlav::SharedParams sp{};
-    shared_bytes = static_cast<size_t>(pl->k_plane) * 4 + shared_layout(pl, &sp) * 4;
-    ok = ok && cudaMalloc(&pl->sh_meta, static_cast<size_t>(pl->k_plane) * 4) == cudaSuccess &&
-         cudaMalloc(&pl->sh_layout, shared_layout(pl, &sp) * 4) == cudaSuccess &&
-         mlav::make_shared_maps(&pl->sh_maps, pl->packed, pl->k_plane, pl->st_q, static_cast<long long>(qrows)) == cudaSuccess;
+  if (ok && pl->shared_ok) {
+    pl->sh_meta = reinterpret_cast<int*>(static_cast<uint8_t*>(pl->packed) + packed_bytes);
+    pl->sh_layout = pl->sh_meta + pl->k_plane;
+    ok = mlav::make_shared_maps(&pl->sh_maps, pl->packed, pl->k_plane, pl->st_q, static_cast<long long>(qrows)) == cudaSuccess;
   }
   if (!ok) {
     cudaGetLastError();
@@ -465,10 +479,9 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
     delete pl;
     return MLA_VERIFY_ERR_OOM;
   }
-  pl->ws_bytes = rows * (mlav::D_V + 1) * sizeof(float) + 256 + packed_bytes + sync_bytes + bit_bytes +
-                 shared_bytes;
-  if (cudaMemset(pl->err, 0, 256) != cudaSuccess || cudaMemset(pl->pack_sync, 0, sync_bytes) != cudaSuccess ||
-      (bit_bytes && cudaMemset(pl->page_bits, 0, bit_bytes) != cudaSuccess) ||
+  pl->ws_bytes = rows * (mlav::D_V + 1) * sizeof(float) + err_bytes + packed_bytes + sync_bytes + shared_bytes;
+  pl->page_bits = reinterpret_cast<unsigned*>(pl->err) + 64;
+  if (cudaMemset(pl->err, 0, err_bytes) != cudaSuccess || cudaMemset(pl->pack_sync, 0, sync_bytes) != cudaSuccess ||
       cudaEventCreateWithFlags(&pl->done_ev, cudaEventDisableTiming) != cudaSuccess ||
       cudaStreamCreateWithFlags(&pl->aux, cudaStreamNonBlocking) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
@@ -928,6 +941,7 @@ int mla_verify_attn_shared(mla_verify_plan* pl, int batch, const void* q, const 
   p.num_slots = pl->num_slots;
   p.max_kv_len = pl->max_kv_len;
   p.clusters = shared_clusters(pl);
+  p.cut_clusters = pl->sh_cut;
   p.max_tiles = static_cast<int>(ceil_div(1LL * batch * pl->R, mlav::SH_ROWS)) + num_groups;
   p.out = out;
   p.lse = lse;

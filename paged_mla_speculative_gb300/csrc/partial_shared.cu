@@ -775,11 +775,20 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
 }  // namespace
 
 cudaError_t make_shared_maps(SharedMaps* maps, void* k16, long long k_plane, void* q16, long long q_plane) {
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-  if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !fn) return e != cudaSuccess ? e : cudaErrorNotSupported;
-  const EncodeTiled encode = reinterpret_cast<EncodeTiled>(fn);
+  // (Looked up once per process: a look-up takes longer than the three maps.)
+  struct Encoder {
+    EncodeTiled fn;
+    cudaError_t e;
+  };
+  static const Encoder encoder = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    const bool found = e == cudaSuccess && q == cudaDriverEntryPointSuccess && fn;
+    return Encoder{reinterpret_cast<EncodeTiled>(fn), found ? cudaSuccess : e != cudaSuccess ? e : cudaErrorNotSupported};
+  }();
+  if (encoder.e != cudaSuccess) return encoder.e;
+  const EncodeTiled encode = encoder.fn;
   // Nine planes of rows of 64 fp16 (128 bytes), swizzled on the way in.
   auto planes = [&](CUtensorMap* map, void* base, long long rows, cuuint32_t box_rows, cuuint32_t box_planes) {
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 9};

@@ -81,6 +81,7 @@ struct SharedParams {
   int64_t num_slots;
   int max_kv_len;
   int clusters;                 // of the attention kernel
+  int cut_clusters;             // of them that may share tiles: those with partials
   int max_tiles;
   void* out;                    // fp32 or bf16 [B * R, 512]
   float* lse;                   // [B * R]
@@ -102,8 +103,8 @@ struct SharedParams {
   SharedTile* tiles;            // [max_tiles]
   SharedShare* share;           // [clusters]
   int* totals;                  // [0] packed keys, [1] tiles
-  float* part_o;                // [2 * clusters][128][512]
-  float* part_lse;              // [2 * clusters][128]
+  float* part_o;                // [2 * cut_clusters][128][512], none when that is 1
+  float* part_lse;              // [2 * cut_clusters][128]
 };
 
 // Partial slot of a segment: a cluster holds at most two tiles that others

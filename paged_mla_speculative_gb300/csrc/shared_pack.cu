@@ -244,7 +244,7 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
   // empty and no two start in one tile's leading cost.  Where every tile can
   // have a cluster of its own and the longest takes no more than an even
   // share, cut tiles starting twice, and the merge, tiles stay whole.
-  int used = max(1, min(p.clusters, total / (SH_SEGMENT_COST + 2)));
+  int used = max(1, min(p.cut_clusters, total / (SH_SEGMENT_COST + 2)));
   const bool whole = tiles <= p.clusters && s_max <= total / p.clusters + SH_SEGMENT_COST + SH_JOIN_COST;
   if (whole) used = tiles;
   for (int c = tid; c <= p.clusters; c += THREADS) {
