@@ -8,6 +8,7 @@ load, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -138,6 +139,17 @@ def _stream_ptr(stream) -> int:
     if stream is None:   # as torch.cuda.current_stream().cuda_stream, without building the object (3 us)
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _allocating_on(stream, device):
+    """Context in which torch allocates from ``stream``'s memory (the current
+    stream's for None), so that a call's own outputs are not written before
+    what their memory held last is read."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+    return torch.cuda.stream(stream)
 
 
 def _ptr(t: torch.Tensor) -> int:
@@ -460,7 +472,8 @@ def mla_verify_attn_shared(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_le
     Arguments of mla_verify_attn, and group_indptr [G + 1] / shared_lens [G]
     int32: requests group_indptr[g] .. group_indptr[g + 1] - 1 have the same
     first shared_lens[g] rows, which are read and scored once for all of them.
-    Enqueued on ``stream`` (default: the current torch stream); no sync.
+    Enqueued on ``stream`` (default: the current torch stream), whose memory
+    outputs that are not given come from; no sync.
     """
     B, G = q.shape[0], shared_lens.shape[0]
     dev = plan.torch_device
@@ -473,7 +486,8 @@ def mla_verify_attn_shared(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_le
     _expect(group_indptr, "group_indptr", torch.int32, dev, (G + 1,))
     _expect(shared_lens, "shared_lens", torch.int32, dev, (G,))
     if out is None or lse is None:
-        o2, l2 = plan.new_outputs(B)
+        with _allocating_on(stream, dev):
+            o2, l2 = plan.new_outputs(B)
         out = o2 if out is None else out
         lse = l2 if lse is None else lse
     _expect(out, "out", plan.out_dtype, dev, (B, plan.T, plan.H, 512))
@@ -497,8 +511,8 @@ def append_kv(plan: Plan, kv, weight, eps: float, cos_sin, positions, slots, kv_
     kv_cache [num_slots, 576] bf16.  q_pe [N, H, 64] bf16 by strides, q_nope
     [N, H, 512] bf16 by strides or None when q's first 512 dims hold it
     already, q [N, H, 576] bf16 out.  ``interleaved`` rotates neighbours
-    (2i, 2i + 1), otherwise the halves (i, i + 32).  Enqueued on ``stream``;
-    no sync.
+    (2i, 2i + 1), otherwise the halves (i, i + 32).  Enqueued on ``stream``,
+    whose memory a q that is not given comes from; no sync.
     """
     N = positions.shape[0]
     dev = plan.torch_device
@@ -519,7 +533,8 @@ def append_kv(plan: Plan, kv, weight, eps: float, cos_sin, positions, slots, kv_
         elif q is None:
             raise ValueError("without q_nope, q must hold the absorbed dims already")
         if q is None:
-            q = torch.empty((N, plan.H, 576), dtype=torch.bfloat16, device=dev)
+            with _allocating_on(stream, dev):
+                q = torch.empty((N, plan.H, 576), dtype=torch.bfloat16, device=dev)
         _expect(q, "q", torch.bfloat16, dev, (N, plan.H, 576))
     elif q_nope is not None or q is not None:
         raise ValueError("q and q_nope need q_pe")
@@ -553,7 +568,8 @@ def fork_kv(plan: Plan, parents, kv_indices, kv_indptr, kv_lens, kv_cache, page_
     page_refs / free_pages [num_slots / 64] and free_count [1] int32 are the
     page pool (counts, stack of free pages, its height).  child_indices
     defaults to C * (pages of max_kv_len) entries; its length is the capacity.
-    Page size 64 only.  Enqueued on ``stream``; no sync.
+    Page size 64 only.  Enqueued on ``stream``, whose memory outputs that are
+    not given come from; no sync.
     """
     C, P = parents.shape[0], kv_lens.shape[0]
     dev = plan.torch_device
@@ -565,12 +581,14 @@ def fork_kv(plan: Plan, parents, kv_indices, kv_indptr, kv_lens, kv_cache, page_
     layer = kv_cache if kv_cache.dim() == 2 else kv_cache[0]
     _expect(layer, "kv_cache", torch.bfloat16, dev, (plan.num_slots, 576))
     _expect_pool(plan, page_refs, free_pages, free_count)
-    if child_indices is None:
-        child_indices = torch.empty(C * -(-plan.max_kv_len // 64), dtype=torch.int32, device=dev)
-    if child_indptr is None:
-        child_indptr = torch.empty(C + 1, dtype=torch.int32, device=dev)
-    if child_lens is None:
-        child_lens = torch.empty(C, dtype=torch.int32, device=dev)
+    if child_indices is None or child_indptr is None or child_lens is None:
+        with _allocating_on(stream, dev):
+            if child_indices is None:
+                child_indices = torch.empty(C * -(-plan.max_kv_len // 64), dtype=torch.int32, device=dev)
+            if child_indptr is None:
+                child_indptr = torch.empty(C + 1, dtype=torch.int32, device=dev)
+            if child_lens is None:
+                child_lens = torch.empty(C, dtype=torch.int32, device=dev)
     _expect(child_indices, "child_indices", torch.int32, dev)
     _expect(child_indptr, "child_indptr", torch.int32, dev, (C + 1,))
     _expect(child_lens, "child_lens", torch.int32, dev, (C,))
