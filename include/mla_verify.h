@@ -42,7 +42,10 @@
  * in [2^-14, 65504] (smaller magnitudes keep an absolute error below 2^-25).
  * A gathered key or query value of magnitude 65536 or more (or NaN) has no
  * fp16 counterpart: the kernel that widens it sets MLA_VERIFY_DEV_RANGE and
- * the rows that read it come out inf or NaN.  The softmax runs in fp32.
+ * the rows that read it come out inf or NaN.  The softmax runs in fp32; its
+ * weights enter the second product in fp16, relative to the largest so far: a
+ * weight below 2^-14 of it is off by 2^-25 of it at most, one below 2^-25 is
+ * lost from out (and still counted in its denominator by TC and PAIR).
  *
  * Ownership: the caller owns every tensor.  The plan owns its workspace
  * (split partials), a device error word and, for mla_verify_attn_host, its
@@ -345,7 +348,9 @@ int mla_verify_combine_parts(mla_verify_plan* plan, int batch, int num_parts,
  * NaN (BAD_INDPTR).  A row that sees a key with a value outside the fp16
  * range (MLA_VERIFY_DEV_RANGE) comes out NaN; rows that do not see it are not
  * touched by it.  A bad slot among the shared rows is masked for the whole
- * group.  Plans with max_batch * max_kv_len of about 2^31 or more give
+ * group.  Numerics as above (keys and queries in fp16), but weights are held
+ * down to 2^-40 of a row's largest, 2^-29 with fp16's full precision.  Plans
+ * with max_batch * max_kv_len of about 2^31 or more give
  * MLA_VERIFY_ERR_SHAPE.  The split count, kernel and pack knobs and the
  * profiling events do not apply.  Otherwise as mla_verify_attn (capturable, no
  * allocation, the plan's workspace).

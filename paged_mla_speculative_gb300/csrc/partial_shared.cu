@@ -10,7 +10,8 @@
 //     S^T[key, row] = K_pair[256 x 576] . Q_tile[128 x 576]^T
 //     O^T[dim, row] += V_pair^T[512 x 256] . P^T[256 x 128]
 // with the running maximum and sum in fp32, P in fp16 (rounded once, 2^-11 of
-// every weight down to 2^-29 of the row's largest; see P_SHIFT),
+// every weight down to 2^-29 of the row's largest; see P_SHIFT), the bf16 keys
+// and queries in fp16 (exact from 2^-14 to 65504, off by less than 2^-25 below),
 // O^T in tensor memory, split by value dim over the two CTAs.
 //
 // What differs is the schedule.  The grid is one cluster per SM pair; cluster

@@ -72,3 +72,27 @@ def test_scores_beyond_the_exactness_of_fp32(sink, others):
     assert (np.abs(out.double().cpu().numpy() - ro) <= REL * np.abs(ro)).all()
     # the scaled score is rounded in units of log2 and again as lse
     assert (np.abs(lse.double().cpu().numpy() - rl) <= 2.0 ** -21 * np.maximum(1, np.abs(rl)) + 2.0 ** -16).all()
+
+
+@pytest.mark.parametrize("exponent", [-10, -18, -22, -27])
+def test_small_values_and_queries(exponent):
+    """bf16 holds magnitudes that fp16 does not: a key or query value keeps an
+    absolute error of 2^-25 (none from 2^-14 on), and one below that becomes 0.
+    Outputs are off by as much beside the rounding of P^T; scores by 2^-25 times
+    the 1-norm of the other side (below 576 * 4) and by the 36 fp32 additions of
+    16 products each, 2^-23 of a sum that is below 200 before the scale of 0.07."""
+    small = 2.0 ** exponent
+    inp, gp, sl = make([2], [900], [9, 40], 4, 16, seed=61, spike_frac=0.0)
+    cache = inp.kv_cache.clone()
+    cache[:, :512] = (cache[:, :512].float() * small).to(torch.bfloat16)
+    q = inp.q.clone()
+    q[:, 2:] = (q[:, 2:].float() * small).to(torch.bfloat16)
+    for case in ((dataclasses.replace(inp, kv_cache=cache), gp, sl), (dataclasses.replace(inp, q=q), gp, sl)):
+        with G.make_plan(case[0]) as plan:
+            out, lse = run(plan, *case)
+            assert plan.get_error() == 0
+        ro, rl = G.oracle_full(case[0])
+        big = float(case[0].kv_cache[case[0].kv_indices.long(), :512].double().abs().max())   # (other rows hold NaN)
+        score = (2.0 ** -25 * 576 * 4 + 36 * 2.0 ** -23 * 200) * abs(case[0].scale)
+        assert (np.abs(lse.double().cpu().numpy() - rl) <= score + 2.0 ** -20).all()
+        assert (np.abs(out.double().cpu().numpy() - ro) <= 2.0 ** -25 + (2.0 ** -11 + 2 * score + 2.0 ** -14) * big).all()
