@@ -494,7 +494,7 @@ def mla_verify_attn_shared(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_le
     _expect(lse, "lse", torch.float32, dev, (B, plan.T, plan.H))
     st = load_library().mla_verify_attn_shared(
         plan.handle, B, q.data_ptr(), kv_cache.data_ptr(), kv_indices.data_ptr(),
-        kv_indptr.data_ptr(), kv_lens.data_ptr(), draft_parent.data_ptr(), float(scale), G,
+        kv_indptr.data_ptr(), kv_lens.data_ptr(), draft_parent.data_ptr(), scale, G,
         group_indptr.data_ptr(), shared_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
         _stream_ptr(stream))
     _check(st, "mla_verify_attn_shared")
@@ -539,7 +539,7 @@ def append_kv(plan: Plan, kv, weight, eps: float, cos_sin, positions, slots, kv_
     elif q_nope is not None or q is not None:
         raise ValueError("q and q_nope need q_pe")
     st = load_library().mla_verify_append_kv(
-        plan.handle, N, kv.data_ptr(), kv_stride, weight.data_ptr(), float(eps), nope, nope_strides[0],
+        plan.handle, N, kv.data_ptr(), kv_stride, weight.data_ptr(), eps, nope, nope_strides[0],
         nope_strides[1], pe, pe_strides[0], pe_strides[1], cos_sin.data_ptr(), cos_sin.shape[0],
         positions.data_ptr(), slots.data_ptr(), ROPE_PAIRS if interleaved else ROPE_HALVES,
         kv_cache.data_ptr(), q.data_ptr() if q is not None else None, _stream_ptr(stream))
@@ -595,7 +595,7 @@ def fork_kv(plan: Plan, parents, kv_indices, kv_indptr, kv_lens, kv_cache, page_
     st = load_library().mla_verify_fork_kv(
         plan.handle, C, parents.data_ptr(), P, kv_indices.data_ptr(), kv_indptr.data_ptr(),
         kv_lens.data_ptr(), kv_cache.data_ptr(), layers, kv_cache.stride(0) if layers > 1 else 0,
-        int(extra_rows), page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+        extra_rows, page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
         child_indices.data_ptr(), child_indices.numel(), child_indptr.data_ptr(),
         child_lens.data_ptr(), _stream_ptr(stream))
     _check(st, "mla_verify_fork_kv")
