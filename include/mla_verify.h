@@ -490,7 +490,7 @@ int mla_verify_compact_kv(mla_verify_plan* plan, int batch, const void* kv_src, 
  * slot outside the cache (MLA_VERIFY_DEV_BAD_SLOT) or a position outside the
  * table (MLA_VERIFY_DEV_BAD_POS) sets its bit and nothing of that token is
  * written.  num_tokens may be 0 and is not bounded by the plan's max_batch.
- * MLA_VERIFY_ERR_ARG for num_tokens < 0, max_pos < 1, a stride that is
+ * MLA_VERIFY_ERR_ARG for num_tokens outside [0, 2^31), max_pos < 1, a stride that is
  * negative or not a multiple of 8, a bad eps or rope style; other errors as
  * for mla_verify_attn.  Capturable; allocates nothing.
  */

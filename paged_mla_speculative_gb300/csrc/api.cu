@@ -980,7 +980,7 @@ int mla_verify_append_kv(mla_verify_plan* pl, int64_t num_tokens, const void* kv
       (q_pe && (!aligned16(q_pe) || !aligned16(q) || !aligned16(q_nope))))
     return MLA_VERIFY_ERR_ALIGN;
   auto bad_stride = [](int64_t s) { return s < 0 || s % 8; };
-  if (num_tokens < 0 || max_pos < 1 || bad_stride(kv_stride) || !(eps >= 0.f) || !std::isfinite(eps) ||
+  if (num_tokens < 0 || num_tokens > INT32_MAX || max_pos < 1 || bad_stride(kv_stride) || !(eps >= 0.f) || !std::isfinite(eps) ||
       (rope_style != MLA_VERIFY_ROPE_PAIRS && rope_style != MLA_VERIFY_ROPE_HALVES) ||
       (q_pe && (bad_stride(pe_stride_token) || bad_stride(pe_stride_head))) ||
       (q_pe && q_nope && (bad_stride(nope_stride_token) || bad_stride(nope_stride_head))))
