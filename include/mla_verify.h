@@ -548,8 +548,9 @@ int mla_verify_append_kv(mla_verify_plan* plan, int64_t num_tokens, const void* 
  * 64] (CAPACITY) frees nothing.
  *
  * MLA_VERIFY_ERR_SHAPE when the plan's page_size is not 64; MLA_VERIFY_ERR_ARG
- * for num_layers < 1, a layer_stride that is negative or not a multiple of 8,
- * extra_rows outside [0, max_kv_len] or capacity outside [0, 2^31); other
+ * for num_layers outside [1, 65536], a layer_stride that is negative, not a
+ * multiple of 8 or, with several layers, below num_slots * 576 (the layers
+ * would overlap), extra_rows outside [0, max_kv_len] or capacity outside [0, 2^31); other
  * errors as for mla_verify_attn.  Both are capturable, allocate nothing, and
  * share the plan's workspace like every call.
  */

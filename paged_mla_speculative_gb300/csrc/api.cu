@@ -1031,7 +1031,8 @@ int mla_verify_fork_kv(mla_verify_plan* pl, int num_children, const int32_t* par
   if (pl->page_size != mlav::PAGE) return MLA_VERIFY_ERR_SHAPE;
   if (num_children < 1 || num_children > std::min(pl->max_batch, 65535) || num_parents < 1 || num_parents > pl->max_batch)
     return MLA_VERIFY_ERR_BATCH;
-  if (num_layers < 1 || layer_stride < 0 || layer_stride % 8 || extra_rows < 0 ||
+  if (num_layers < 1 || num_layers > mlav::FORK_MAX_LAYERS || layer_stride < 0 || layer_stride % 8 ||
+      (num_layers > 1 && layer_stride < pl->num_slots * mlav::D_QK) || extra_rows < 0 ||
       extra_rows > pl->max_kv_len || capacity < 0 || capacity > INT32_MAX)
     return MLA_VERIFY_ERR_ARG;
   const int dev_status = check_device(pl);

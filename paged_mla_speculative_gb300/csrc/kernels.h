@@ -156,6 +156,7 @@ struct AppendArgs {
 cudaError_t launch_append_kv(const AppendArgs& a, cudaStream_t stream);
 
 // Forking and freeing requests of a cache with counted pages (page_pool.cu).
+constexpr int FORK_MAX_LAYERS = 1 << 16;   // pieces of a copy are counted in 32 bits
 struct ForkArgs {
   const int32_t* parents;           // [num_children]
   int num_children, num_parents;
