@@ -96,3 +96,13 @@ def test_small_values_and_queries(exponent):
         score = (2.0 ** -25 * 576 * 4 + 36 * 2.0 ** -23 * 200) * abs(case[0].scale)
         assert (np.abs(lse.double().cpu().numpy() - rl) <= score + 2.0 ** -20).all()
         assert (np.abs(out.double().cpu().numpy() - ro) <= 2.0 ** -25 + (2.0 ** -11 + 2 * score + 2.0 ** -14) * big).all()
+
+
+@pytest.mark.parametrize("scale", [-0.07, 0.0, -0.0, 1e-30])
+def test_negative_and_vanishing_scales(scale):
+    inp, gp, sl = make([2, 1], [600, 100], [9, 300, 40], 4, 16, seed=62, spike_frac=0.0)
+    case = (dataclasses.replace(inp, scale=scale), gp, sl)
+    with G.make_plan(inp) as plan:
+        out, lse = run(plan, *case)
+        assert plan.get_error() == 0
+    G.assert_parity(out.cpu().numpy(), lse.cpu().numpy(), *G.oracle_full(case[0]))
