@@ -353,7 +353,8 @@ int mla_verify_combine_parts(mla_verify_plan* plan, int batch, int num_parts,
  * with max_batch * max_kv_len of about 2^31 or more give
  * MLA_VERIFY_ERR_SHAPE.  The split count, kernel and pack knobs and the
  * profiling events do not apply.  Otherwise as mla_verify_attn (capturable, no
- * allocation, the plan's workspace).
+ * allocation, the plan's workspace).  With less than some 16 000 rows in all
+ * the requests' tables mla_verify_attn is as fast or faster.
  */
 int mla_verify_attn_shared(mla_verify_plan* plan, int batch, const void* q, const void* kv_cache,
                            const int32_t* kv_indices, const int32_t* kv_indptr,
