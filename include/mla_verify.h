@@ -363,6 +363,44 @@ int mla_verify_attn_shared(mla_verify_plan* plan, int batch, const void* q, cons
                            const int32_t* shared_lens, void* out, float* lse, void* stream);
 
 /*
+ * Causal attention of chunks of new tokens: request b's tokens
+ * q_indptr[b] .. q_indptr[b+1] - 1, c_b of them (any number, 0 too), whose own
+ * rows are the last c_b of its n_b = kv_lens[b] cached rows.  Token i of the
+ * request sees its rows 0 .. n_b - c_b + i:
+ *
+ *     s_j = scale * dot(q[q_indptr[b] + i, h, 0:576], k_j[0:576]),  j <= n_b - c_b + i
+ *     lse = log(sum exp(s_j)),  out = sum exp(s_j - lse) * k_j[0:512]
+ *
+ * A prompt prefilled piece by piece, beside requests that decode one token.
+ *
+ *   q         bf16  [num_tokens][H][576], the plan's H; T does not apply.
+ *   q_indptr  int32 [batch + 1]: not decreasing, 0 <= q_indptr[0],
+ *             q_indptr[batch] <= num_tokens.  Tokens before q_indptr[0] and from
+ *             q_indptr[batch] on (padding) are not read, and nothing is written
+ *             for them.
+ *   out       fp32 or bf16 [num_tokens][H][512] (plan's out_dtype)
+ *   lse       fp32 [num_tokens][H]
+ *
+ * kv_indices, kv_indptr and kv_lens as for mla_verify_attn, with c_b <= n_b <=
+ * max_kv_len; a request without new tokens is not read.  A request whose length
+ * or table is out of order comes out NaN (MLA_VERIFY_DEV_BAD_LEN / BAD_INDPTR); a
+ * q_indptr that is out of order makes all num_tokens tokens NaN (BAD_INDPTR).
+ * Bad slots are masked (BAD_SLOT); a token none of whose keys is left has out 0
+ * and lse -inf.  Values outside the fp16 range (MLA_VERIFY_DEV_RANGE) make the
+ * rows that see them NaN and touch no others.  Numerics as for
+ * mla_verify_attn_shared.  num_tokens may be 0 and is not bounded by the plan
+ * (no workspace grows with it); num_tokens * H below 2^31, else
+ * MLA_VERIFY_ERR_ARG.  Plans that mla_verify_attn_shared refuses give
+ * MLA_VERIFY_ERR_SHAPE.  Otherwise as mla_verify_attn (capturable with q at
+ * the same address, no allocation, the plan's workspace).
+ */
+int mla_verify_attn_chunk(mla_verify_plan* plan, int batch, int64_t num_tokens, const void* q,
+                          const void* kv_cache, const int32_t* kv_indices,
+                          const int32_t* kv_indptr, const int32_t* kv_lens,
+                          const int32_t* q_indptr, float scale, void* out, float* lse,
+                          void* stream);
+
+/*
  * Read the sticky device error word (MLA_VERIFY_DEV_* bits) into
  * *device_status; clear it when `clear` is nonzero.  Waits for the plan's
  * last eagerly launched call (an event the plan records at the end of every

@@ -87,6 +87,8 @@ SIGNATURES = {
                                    ctypes.c_int64, _P, _P, _P]),
     "mla_verify_attn_shared": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, ctypes.c_float, _I, _P, _P, _P, _P,
                                     _P]),
+    "mla_verify_attn_chunk": (_I, [_P, _I, ctypes.c_int64, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P,
+                                   _P]),
     "mla_verify_append_kv": (_I, [_P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_float, _P,
                                   ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64,
                                   ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _I, _P, _P, _P]),
@@ -498,6 +500,44 @@ def mla_verify_attn_shared(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_le
         group_indptr.data_ptr(), shared_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
         _stream_ptr(stream))
     _check(st, "mla_verify_attn_shared")
+    return out, lse
+
+
+def mla_verify_attn_chunk(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_lens, q_indptr,
+                          scale: float, out=None, lse=None, stream=None):
+    """Causal attention of chunks of new tokens; returns (out, lse).
+
+    q [N, H, 576] bf16 holds the tokens of all requests, those of request b at
+    q_indptr[b] .. q_indptr[b + 1] - 1 (q_indptr [B + 1] int32; any number of
+    them, 0 too); their own rows are the last of the request's kv_lens[b]
+    cached rows, and token i of c sees rows 0 .. kv_lens[b] - c + i.
+    kv_cache, kv_indices, kv_indptr, kv_lens as for mla_verify_attn; out
+    [N, H, 512] (plan's dtype), lse [N, H] fp32.  Tokens outside q_indptr are
+    padding: nothing is written for them.  Enqueued on ``stream`` (default:
+    the current torch stream), whose memory outputs that are not given come
+    from; no sync.
+    """
+    N, B = q.shape[0], kv_lens.shape[0]
+    dev = plan.torch_device
+    _expect(q, "q", torch.bfloat16, dev, (N, plan.H, 576))
+    _expect(kv_cache, "kv_cache", torch.bfloat16, dev, (plan.num_slots, 576))
+    _expect(kv_indices, "kv_indices", torch.int32, dev)
+    _expect(kv_indptr, "kv_indptr", torch.int32, dev, (B + 1,))
+    _expect(kv_lens, "kv_lens", torch.int32, dev, (B,))
+    _expect(q_indptr, "q_indptr", torch.int32, dev, (B + 1,))
+    if out is None or lse is None:
+        with _allocating_on(stream, dev):
+            if out is None:
+                out = torch.empty((N, plan.H, 512), dtype=plan.out_dtype, device=dev)
+            if lse is None:
+                lse = torch.empty((N, plan.H), dtype=torch.float32, device=dev)
+    _expect(out, "out", plan.out_dtype, dev, (N, plan.H, 512))
+    _expect(lse, "lse", torch.float32, dev, (N, plan.H))
+    st = load_library().mla_verify_attn_chunk(
+        plan.handle, B, N, q.data_ptr(), kv_cache.data_ptr(), kv_indices.data_ptr(),
+        kv_indptr.data_ptr(), kv_lens.data_ptr(), q_indptr.data_ptr(), scale, out.data_ptr(),
+        lse.data_ptr(), _stream_ptr(stream))
+    _check(st, "mla_verify_attn_chunk")
     return out, lse
 
 

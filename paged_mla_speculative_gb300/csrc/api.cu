@@ -115,7 +115,7 @@ int shared_cut_clusters(const mla_verify_plan* pl) {
   return static_cast<int>(std::clamp(cost / (mlav::SH_SEGMENT_COST + 2), 1.0, static_cast<double>(shared_clusters(pl))));
 }
 
-// The layout arrays of a shared-prefix call, one after another in the plan's
+// The layout arrays of a shared-prefix or chunk call, one after another in the plan's
 // sh_layout; returns the 32-bit words they take.
 size_t shared_layout(const mla_verify_plan* pl, mlav::SharedParams* p) {
   size_t at = 0;
@@ -129,11 +129,12 @@ size_t shared_layout(const mla_verify_plan* pl, mlav::SharedParams* p) {
   p->source = take(B);
   p->own = take(B);
   p->anc = reinterpret_cast<uint32_t*>(take(B * pl->T));
-  p->tile0 = take(B);
+  p->tile0 = take(B + 1);
   p->cost = take(tiles + 1);
   p->tiles = reinterpret_cast<mlav::SharedTile*>(take(tiles * sizeof(mlav::SharedTile) / 4));
   p->share = reinterpret_cast<mlav::SharedShare*>(take(static_cast<size_t>(shared_clusters(pl)) * sizeof(mlav::SharedShare) / 4));
-  p->totals = take(2);
+  p->totals = take(3);
+  p->chunk_cost = reinterpret_cast<long long*>(take(2 * (B + 1)));
   return at;
 }
 
@@ -960,6 +961,59 @@ int mla_verify_attn_shared(mla_verify_plan* pl, int batch, const void* q, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (mlav::launch_shared_prepare(p, pl->num_sms, s) != cudaSuccess ||
       mlav::launch_partial_shared(p, pl->sh_maps, s) != cudaSuccess || mlav::launch_shared_join(p, s) != cudaSuccess ||
+      note_done(pl, s) != cudaSuccess)
+    return MLA_VERIFY_ERR_CUDA;
+  return MLA_VERIFY_OK;
+}
+
+int mla_verify_attn_chunk(mla_verify_plan* pl, int batch, int64_t num_tokens, const void* q, const void* kv_cache,
+                          const int32_t* kv_indices, const int32_t* kv_indptr, const int32_t* kv_lens,
+                          const int32_t* q_indptr, float scale, void* out, float* lse, void* stream) {
+  if (!pl) return MLA_VERIFY_ERR_NULL;
+  if (num_tokens == 0) return check_device(pl);
+  if (!q || !kv_cache || !kv_indices || !kv_indptr || !kv_lens || !q_indptr || !out || !lse) return MLA_VERIFY_ERR_NULL;
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(kv_indices) || !aligned16(kv_indptr) || !aligned16(kv_lens) ||
+      !aligned16(q_indptr) || !aligned16(out) || !aligned16(lse))
+    return MLA_VERIFY_ERR_ALIGN;
+  if (!pl->shared_ok) return MLA_VERIFY_ERR_SHAPE;
+  if (batch < 1 || batch > pl->max_batch) return MLA_VERIFY_ERR_BATCH;
+  if (!std::isfinite(scale)) return MLA_VERIFY_ERR_SCALE;
+  if (num_tokens < 0 || num_tokens > INT32_MAX / pl->H) return MLA_VERIFY_ERR_ARG;
+  const int dev_status = check_device(pl);
+  if (dev_status != MLA_VERIFY_OK) return dev_status;
+  mlav::SharedParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.kv = static_cast<const uint16_t*>(kv_cache);
+  p.kv_indices = kv_indices;
+  p.kv_indptr = kv_indptr;
+  p.kv_lens = kv_lens;
+  p.q_indptr = q_indptr;
+  p.num_tokens = static_cast<int>(num_tokens);
+  p.scale_log2 = scale * mlav::kLog2e;
+  p.batch = batch;
+  p.H = pl->H;
+  p.page_size = pl->page_size;
+  p.num_slots = pl->num_slots;
+  p.max_kv_len = pl->max_kv_len;
+  p.clusters = shared_clusters(pl);
+  p.cut_clusters = pl->sh_cut;
+  p.out = out;
+  p.lse = lse;
+  p.out_bf16 = pl->out_dtype == MLA_VERIFY_OUT_BF16;
+  p.err = pl->err;
+  p.fault_rank = pl->fault == MLA_VERIFY_FAULT_EVEN_GIVES_UP ? 0 : pl->fault == MLA_VERIFY_FAULT_ODD_GIVES_UP ? 1 : -1;
+  pl->fault = MLA_VERIFY_FAULT_NONE;
+  p.k16 = static_cast<uint16_t*>(pl->packed);
+  p.k_plane = pl->k_plane;
+  p.meta = pl->sh_meta;
+  shared_layout(pl, &p);
+  p.part_o = pl->ws_o;
+  p.part_lse = pl->ws_lse;
+  mlav::SharedMaps maps = pl->sh_maps;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (mlav::make_chunk_query_map(&maps.q, q, num_tokens * pl->H) != cudaSuccess ||
+      mlav::launch_chunk_prepare(p, pl->num_sms, s) != cudaSuccess ||
+      mlav::launch_partial_shared(p, maps, s) != cudaSuccess || mlav::launch_chunk_join(p, s) != cudaSuccess ||
       note_done(pl, s) != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
   return MLA_VERIFY_OK;

@@ -131,6 +131,13 @@ cudaError_t partial_shared_prepare();
 cudaError_t launch_shared_prepare(const SharedParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_partial_shared(const SharedParams& p, const SharedMaps& maps, cudaStream_t stream);
 cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream);
+// Attention of chunks of new tokens (SharedParams::q_indptr set): the layout
+// with the packed keys, launch_partial_shared with maps.q from
+// make_chunk_query_map (the other maps are those of the shared-prefix call),
+// the merge.
+cudaError_t make_chunk_query_map(CUtensorMap* map, const void* q, long long rows);
+cudaError_t launch_chunk_prepare(const SharedParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_chunk_join(const SharedParams& p, cudaStream_t stream);
 
 // New tokens' cache rows and queries (append_kv.cu).
 struct AppendArgs {

@@ -26,6 +26,12 @@
 // A tile that one cluster holds whole is normalised and stored directly;
 // otherwise the segment's partial goes to the workspace for shared_join_kernel.
 //
+// CAUSAL: the attention of chunks of new tokens (chunk_pack.cu).  Tiles follow
+// from the lengths, so there are no records of them; the mask is causal; and
+// the queries, of which a chunk may have gigabytes, are not widened ahead of
+// the kernel but where a tile's land in shared memory, in place, by the
+// softmax warps while the last O^T of the tile before is computed.
+//
 // Roles (20 warps per CTA): warps 0-15 softmax, warp 16 MMA issue (even CTA)
 // or P^T hand-off (odd CTA), warps 17-19 the key ring (17 the queries too).
 // Every wait is bounded.  A CTA whose wait runs out arms and sends nothing any
@@ -84,6 +90,7 @@ constexpr int MB_QE = 15;      // the segment's last S^T is done: its queries ca
 constexpr int MB_X = 20;       // [2][4] the peer's row maxima of the step and row group landed (st.async bytes)
 constexpr int MB_XS = 16;      // the peer's row sums landed (st.async bytes)
 constexpr int MB_DONE = 17;    // after an abort: every MMA issued is done
+constexpr int MB_QW = 18;      // CAUSAL, even CTA: both halves of a segment's queries are widened (MB_Q: this CTA's half landed)
 
 constexpr int TMEM_COLS = 512;
 constexpr uint32_t TM_S = 256;                  // S^T buffer u at 256 + 128u; O^T tile t at 128t
@@ -172,14 +179,21 @@ struct Segment {
 __device__ __forceinline__ SharedTile load_tile(const SharedTile* rec) {
   const int4* q = reinterpret_cast<const int4*>(rec);
   const int4 a = q[0], b = q[1], c = q[2];
-  return SharedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, {0, 0}};
+  return SharedTile{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
 }
 // The cluster's next segment at or after tile `tile`; false when there is none.
+template <bool CAUSAL>
 __device__ __forceinline__ bool next_segment(const SharedParams& p, const SharedShare* share, const SharedPos& from,
                                              const SharedPos& to, int tile, Segment& s) {
   for (; tile < to.tile || (tile == to.tile && to.step > 0); ++tile) {
     s.first = tile == from.tile;
-    s.t = load_tile(s.first ? &share->first : p.tiles + tile);
+    if (CAUSAL && !s.first) {
+      int b = s.t.own_base;   // of the tile before
+      while (p.tile0[b + 1] <= tile) ++b;
+      s.t = chunk_tile(p, b, tile - p.tile0[b], p.base[b]);
+    } else {
+      s.t = load_tile(s.first ? &share->first : p.tiles + tile);
+    }
     s.tile = tile;
     s.sa = s.first ? from.step : 0;
     const bool ends = tile == to.tile;
@@ -209,6 +223,39 @@ __device__ __forceinline__ void write_nan_segment(const SharedParams& p, const S
   }
 }
 
+// A pair of fp16 values, those that are no numbers made NaN.
+__device__ __forceinline__ uint32_t nan_for_inf(uint32_t w) {
+  return w | ((w & 0x7c00u) == 0x7c00u ? 0x200u : 0u) | ((w & 0x7c000000u) == 0x7c000000u ? 0x2000000u : 0u);
+}
+
+// CAUSAL: this CTA's half of a tile's queries (rows 64 rank .. of the tile),
+// just landed as bf16, widened to fp16 where it lies, by the softmax warps.
+// The elements stay where they are, so the swizzle does not matter.
+__device__ __forceinline__ void widen_queries(uint8_t* q, int rows, int tid, int* err) {
+  constexpr int THREADS = SOFTMAX_WARPS * 32, PER = 9 * Q_CHUNK / 16 / THREADS, FLIGHT = 3;
+  static_assert(PER * THREADS * 16 == 9 * Q_CHUNK && PER % FLIGHT == 0, "even split");
+  bool out_of_range = false;
+#pragma unroll 1
+  for (int u0 = 0; u0 < PER; u0 += FLIGHT) {
+    uint4 v[FLIGHT];
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) v[u] = reinterpret_cast<const uint4*>(q)[tid + (u0 + u) * THREADS];
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u) {
+      const int e = tid + (u0 + u) * THREADS;
+      bool bad = false;
+      uint4 w = widen_bf16x8(v[u], bad);
+      if (bad) {   // NaN, so that no score of the row is a number (an infinity might pass for a masked key)
+        w.x = nan_for_inf(w.x), w.y = nan_for_inf(w.y), w.z = nan_for_inf(w.z), w.w = nan_for_inf(w.w);
+        out_of_range |= (e >> 3) % HROWS < rows;   // (rows behind the tile's are not its own)
+      }
+      reinterpret_cast<uint4*>(q)[e] = w;
+    }
+  }
+  report_range(out_of_range, err);
+}
+
+template <bool CAUSAL>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     partial_shared_kernel(const SharedParams p, const __grid_constant__ CUtensorMap tm_pair,
                           const __grid_constant__ CUtensorMap tm_chunk, const __grid_constant__ CUtensorMap tm_q) {
@@ -232,7 +279,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   auto mbar = [&](int i) { return mbar0 + 8u * static_cast<uint32_t>(i); };
 
   if (tid == 0) {
-    for (int i = 0; i < NMBAR; ++i) tc::mbar_init(mbar(i), i == MB_P ? SOFTMAX_WARPS : 1);
+    for (int i = 0; i < NMBAR; ++i)
+      tc::mbar_init(mbar(i), i == MB_P ? SOFTMAX_WARPS : CAUSAL && i == MB_QW ? 2 * SOFTMAX_WARPS : 1);
     tc::mbar_fence_init();
     s_abort[0] = s_abort[1] = 0;
   }
@@ -271,9 +319,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const int cw = warp - COPY_WARP;
     const uint32_t absent_word = tc::peer_addr(smem_u32(s_tmem + 2), 0);
     int n = 0, g0 = 0, k = 0;   // units and segments so far, steps of the segments before
+    // CAUSAL: a CTA's own queries, for its own softmax warps.
+    auto load_queries = [&](int row0) {
+      if (lane == 0) tc::mbar_arrive_expect(mbar(MB_Q), 9 * Q_CHUNK);
+      __syncwarp();
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
-      if (cw == 0) {
+      for (int z = 0; z < 9; ++z)
+        tc::tma_load_2d(sbase + OFF_Q + z * Q_CHUNK, &tm_q, 64 * z, row0 + static_cast<int>(rank) * HROWS, mbar(MB_Q));
+    };
+    Segment ahead;
+    ahead.t.own_base = 0;
+#pragma unroll 1
+    for (int tile = from.tile; next_segment<CAUSAL>(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
+      if (CAUSAL) {
+        if (cw == 0 && k == 0) load_queries(s.t.q_row0);
+      } else if (cw == 0) {
         // The tile's queries, once the last S^T of the segment before is done
         // (its O^T units, already under way, come after it).  Rows past the
         // tile are the next tile's (or zeros past the batch): their columns
@@ -296,6 +356,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         phase_of(f, s.steps, is_s, i);
         const int hb0 = 2 * (s.sa + i);
         int count;
+        if (CAUSAL && cw == 0 && f == 2 * s.steps - 1) {
+          // The next tile's queries, as soon as the last S^T of this one is
+          // done: its last O^T units, next in order, would wait for that too.
+          ahead.t = s.t;
+          if (next_segment<CAUSAL>(p, share, from, to, s.tile + 1, ahead)) {
+            wait_own(mbar(MB_QE), static_cast<uint32_t>(k & 1), s_abort, p.err);
+            if (*s_abort) break;
+            load_queries(ahead.t.q_row0);
+          }
+        }
 #pragma unroll 1
         for (int u = 0; u < 4; ++u, ++n) {
           const int slot = n % NSLOT;
@@ -348,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const uint32_t even_word = tc::peer_addr(smem_u32(s_word), 0);
     int g = 0;
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1) {
+    for (int tile = from.tile; next_segment<CAUSAL>(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1) {
 #pragma unroll 1
       for (int i = 0; i < s.steps && !*s_abort; ++i, ++g) {
         if (lane == 0) tc::mbar_arrive_expect(mbar(MB_PX), CHUNK);
@@ -365,8 +435,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     // ======================= MMA issuer (even CTA) ==========================
     int n = 0, g0 = 0, k = 0;
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
-      wait_own(mbar(MB_Q), static_cast<uint32_t>(k & 1), s_abort, p.err);
+    for (int tile = from.tile; next_segment<CAUSAL>(p, share, from, to, tile, s) && !*s_abort; tile = s.tile + 1, g0 += s.steps, ++k) {
+      if (CAUSAL) wait_peer(mbar(MB_QW), static_cast<uint32_t>(k & 1), s_abort, p.err);
+      else wait_own(mbar(MB_Q), static_cast<uint32_t>(k & 1), s_abort, p.err);
+      if (CAUSAL) tc::fence_async_smem();
       tc::fence_after_sync();
 #pragma unroll 1
       for (int f = 0; f < 2 * s.steps && !*s_abort; ++f) {
@@ -467,8 +539,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
     const uint32_t red_off = (row * 4 + quad) * 4;   // this warp's maximum of the lane's row
     const uint32_t xred_peer = tc::peer_addr(sbase + OFF_XRED + red_off, peer);
     int g = 0, k = 0;   // steps and segments so far
+    // CAUSAL: segment `seg`'s queries, landed in this CTA, made fp16.
+    auto take_queries = [&](int seg, int nrows) {
+      wait_own(mbar(MB_Q), static_cast<uint32_t>(seg & 1), s_abort, p.err);
+      if (!__all_sync(0xffffffffu, *s_abort == 0)) return;   // (what lies there may not have landed)
+      widen_queries(smem + OFF_Q, nrows - static_cast<int>(rank) * HROWS, tid, p.err);
+      tc::fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(even_mbar(MB_QW));
+    };
 #pragma unroll 1
-    for (int tile = from.tile; next_segment(p, share, from, to, tile, s); tile = s.tile + 1, ++k) {
+    for (int tile = from.tile; next_segment<CAUSAL>(p, share, from, to, tile, s); tile = s.tile + 1, ++k) {
       // This CTA's half block of each step: h0, h0 + 2, ..  Its keys' meta
       // words start at meta0 + 128 hb, those of the own range meta_gap behind.
       const int h0 = 2 * s.sa + static_cast<int>(rank), np = prefix_halves(s.t);
@@ -476,8 +557,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       const int* meta0 = p.meta + s.t.prefix_base + j;
       const int meta_gap = s.t.own_base - np * BN - s.t.prefix_base;
       const int nsteps = s.steps;
+      if (CAUSAL && k == 0) take_queries(0, s.t.nrows);
       auto load_meta = [&](int step) {
         const int key = (h0 + 2 * step) * BN;
+        if (CAUSAL) return step >= nsteps || key + j >= prefix_len ? META_MASKED : meta0[key];
         const bool shared = key < np * BN;
         if (step >= nsteps || key + j >= (shared ? prefix_len : own_len)) return META_MASKED;
         return meta0[key + (shared ? 0 : meta_gap)];
@@ -486,13 +569,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       group_sync();   // the previous segment's rows are read
       if (quad == 0) {
         int2 of = make_int2(-1, 0);
-        if (c0 + lane < s.t.nrows) {
+        if (CAUSAL) {
+          // The keys that the row's token sees.
+          of.x = c0 + lane < s.t.nrows ? s.t.cached + (s.t.row0 + c0 + lane) / p.H + 1 : 0;
+        } else if (c0 + lane < s.t.nrows) {
           const int q = s.t.q_row0 + c0 + lane, b = q / p.R;
           if (p.own[b] > 0) of = make_int2(b, static_cast<int>(p.anc[b * p.T + (q - b * p.R) / p.H]));
         }
         s_row[c0 + lane] = of;
       }
       group_sync();
+      // CAUSAL: keys that all rows of the tile see.
+      const int all_see = CAUSAL ? s.t.cached + s.t.row0 / p.H + 1 : 0;
       float mrow = -INFINITY;             // the lane's row's running max less P_SHIFT, the same in the group's warps of both CTAs
       float lrun = 0.f;                   // its sum over this warp's keys so far
 #pragma unroll 1
@@ -502,7 +590,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         const bool alive = *s_abort == 0;
         // Decided while S^T is computed: do all rows see all of the warp's
         // keys?  If not, which: bit 8k + 2i + e for key k and row (i, e).
-        const bool plain = __all_sync(0xffffffffu, meta == META_SHARED);
+        const int key0 = (h0 + 2 * it) * BN + quad * 32;   // CAUSAL: the warp's first key in the request
+        const bool plain = __all_sync(0xffffffffu, meta == META_SHARED) && (!CAUSAL || key0 + 32 <= all_see);
         uint32_t vis = 0xffffffffu, poison = 0;
         if (!plain) {
           vis = 0;
@@ -515,7 +604,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
               const int2 r = s_row[c0 + 8 * (c >> 1) + pair + (c & 1)];
-              const bool v = w == META_SHARED || (r.x == b && (d < 0 || ((static_cast<uint32_t>(r.y) >> d) & 1u)));
+              const bool v = CAUSAL ? key0 + key + 8 * k8 < r.x
+                                   : w == META_SHARED || (r.x == b && (d < 0 || ((static_cast<uint32_t>(r.y) >> d) & 1u)));
               vis |= (v ? 1u : 0u) << (8 * k8 + c);
             }
           }
@@ -678,6 +768,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         // The step's row sums over this warp's 32 keys, off the way to O^T.
         lrun = lrun * alpha + reduce_rows<true>(y, lane);
       }
+      if (CAUSAL) {
+        // The next tile's queries, while the last O^T is computed: its first
+        // S^T follows without a pause.
+        Segment ahead;
+        ahead.t = s.t;
+        if (next_segment<CAUSAL>(p, share, from, to, s.tile + 1, ahead)) take_queries(k + 1, ahead.t.nrows);
+      }
       // ---- the segment's end: row sums over the group's warps, then the peer's
       const int eb = (g & 1) * ROWS;   // the halves of s_red and s_m that the last step did not use
       s_red[(eb + row) * 4 + quad] = lrun;
@@ -761,7 +858,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       wait_drain(mbar(MB_DONE), 0, p.err);
     }
     const SharedPos end{range.z, range.w};
-    for (int tile = from.tile; next_segment(p, share, from, end, tile, s); tile = s.tile + 1)
+    for (int tile = from.tile; next_segment<CAUSAL>(p, share, from, end, tile, s); tile = s.tile + 1)
       write_nan_segment(p, s, cluster, rank, tid);
     tc::cluster_sync();
     tc::fence_after_sync();
@@ -773,14 +870,12 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-}  // namespace
-
-cudaError_t make_shared_maps(SharedMaps* maps, void* k16, long long k_plane, void* q16, long long q_plane) {
-  // (Looked up once per process: a look-up takes longer than the three maps.)
-  struct Encoder {
-    EncodeTiled fn;
-    cudaError_t e;
-  };
+// (Looked up once per process: a look-up takes longer than the three maps.)
+struct Encoder {
+  EncodeTiled fn;
+  cudaError_t e;
+};
+const Encoder& tensor_map_encoder() {
   static const Encoder encoder = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
@@ -788,6 +883,13 @@ cudaError_t make_shared_maps(SharedMaps* maps, void* k16, long long k_plane, voi
     const bool found = e == cudaSuccess && q == cudaDriverEntryPointSuccess && fn;
     return Encoder{reinterpret_cast<EncodeTiled>(fn), found ? cudaSuccess : e != cudaSuccess ? e : cudaErrorNotSupported};
   }();
+  return encoder;
+}
+
+}  // namespace
+
+cudaError_t make_shared_maps(SharedMaps* maps, void* k16, long long k_plane, void* q16, long long q_plane) {
+  const Encoder& encoder = tensor_map_encoder();
   if (encoder.e != cudaSuccess) return encoder.e;
   const EncodeTiled encode = encoder.fn;
   // Nine planes of rows of 64 fp16 (128 bytes), swizzled on the way in.
@@ -804,11 +906,27 @@ cudaError_t make_shared_maps(SharedMaps* maps, void* k16, long long k_plane, voi
   return cudaSuccess;
 }
 
+// The same for queries as they are given: rows of 576 bf16.
+cudaError_t make_chunk_query_map(CUtensorMap* map, const void* q, long long rows) {
+  const Encoder& encoder = tensor_map_encoder();
+  if (encoder.e != cudaSuccess) return encoder.e;
+  const cuuint64_t dims[2] = {D_QK, static_cast<cuuint64_t>(rows)}, strides[1] = {ROW_BYTES};
+  const cuuint32_t box[2] = {64, HROWS}, estrides[2] = {1, 1};
+  return encoder.fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(q), dims, strides, box, estrides,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 cudaError_t partial_shared_prepare() {
-  cudaError_t e = cudaFuncSetAttribute(partial_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(partial_shared_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                              cudaSharedmemCarveoutMaxShared);
+  for (auto kernel : {partial_shared_kernel<false>, partial_shared_kernel<true>}) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_TOTAL);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_partial_shared(const SharedParams& p, const SharedMaps& maps, cudaStream_t stream) {
@@ -822,7 +940,8 @@ cudaError_t launch_partial_shared(const SharedParams& p, const SharedMaps& maps,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, partial_shared_kernel, p, maps.pair, maps.chunk, maps.q);
+  return cudaLaunchKernelEx(&cfg, p.q_indptr ? partial_shared_kernel<true> : partial_shared_kernel<false>, p, maps.pair, maps.chunk,
+                            maps.q);
 }
 
 }  // namespace mlav

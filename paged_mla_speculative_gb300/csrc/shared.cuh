@@ -1,5 +1,10 @@
 // Definitions shared by the kernels of the shared-prefix verify attention.
 //
+// partial_shared.cu's kernel also runs the attention of chunks of new tokens
+// (chunk_pack.cu): there a tile holds rows of one request, its key sequence is
+// the request's rows up to the last that the tile's last token sees, and a key
+// is masked for the rows of earlier tokens by its position.
+//
 // Every call lays its keys out once in a dense packed space: for each group
 // its shared rows, then its requests' own rows, one after another.  Query rows
 // go in tiles of 128 consecutive rows of one group (a tile may hold several
@@ -9,6 +14,7 @@
 // not an ancestor, is masked by the key's meta word.
 #pragma once
 
+#include "chunk_steps.h"
 #include "common.cuh"
 
 namespace mlav {
@@ -34,11 +40,11 @@ constexpr int SH_MAX_CLUSTERS = 128;   // of the attention kernel (an SM pair ea
 struct SharedTile {
   int q_row0, nrows;        // query rows
   int prefix_base, prefix_len;
-  int own_base, own_len;
+  int own_base, own_len;    // (chunks: the request, 0)
   int halves;               // half blocks of the whole sequence
   int steps;                // (halves + 1) / 2
   int seg0, nseg;           // clusters seg0 .. seg0 + nseg - 1 hold its steps
-  int pad[2];
+  int row0, cached;         // chunks: the tile's first row in its request, the request's rows before the chunk
 };
 static_assert(sizeof(SharedTile) == 48, "three 16-byte loads");
 
@@ -102,10 +108,34 @@ struct SharedParams {
   int* cost;                    // [max_tiles + 1] prefix sum of the tiles' costs
   SharedTile* tiles;            // [max_tiles]
   SharedShare* share;           // [clusters]
-  int* totals;                  // [0] packed keys, [1] tiles
+  int* totals;                  // [0] packed keys, [1] tiles; chunks: [2] what cannot be served
   float* part_o;                // [2 * cut_clusters][128][512], none when that is 1
   float* part_lse;              // [2 * cut_clusters][128]
+  // Chunks of new tokens: q is bf16 [num_tokens * H, 576], own[b] the rows of
+  // request b, 0 when it has no new tokens or cannot be served; base [B + 1]
+  // and tile0 [B + 1] are by request.
+  const int32_t* q_indptr;      // [B + 1]
+  int num_tokens;
+  long long* chunk_cost;        // [B + 1]
 };
+
+// Tile t of the chunk of request b, whose first packed key is `base`.
+__device__ __forceinline__ SharedTile chunk_tile(const SharedParams& p, int b, int t, int base) {
+  const int n = p.kv_lens[b], q0 = p.q_indptr[b], c = p.q_indptr[b + 1] - q0;
+  SharedTile x;
+  x.row0 = t * SH_ROWS;
+  x.cached = n - c;
+  x.q_row0 = q0 * p.H + x.row0;
+  x.nrows = min(SH_ROWS, c * p.H - x.row0);
+  x.prefix_base = base;
+  x.prefix_len = x.cached + (x.row0 + x.nrows - 1) / p.H + 1;
+  x.own_base = b;
+  x.own_len = 0;
+  x.halves = (x.prefix_len + SH_HALF - 1) / SH_HALF;
+  x.steps = (x.halves + 1) / 2;
+  x.seg0 = x.nseg = 0;
+  return x;
+}
 
 // Partial slot of a segment: a cluster holds at most two tiles that others
 // hold parts of, its first and its last.

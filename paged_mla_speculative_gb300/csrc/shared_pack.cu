@@ -21,8 +21,7 @@
 // shared_join_kernel: the LSE merge of the tiles that several clusters share.
 #include "shared.cuh"
 #include "kernels.h"
-
-#include <cuda_bf16.h>
+#include "pack_rows.cuh"
 
 #include <algorithm>
 #include <climits>
@@ -30,42 +29,7 @@
 namespace mlav {
 namespace {
 
-constexpr int THREADS = 256;
-constexpr int PACK_KEYS = 32;                                   // rows per CTA iteration
-constexpr int PER_THREAD = PACK_KEYS * ROW_CHUNKS / THREADS;    // 9 granules
-static_assert(PER_THREAD * THREADS == PACK_KEYS * ROW_CHUNKS, "even split");
 constexpr int SMALL = 512;     // requests, groups and tiles laid out in shared memory
-
-// Inclusive block scan; `all` receives the block's total.
-__device__ __forceinline__ int block_scan(int x, int* s_warp, int& all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) s_warp[warp] = x;
-  __syncthreads();
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w == warp) x += all;
-    all += s_warp[w];
-  }
-  return x;
-}
-
-// Largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
-__device__ __forceinline__ int last_not_above(const int* a, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a[mid] <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
 
 // The groups of a call; when they do not partition the batch: one group, and
 // no request is served.
@@ -91,7 +55,7 @@ __device__ __forceinline__ int scan_requests(const SharedParams& p, int* own, in
   int n = 0, ip0 = 0, ip1 = 0;
   const int ipn = p.kv_indptr[B];
   if (tid < B) n = p.kv_lens[tid], ip0 = p.kv_indptr[tid], ip1 = p.kv_indptr[tid + 1];
-  for (int g = tid; g < p.groups; g += THREADS) {
+  for (int g = tid; g < p.groups; g += PACK_THREADS) {
     const int a = p.group_indptr[g], z = p.group_indptr[g + 1];
     bad |= z < a || (g == 0 && a != 0) || (g == p.groups - 1 && z != B);
     source[g] = INT_MAX;
@@ -104,9 +68,9 @@ __device__ __forceinline__ int scan_requests(const SharedParams& p, int* own, in
   const bool groups_ok = __syncthreads_or(bad) == 0;
   grp = Groups{indptr ? indptr : p.group_indptr, indptr ? lens : p.shared_lens, groups_ok ? p.groups : 1, B, groups_ok};
   int errs = groups_ok ? 0 : ERR_INDPTR;
-  for (int b = tid; b < B; b += THREADS) {
+  for (int b = tid; b < B; b += PACK_THREADS) {
     const int g = grp.of(b);
-    if (b >= THREADS) n = p.kv_lens[b], ip0 = p.kv_indptr[b], ip1 = p.kv_indptr[b + 1];
+    if (b >= PACK_THREADS) n = p.kv_lens[b], ip0 = p.kv_indptr[b], ip1 = p.kv_indptr[b + 1];
     const long long need = p.page_size == 1 ? n : (static_cast<long long>(n) + PAGE - 1) / PAGE;
     const int S = groups_ok ? grp.shared_lens[g] : 0;
     const bool len_ok = n >= p.T && n <= p.max_kv_len && S >= 0 && S <= n - p.T;
@@ -120,7 +84,7 @@ __device__ __forceinline__ int scan_requests(const SharedParams& p, int* own, in
   if (report && errs) atomicOr(p.err, errs);
   __syncthreads();
   int before = 0;
-  for (int b0 = 0; b0 < B; b0 += THREADS) {
+  for (int b0 = 0; b0 < B; b0 += PACK_THREADS) {
     const int b = b0 + tid;
     int prefix = 0, mine = 0;
     if (b < B) {
@@ -155,7 +119,7 @@ struct PlanLayout {
 // shuffles (walking them in global memory took a load per level).
 __device__ __forceinline__ void plan_ancestors(const SharedParams& p) {
   const int lane = threadIdx.x & 31;
-  for (int b = threadIdx.x >> 5; b < p.batch; b += THREADS / 32) {
+  for (int b = threadIdx.x >> 5; b < p.batch; b += PACK_THREADS / 32) {
     const int par = lane < p.T ? p.draft_parent[static_cast<size_t>(b) * p.T + lane] : -1;
     if (par < -1 || par >= lane + (lane < p.T ? 0 : 1)) atomicOr(p.err, ERR_PARENT);
     const int up = par >= lane ? -1 : par;
@@ -182,12 +146,12 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
   const int keys = scan_requests(p, own, base, small ? s.l.source : p.source, small ? s.l.indptr : nullptr, s.l.lens, s_warp, grp,
                                  true);
   if (small)
-    for (int b = tid; b < B; b += THREADS) p.own[b] = own[b];
+    for (int b = tid; b < B; b += PACK_THREADS) p.own[b] = own[b];
   // Tiles of each group.
   const int G = grp.n;
   int* tile0 = small ? s.tile0 : p.tile0;
   int tiles = 0;
-  for (int g0 = 0; g0 < G; g0 += THREADS) {
+  for (int g0 = 0; g0 < G; g0 += PACK_THREADS) {
     const int g = g0 + tid;
     int n = 0;
     if (g < G) n = static_cast<int>((static_cast<long long>(grp.begin(g + 1) - grp.begin(g)) * p.R + SH_ROWS - 1) / SH_ROWS);
@@ -205,7 +169,7 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
   int* cost = tiles <= SMALL ? s.cost : p.cost;
   SharedTile* recs = tiles <= SMALL ? s.tiles : p.tiles;
   int total = 0, most = 0;
-  for (int t0 = 0; t0 < tiles; t0 += THREADS) {
+  for (int t0 = 0; t0 < tiles; t0 += PACK_THREADS) {
     const int t = t0 + tid;
     SharedTile rec{};
     int c = 0;
@@ -247,7 +211,7 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
   int used = max(1, min(p.cut_clusters, total / (SH_SEGMENT_COST + 2)));
   const bool whole = tiles <= p.clusters && s_max <= total / p.clusters + SH_SEGMENT_COST + SH_JOIN_COST;
   if (whole) used = tiles;
-  for (int c = tid; c <= p.clusters; c += THREADS) {
+  for (int c = tid; c <= p.clusters; c += PACK_THREADS) {
     SharedPos at{tiles, 0};
     if (whole) {
       at.tile = min(c, tiles);
@@ -259,7 +223,7 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
     s.start[c] = at;
   }
   __syncthreads();
-  for (int c = tid; c < p.clusters; c += THREADS) {
+  for (int c = tid; c < p.clusters; c += PACK_THREADS) {
     SharedShare sh{};
     sh.from = s.start[c];
     sh.to = s.start[c + 1];
@@ -267,7 +231,7 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
     p.share[c] = sh;
   }
   // Which clusters hold each tile.
-  for (int t = tid; t < tiles; t += THREADS) {
+  for (int t = tid; t < tiles; t += PACK_THREADS) {
     const int c = cost[t + 1] - cost[t];
     SharedTile rec = recs[t];
     if (c > 0) {
@@ -289,63 +253,11 @@ __device__ void plan_call(const SharedParams& p, PlanLayout& s, bool small, int*
   }
 }
 
-struct Rows {
-  uint4 v[PER_THREAD];
-};
-// A granule that the call reads once.  (No read-only load: those are for
-// memory that nothing writes while the kernel runs, and this one is launched
-// while the kernel before it may still write its inputs.)
-__device__ __forceinline__ uint4 load_once(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-// Row r of 32 (each THREADS / 8 granules apart) at src + s_row[r] * 576, or
-// zeros where s_row is negative.
-__device__ __forceinline__ void load_rows(const uint16_t* src, const long long* s_row, Rows& x) {
-#pragma unroll
-  for (int u = 0; u < PER_THREAD; ++u) {
-    const int e = threadIdx.x + u * THREADS;
-    const int r = e / ROW_CHUNKS, c = e - r * ROW_CHUNKS;
-    const long long row = s_row[r];
-    x.v[u] = row >= 0 ? load_once(reinterpret_cast<const uint4*>(src + row * D_QK) + c) : make_uint4(0, 0, 0, 0);
-  }
-}
-// Widened into the planes at plane rows row0 .. row0 + rows - 1.  A value
-// outside fp16 is packed as zero and sets s_bad of its row; returns whether
-// this thread met one.
-__device__ __forceinline__ bool store_rows(const Rows& x, int* s_bad, uint16_t* dst, long long plane, long long row0, int rows) {
-  bool any = false;
-#pragma unroll
-  for (int u = 0; u < PER_THREAD; ++u) {
-    const int e = threadIdx.x + u * THREADS;
-    const int r = e / ROW_CHUNKS, c = e - r * ROW_CHUNKS;
-    bool bad = false;
-    uint4 w = widen_bf16x8(x.v[u], bad);
-    if (bad) {
-      any = true;
-      s_bad[r] = 1;
-      uint32_t h[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if ((h[k] & 0x7c00u) == 0x7c00u) h[k] &= 0xffff0000u;
-        if ((h[k] & 0x7c000000u) == 0x7c000000u) h[k] &= 0x0000ffffu;
-      }
-      w = make_uint4(h[0], h[1], h[2], h[3]);
-    }
-    if (r < rows) *reinterpret_cast<uint4*>(dst + ((c >> 3) * plane + row0 + r) * 64 + (c & 7) * 8) = w;
-  }
-  return any;
-}
-
 // `packers` CTAs (the last of the grid) gather keys, those before them widen
 // queries, the first `plans` (2 or 0) lay out the call.
-__global__ void __launch_bounds__(THREADS, 4) shared_prepare_kernel(const SharedParams p, int plans, int packers) {
+__global__ void __launch_bounds__(PACK_THREADS, 4) shared_prepare_kernel(const SharedParams p, int plans, int packers) {
   __shared__ PlanLayout s;
-  __shared__ int s_warp[THREADS / 32];
+  __shared__ int s_warp[PACK_THREADS / 32];
   __shared__ long long s_row[2][PACK_KEYS];
   __shared__ int s_meta[2][PACK_KEYS], s_bad[2][PACK_KEYS];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -366,13 +278,13 @@ __global__ void __launch_bounds__(THREADS, 4) shared_prepare_kernel(const Shared
     uint4 v[PER_THREAD];
 #pragma unroll
     for (int u = 0; u < PER_THREAD; ++u) {
-      const int e = tid + u * THREADS;
+      const int e = tid + u * PACK_THREADS;
       const long long row = row0 + e / ROW_CHUNKS;
       v[u] = row < rows ? load_once(reinterpret_cast<const uint4*>(p.q + row * D_QK) + e % ROW_CHUNKS) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < PER_THREAD; ++u) {
-      const int e = tid + u * THREADS;
+      const int e = tid + u * PACK_THREADS;
       const long long row = row0 + e / ROW_CHUNKS;
       const int c = e % ROW_CHUNKS;
       if (row < rows)
@@ -438,18 +350,16 @@ __global__ void __launch_bounds__(THREADS, 4) shared_prepare_kernel(const Shared
 
 // Rows of tiles that several clusters hold parts of (or none: no request of
 // the tile is served): 128 threads per row, a float4 of each part per thread,
-// up to JOIN_FLIGHT parts loaded before any is used.  A row's parts were just
+// a row's parts were just
 // written and mostly come from L2; the launch and one round trip are the time.
 constexpr int JOIN_ROWS = 2;
-constexpr int JOIN_FLIGHT = 8;
-constexpr int JOIN_MAX = SH_MAX_CLUSTERS / 32;   // parts per lane
 
 __global__ void __launch_bounds__(JOIN_ROWS * 128) shared_join_kernel(const SharedParams p) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int tile = blockIdx.x / (SH_ROWS / JOIN_ROWS);
   if (tile >= p.totals[1]) return;
   const SharedTile t = p.tiles[tile];
-  const int lane = threadIdx.x & 31, col = threadIdx.x & 127;
+  const int col = threadIdx.x & 127;
   const int r = (blockIdx.x % (SH_ROWS / JOIN_ROWS)) * JOIN_ROWS + (threadIdx.x >> 7);
   if (t.nseg == 1 || r >= t.nrows) return;
   const int row = t.q_row0 + r;
@@ -462,61 +372,9 @@ __global__ void __launch_bounds__(JOIN_ROWS * 128) shared_join_kernel(const Shar
     const SharedPos from = p.share[t.seg0].from;
     const int slot0 = part_slot(t.seg0, from.tile == tile);
     auto at = [&](int s) { return static_cast<size_t>(s ? part_slot(t.seg0 + s, true) : slot0) * SH_ROWS + r; };
-    float L[JOIN_MAX], mx = -INFINITY;
-    bool any_nan = false;
-#pragma unroll
-    for (int k = 0; k < JOIN_MAX; ++k) {
-      L[k] = 32 * k + lane < t.nseg ? p.part_lse[at(32 * k + lane)] : -INFINITY;
-      any_nan |= L[k] != L[k];
-      mx = fmaxf(mx, L[k]);
-    }
-    any_nan = __any_sync(0xffffffffu, any_nan);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    const float top = mx == -INFINITY ? 0.f : mx;
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < JOIN_MAX; ++k) {
-      L[k] = ex2((L[k] - top) * kLog2e);
-      sum += L[k];
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    // Every key masked (bad slots): weight 0 everywhere.
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < JOIN_MAX; ++k) {
-      for (int s0 = 32 * k; s0 < min(t.nseg, 32 * k + 32); s0 += JOIN_FLIGHT) {
-        float4 x[JOIN_FLIGHT];
-#pragma unroll
-        for (int f = 0; f < JOIN_FLIGHT; ++f)
-          if (s0 + f < t.nseg) x[f] = __ldcs(reinterpret_cast<const float4*>(p.part_o + at(s0 + f) * D_V) + col);
-#pragma unroll
-        for (int f = 0; f < JOIN_FLIGHT; ++f) {
-          const float w = __shfl_sync(0xffffffffu, L[k], (s0 + f) & 31) * inv;
-          if (s0 + f >= t.nseg || w == 0.f) continue;   // (a part of weight 0 may hold anything)
-          acc.x += w * x[f].x;
-          acc.y += w * x[f].y;
-          acc.z += w * x[f].z;
-          acc.w += w * x[f].w;
-        }
-      }
-    }
-    lse = sum > 0.f ? top + logf(sum) : -INFINITY;
-    if (any_nan) {
-      acc = make_float4(nan, nan, nan, nan);
-      lse = nan;
-    }
+    merge_parts(p, t.nseg, at, col, acc, lse);
   }
-  const size_t at = static_cast<size_t>(row) * (D_V / 4) + col;
-  if (p.out_bf16) {
-    __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-    reinterpret_cast<uint2*>(p.out)[at] = make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
-  } else {
-    reinterpret_cast<float4*>(p.out)[at] = acc;
-  }
-  if (col == 0) p.lse[row] = lse;
+  store_merged(p, row, col, acc, lse);
 }
 
 }  // namespace
@@ -532,9 +390,9 @@ cudaError_t launch_shared_prepare(const SharedParams& p, int num_sms, cudaStream
   const long long wave = std::max(2LL * num_sms, 4LL * num_sms - 2 - query_ctas);
   const int packers = static_cast<int>(std::min<long long>((most + PACK_KEYS - 1) / PACK_KEYS, wave));
   if (p.batch <= SMALL && p.groups <= SMALL)
-    return launch_overlapping(shared_prepare_kernel, grid(2 + query_ctas + packers), THREADS, 0, stream, 1, p, 2, packers);
-  const cudaError_t e = launch_overlapping(shared_prepare_kernel, grid(2 + query_ctas), THREADS, 0, stream, 1, p, 2, 0);
-  return e != cudaSuccess ? e : launch_overlapping(shared_prepare_kernel, grid(packers), THREADS, 0, stream, 1, p, 0, packers);
+    return launch_overlapping(shared_prepare_kernel, grid(2 + query_ctas + packers), PACK_THREADS, 0, stream, 1, p, 2, packers);
+  const cudaError_t e = launch_overlapping(shared_prepare_kernel, grid(2 + query_ctas), PACK_THREADS, 0, stream, 1, p, 2, 0);
+  return e != cudaSuccess ? e : launch_overlapping(shared_prepare_kernel, grid(packers), PACK_THREADS, 0, stream, 1, p, 0, packers);
 }
 
 cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream) {
