@@ -401,6 +401,40 @@ int mla_verify_attn_chunk(mla_verify_plan* plan, int batch, int64_t num_tokens, 
                           void* stream);
 
 /*
+ * The attention weight that new tokens give to each cached row, added to what
+ * the row has: with the tokens and tables of mla_verify_attn_chunk and the lse
+ * that the attention of these tokens wrote (mla_verify_attn_chunk, or
+ * mla_verify_attn for drafts that were accepted: a chain), for each row j of
+ * request b
+ *
+ *     weights[b][j] += sum over tokens i with j <= n_b - c_b + i and heads h of
+ *                      exp(scale * dot(q[q_indptr[b] + i, h], k_j) - lse[q_indptr[b] + i, h])
+ *
+ * The caller zeroes a request's row of `weights` when it starts.  Any of a
+ * request's last tokens may be given alone (c_b counts those), several layers
+ * may add to the same weights.
+ *
+ *   lse      fp32 [num_tokens][H]; a row that is not finite adds nothing.
+ *   weights  fp32 [batch] rows, weight_stride >= max_kv_len floats apart; places
+ *            from kv_lens[b] on are not touched, nor are rows of requests without
+ *            new tokens or out of order (MLA_VERIFY_DEV_BAD_LEN / BAD_INDPTR), nor
+ *            places whose slot is bad (BAD_SLOT).  If q_indptr is out of order
+ *            (BAD_INDPTR) nothing is added at all.
+ *
+ * Products in bf16 (exact), sums in fp32: a score of magnitude s is off by
+ * about 1e-6 s, and so its weight by that relative amount times scale.  A NaN
+ * or infinite value in a query reaches the rows that it sees, one in a cached
+ * row that row alone.  Sums are made in one order: equal inputs give equal
+ * weights.  num_tokens as for mla_verify_attn_chunk; a weight_stride below
+ * max_kv_len gives MLA_VERIFY_ERR_ARG; other errors as for mla_verify_attn.
+ * Capturable; allocates nothing; shares the plan's workspace.
+ */
+int mla_verify_weigh_kv(mla_verify_plan* plan, int batch, int64_t num_tokens, const void* q,
+                        const void* kv_cache, const int32_t* kv_indices, const int32_t* kv_indptr,
+                        const int32_t* kv_lens, const int32_t* q_indptr, const float* lse,
+                        float scale, float* weights, int64_t weight_stride, void* stream);
+
+/*
  * Read the sticky device error word (MLA_VERIFY_DEV_* bits) into
  * *device_status; clear it when `clear` is nonzero.  Waits for the plan's
  * last eagerly launched call (an event the plan records at the end of every

@@ -89,6 +89,8 @@ SIGNATURES = {
                                     _P]),
     "mla_verify_attn_chunk": (_I, [_P, _I, ctypes.c_int64, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P, _P,
                                    _P]),
+    "mla_verify_weigh_kv": (_I, [_P, _I, ctypes.c_int64, _P, _P, _P, _P, _P, _P, _P, ctypes.c_float, _P,
+                                 ctypes.c_int64, _P]),
     "mla_verify_append_kv": (_I, [_P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_float, _P,
                                   ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64,
                                   ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _I, _P, _P, _P]),
@@ -539,6 +541,51 @@ def mla_verify_attn_chunk(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_len
         lse.data_ptr(), _stream_ptr(stream))
     _check(st, "mla_verify_attn_chunk")
     return out, lse
+
+
+def _expect_weights(plan: Plan, weights, name: str, batch: int):
+    """Rows of fp32 weights; returns their stride."""
+    if not isinstance(weights, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if weights.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {weights.dtype}")
+    if weights.device != plan.torch_device:
+        raise ValueError(f"{name} must be on {plan.torch_device}, got {weights.device}")
+    if weights.dim() != 2 or weights.shape[0] != batch or weights.shape[1] < plan.max_kv_len:
+        raise ValueError(f"{name} must be [{batch}, {plan.max_kv_len} or more], got {tuple(weights.shape)}")
+    stride, last = weights.stride()
+    if last != 1 or (batch > 1 and stride < weights.shape[1]):
+        raise ValueError(f"{name}'s rows must be contiguous and must not overlap")
+    return stride if batch > 1 else weights.shape[1]
+
+
+def weigh_kv(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_lens, q_indptr, lse, scale: float,
+             weights, stream=None):
+    """Add the attention weight that new tokens give to each cached row;
+    returns weights.
+
+    q, kv_cache, the tables and q_indptr as for mla_verify_attn_chunk, lse
+    [N, H] fp32 as the attention of these tokens wrote it.  weights [B, W >=
+    max_kv_len] fp32 (any row stride): row j of request b gets, in place, the
+    sum over its tokens and heads that see it of exp(scale * score - lse).
+    Enqueued on ``stream``; no sync.
+    """
+    N, B = q.shape[0], kv_lens.shape[0]
+    dev = plan.torch_device
+    _expect(q, "q", torch.bfloat16, dev, (N, plan.H, 576))
+    _expect(kv_cache, "kv_cache", torch.bfloat16, dev, (plan.num_slots, 576))
+    _expect(kv_indices, "kv_indices", torch.int32, dev)
+    _expect(kv_indptr, "kv_indptr", torch.int32, dev, (B + 1,))
+    _expect(kv_lens, "kv_lens", torch.int32, dev, (B,))
+    _expect(q_indptr, "q_indptr", torch.int32, dev, (B + 1,))
+    _expect(lse, "lse", torch.float32, dev, (N, plan.H))
+    stride = _expect_weights(plan, weights, "weights", B)
+    st = load_library().mla_verify_weigh_kv(
+        plan.handle, B, N, q.data_ptr(), kv_cache.data_ptr(), kv_indices.data_ptr(),
+        kv_indptr.data_ptr(), kv_lens.data_ptr(), q_indptr.data_ptr(), lse.data_ptr(), scale,
+        weights.data_ptr(), stride, _stream_ptr(stream))
+    _check(st, "mla_verify_weigh_kv")
+    return weights
 
 
 def append_kv(plan: Plan, kv, weight, eps: float, cos_sin, positions, slots, kv_cache, q_nope=None,

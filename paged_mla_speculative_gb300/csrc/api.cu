@@ -402,7 +402,8 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
     return MLA_VERIFY_ERR_CUDA;
   if (mlav::partial_mma_prepare() != cudaSuccess || mlav::partial_tc_prepare() != cudaSuccess ||
       mlav::partial_pair_prepare() != cudaSuccess || mlav::pack_kv_prepare() != cudaSuccess ||
-      mlav::partial_shared_prepare() != cudaSuccess || mlav::page_pool_prepare() != cudaSuccess)
+      mlav::partial_shared_prepare() != cudaSuccess || mlav::page_pool_prepare() != cudaSuccess ||
+      mlav::weigh_prepare() != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
 
   mla_verify_plan* pl = new (std::nothrow) mla_verify_plan();
@@ -436,8 +437,10 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
   pl->shared_ok = pl->k_plane <= INT32_MAX && 1LL * max_batch * pl->R <= INT32_MAX / 2 && max_batch < mlav::SH_MAX_BATCH;
   // The shared-prefix kernel's partials: two tiles per cluster, where any are cut.
   pl->sh_cut = pl->shared_ok ? shared_cut_clusters(pl) : 1;
-  const size_t rows = std::max(static_cast<size_t>(cap) * pl->R,
-                               pl->sh_cut > 1 ? static_cast<size_t>(2 * pl->sh_cut) * mlav::SH_ROWS : 0);
+  // mla_verify_weigh_kv's parts and records lie there too.
+  const size_t rows = std::max({static_cast<size_t>(cap) * pl->R,
+                                pl->sh_cut > 1 ? static_cast<size_t>(2 * pl->sh_cut) * mlav::SH_ROWS : 0,
+                                mlav::weigh_workspace_bytes(shared_clusters(pl)) / (mlav::D_V * sizeof(float)) + 1});
   const size_t out_elt = out_dtype == MLA_VERIFY_OUT_BF16 ? 2 : 4;
   const long long idx_per_req = page_size == 1 ? max_kv_len : ceil_div(max_kv_len, mlav::PAGE);
   pl->st_idx_cap = idx_per_req * max_batch;
@@ -1015,6 +1018,49 @@ int mla_verify_attn_chunk(mla_verify_plan* pl, int batch, int64_t num_tokens, co
       mlav::launch_chunk_prepare(p, pl->num_sms, s) != cudaSuccess ||
       mlav::launch_partial_shared(p, maps, s) != cudaSuccess || mlav::launch_chunk_join(p, s) != cudaSuccess ||
       note_done(pl, s) != cudaSuccess)
+    return MLA_VERIFY_ERR_CUDA;
+  return MLA_VERIFY_OK;
+}
+
+int mla_verify_weigh_kv(mla_verify_plan* pl, int batch, int64_t num_tokens, const void* q, const void* kv_cache,
+                        const int32_t* kv_indices, const int32_t* kv_indptr, const int32_t* kv_lens,
+                        const int32_t* q_indptr, const float* lse, float scale, float* weights, int64_t weight_stride,
+                        void* stream) {
+  if (!pl) return MLA_VERIFY_ERR_NULL;
+  if (num_tokens == 0) return check_device(pl);
+  if (!q || !kv_cache || !kv_indices || !kv_indptr || !kv_lens || !q_indptr || !lse || !weights) return MLA_VERIFY_ERR_NULL;
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(kv_indices) || !aligned16(kv_indptr) || !aligned16(kv_lens) ||
+      !aligned16(q_indptr) || !aligned16(lse) || !aligned16(weights))
+    return MLA_VERIFY_ERR_ALIGN;
+  if (batch < 1 || batch > pl->max_batch) return MLA_VERIFY_ERR_BATCH;
+  if (!std::isfinite(scale)) return MLA_VERIFY_ERR_SCALE;
+  if (num_tokens < 0 || num_tokens > INT32_MAX / pl->H || weight_stride < pl->max_kv_len || weight_stride > INT64_MAX / 4 / batch)
+    return MLA_VERIFY_ERR_ARG;
+  const int dev_status = check_device(pl);
+  if (dev_status != MLA_VERIFY_OK) return dev_status;
+  mlav::WeighParams p{};
+  p.kv_indices = kv_indices;
+  p.kv_indptr = kv_indptr;
+  p.kv_lens = kv_lens;
+  p.q_indptr = q_indptr;
+  p.lse = lse;
+  p.weights = weights;
+  p.stride = weight_stride;
+  p.scale_log2 = scale * mlav::kLog2e;
+  p.batch = batch;
+  p.num_tokens = static_cast<int>(num_tokens);
+  p.H = pl->H;
+  p.page_size = pl->page_size;
+  p.num_slots = pl->num_slots;
+  p.max_kv_len = pl->max_kv_len;
+  p.clusters = shared_clusters(pl);
+  p.part = pl->ws_o;
+  p.cut = reinterpret_cast<mlav::WeighCut*>(pl->ws_o + static_cast<size_t>(p.clusters) * 2 * 256);
+  p.err = pl->err;
+  mlav::WeighMaps maps;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (mlav::make_weigh_maps(&maps, kv_cache, pl->num_slots, pl->page_size, q, num_tokens * pl->H) != cudaSuccess ||
+      mlav::launch_weigh_kv(p, maps, s) != cudaSuccess || note_done(pl, s) != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
   return MLA_VERIFY_OK;
 }

@@ -126,6 +126,8 @@ cudaError_t launch_compact_kv(const CompactArgs& a, cudaStream_t stream);
 struct SharedMaps {
   CUtensorMap pair, chunk, q;   // of the packed keys (two planes, one plane) and queries
 };
+// The driver's tensor map encoder.
+cudaError_t tensor_map_encode(void** fn);
 cudaError_t make_shared_maps(SharedMaps* maps, void* k16, long long k_plane, void* q16, long long q_plane);
 cudaError_t partial_shared_prepare();
 cudaError_t launch_shared_prepare(const SharedParams& p, int num_sms, cudaStream_t stream);
@@ -138,6 +140,40 @@ cudaError_t launch_shared_join(const SharedParams& p, cudaStream_t stream);
 cudaError_t make_chunk_query_map(CUtensorMap* map, const void* q, long long rows);
 cudaError_t launch_chunk_prepare(const SharedParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_chunk_join(const SharedParams& p, cudaStream_t stream);
+
+// The attention weight given to cached rows (weigh_kv.cu).
+struct WeighCut {                   // what a cluster shares with others of its first and its last block
+  int first_request, first_block, last_request, last_block;
+  int continues, goes_on;           // its first block began, its last ends in another cluster
+  int last_slot;                    // its last block is not its first
+  int pad;
+};
+struct WeighParams {
+  const int32_t* kv_indices;
+  const int32_t* kv_indptr;         // [batch + 1]
+  const int32_t* kv_lens;           // [batch]
+  const int32_t* q_indptr;          // [batch + 1]
+  const float* lse;                 // [num_tokens][H]
+  float* weights;                   // [batch] rows, stride floats apart
+  long long stride;
+  float scale_log2;
+  int batch, num_tokens, H, page_size;
+  long long num_slots;
+  int max_kv_len;
+  int clusters;
+  WeighCut* cut;                    // [clusters]
+  float* part;                      // [2 * clusters][256]
+  int* err;
+};
+struct WeighMaps {
+  CUtensorMap kv, q;                // rows of 576 bf16: the cache (boxes of a page, or of one slot) and the queries
+};
+constexpr size_t weigh_workspace_bytes(int clusters) {
+  return static_cast<size_t>(clusters) * (sizeof(WeighCut) + 2 * 256 * sizeof(float));
+}
+cudaError_t make_weigh_maps(WeighMaps* maps, const void* kv, long long num_slots, int page_size, const void* q, long long q_rows);
+cudaError_t weigh_prepare();
+cudaError_t launch_weigh_kv(const WeighParams& p, const WeighMaps& maps, cudaStream_t stream);
 
 // New tokens' cache rows and queries (append_kv.cu).
 struct AppendArgs {

@@ -888,6 +888,12 @@ const Encoder& tensor_map_encoder() {
 
 }  // namespace
 
+cudaError_t tensor_map_encode(void** fn) {
+  const Encoder& encoder = tensor_map_encoder();
+  *fn = reinterpret_cast<void*>(encoder.fn);
+  return encoder.e;
+}
+
 cudaError_t make_shared_maps(SharedMaps* maps, void* k16, long long k_plane, void* q16, long long q_plane) {
   const Encoder& encoder = tensor_map_encoder();
   if (encoder.e != cudaSuccess) return encoder.e;
