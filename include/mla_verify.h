@@ -246,8 +246,8 @@ int mla_verify_plan_inject_fault(mla_verify_plan* plan, int fault);
  * pack hand-off flags, error word; and for mla_verify_attn_shared a 128-key
  * block, 4 bytes per key of max_batch * max_kv_len and, if more than the
  * partials of mla_verify_attn, two partials of 128 rows for each SM pair that
- * a call can keep busy: 40 MB at most on 152 SMs; for mla_verify_free_kv a
- * bit per page). */
+ * a call can keep busy: 40 MB at most on 152 SMs; for mla_verify_free_kv and
+ * mla_verify_evict_kv a bit per page or slot). */
 size_t mla_verify_plan_workspace_bytes(const mla_verify_plan* plan);
 
 /*
@@ -636,6 +636,64 @@ int mla_verify_fork_kv(mla_verify_plan* plan, int num_children, const int32_t* p
 int mla_verify_free_kv(mla_verify_plan* plan, int batch, const int32_t* kv_indices,
                        const int32_t* kv_indptr, int32_t* page_refs, int32_t* free_pages,
                        int32_t* free_count, void* stream);
+
+/*
+ * Eviction: each request of more than `budget` rows is cut down to the budget's.
+ * It keeps its first `sink` rows, its last `recent` rows and, of the others,
+ * those with the largest weights (mla_verify_weigh_kv's, or any), the lowest
+ * index first among equals; -0 counts as 0 and NaN is below every number.  The
+ * kept rows stay in their order.  Requests within the budget keep all rows.
+ *
+ *   weights      fp32 [batch] rows, weight_stride >= max_kv_len floats apart.
+ *   kv_indices, kv_indptr [batch + 1], kv_lens [batch]: the requests' tables, at
+ *                least the entries that kv_lens[b] rows need (what is behind
+ *                those is given back, too).
+ *   page_refs, free_pages, free_count: the pool of mla_verify_fork_kv; with
+ *                page_size 1 of slots (num_slots entries).
+ *   new_indices int32 [capacity] out, new_indptr int32 [batch + 1] out, new_lens
+ *                int32 [batch] out: the new tables, with room for extra_rows
+ *                more rows each (included in new_lens).
+ *   new_weights  fp32 [batch] rows of new_width >= max_kv_len, new_weight_stride
+ *                floats apart, out: the kept rows' weights in their new places,
+ *                0 behind them.
+ *
+ * page_size 64: an evicted request's first sink / 64 pages stay; its other kept
+ * rows are copied into fresh pages in each of the num_layers caches (as for
+ * mla_verify_fork_kv) and every other page of its table loses a count.  So
+ * pages that other tables hold, too, are not written, and a call needs fresh
+ * pages for the rows that it keeps: those it gives back are on the stack when
+ * it is done.  page_size 1: kept slots stay, the others lose a count; no row
+ * moves, kv_cache may be NULL and num_layers and layer_stride are ignored.
+ * The j-th fresh entry of the call, in request order, is free_pages[free_count
+ * - 1 - j]; entries whose count falls to 0 are pushed in ascending order.
+ * The outputs must not be the inputs, nor may the two weights overlap.
+ *
+ * Device-side problems: a length outside [0, max_kv_len], or whose kept rows
+ * with extra_rows exceed max_kv_len (MLA_VERIFY_DEV_BAD_LEN), or a table that does
+ * not hold it (BAD_INDPTR) gives length 0, no entries and weights of 0, and
+ * nothing of that request is given back.  When the stack or the capacity runs
+ * out the longest leading run of requests that fits is served and later ones
+ * get none (CAPACITY): their old tables stay valid.  (A free_count outside [0,
+ * num_slots / page_size] serves nobody and stays.)  A page outside the cache is
+ * reported (BAD_SLOT): it stays in the table uncounted, its rows are copied as
+ * zeros, or it is left out of the pool.  A count that contradicts its use is
+ * reported (BAD_REF) as by mla_verify_fork_kv and mla_verify_free_kv.
+ *
+ * budget >= 0, sink >= 0, recent >= 0, sink + recent <= budget, extra_rows in
+ * [0, max_kv_len], capacity in [0, 2^31), else MLA_VERIFY_ERR_ARG; the layers as
+ * for mla_verify_fork_kv; plans that mla_verify_attn_shared refuses give
+ * MLA_VERIFY_ERR_SHAPE.  Capturable, allocates nothing, shares the plan's
+ * workspace.
+ */
+int mla_verify_evict_kv(mla_verify_plan* plan, int batch, const float* weights,
+                        int64_t weight_stride, int budget, int sink, int recent,
+                        const int32_t* kv_indices, const int32_t* kv_indptr,
+                        const int32_t* kv_lens, void* kv_cache, int num_layers,
+                        int64_t layer_stride, int extra_rows, int32_t* page_refs,
+                        int32_t* free_pages, int32_t* free_count, int32_t* new_indices,
+                        int64_t capacity, int32_t* new_indptr, int32_t* new_lens,
+                        float* new_weights, int64_t new_weight_stride, int64_t new_width,
+                        void* stream);
 
 /*
  * Allocation-free verify attention, for callers that cannot allocate device

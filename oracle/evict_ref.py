@@ -80,7 +80,8 @@ def evict_kv(weights, budget, sink, recent, extra, page, kv_indices, kv_indptr, 
             old = list(kv_indices[p0:p1])
             if page == 1:
                 stay = [old[j] for j in kept]
-                left = [old[j] for j in range(len(old)) if j not in set(kept)]
+                stays = set(kept)
+                left = [old[j] for j in range(len(old)) if j not in stays]
             else:
                 count = -(-n // page) if n <= budget else sink // page
                 stay, left = old[:count], old[count:]

@@ -97,6 +97,9 @@ SIGNATURES = {
     "mla_verify_fork_kv": (_I, [_P, _I, _P, _I, _P, _P, _P, _P, _I, ctypes.c_int64, _I, _P, _P, _P, _P,
                                 ctypes.c_int64, _P, _P, _P]),
     "mla_verify_free_kv": (_I, [_P, _I, _P, _P, _P, _P, _P, _P]),
+    "mla_verify_evict_kv": (_I, [_P, _I, _P, ctypes.c_int64, _I, _I, _I, _P, _P, _P, _P, _I, ctypes.c_int64,
+                                 _I, _P, _P, _P, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int64,
+                                 ctypes.c_int64, _P]),
     "mla_verify_strerror": (ctypes.c_char_p, [_I]),
     "mla_verify_version": (_I, []),
 }
@@ -702,6 +705,66 @@ def free_kv(plan: Plan, kv_indices, kv_indptr, page_refs, free_pages, free_count
         plan.handle, B, kv_indices.data_ptr(), kv_indptr.data_ptr(), page_refs.data_ptr(),
         free_pages.data_ptr(), free_count.data_ptr(), _stream_ptr(stream))
     _check(st, "mla_verify_free_kv")
+
+
+def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, kv_cache, page_refs,
+             free_pages, free_count, sink: int = 0, recent: int = 0, extra_rows: int = 0,
+             new_indices=None, new_indptr=None, new_lens=None, new_weights=None, stream=None):
+    """Cut requests of more than ``budget`` rows down to it; returns
+    (new_indices, new_indptr, new_lens, new_weights).
+
+    Kept, in their order: the first ``sink`` rows, the last ``recent`` rows and
+    of the others those with the largest ``weights`` ([B, W >= max_kv_len]
+    fp32), the lowest index first among equals.  Page size 64: kept rows behind
+    the first sink // 64 pages move to fresh pages of the pool, in every layer
+    of kv_cache ([num_slots, 576] or [layers, num_slots, 576] bf16); page size
+    1: no row moves and kv_cache may be None.  Entries that are left lose a
+    count.  page_refs / free_pages [num_slots / page size] and free_count [1]
+    int32 are the pool of fork_kv.  The new tables have room for ``extra_rows``
+    more rows each (included in new_lens); new_weights [B, W' >= max_kv_len]
+    holds the kept rows' weights, 0 behind them.  new_indices defaults to B *
+    (entries of budget + extra_rows); its length is the capacity.  Enqueued on
+    ``stream``, whose memory outputs that are not given come from; no sync.
+    """
+    B = kv_lens.shape[0]
+    dev = plan.torch_device
+    stride = _expect_weights(plan, weights, "weights", B)
+    _expect(kv_indices, "kv_indices", torch.int32, dev)
+    _expect(kv_indptr, "kv_indptr", torch.int32, dev, (B + 1,))
+    _expect(kv_lens, "kv_lens", torch.int32, dev, (B,))
+    units = plan.num_slots // plan.page_size
+    _expect(page_refs, "page_refs", torch.int32, dev, (units,))
+    _expect(free_pages, "free_pages", torch.int32, dev, (units,))
+    _expect(free_count, "free_count", torch.int32, dev, (1,))
+    cache, layers, layer_stride = None, 1, 0
+    if kv_cache is not None:
+        layers = 1 if kv_cache.dim() == 2 else kv_cache.shape[0]
+        layer = kv_cache if kv_cache.dim() == 2 else kv_cache[0]
+        _expect(layer, "kv_cache", torch.bfloat16, dev, (plan.num_slots, 576))
+        cache, layer_stride = kv_cache.data_ptr(), kv_cache.stride(0) if layers > 1 else 0
+    if new_indices is None or new_indptr is None or new_lens is None or new_weights is None:
+        with _allocating_on(stream, dev):
+            if new_indices is None:
+                entries = -(-min(budget + extra_rows, plan.max_kv_len) // plan.page_size)
+                new_indices = torch.empty(max(B * entries, 4), dtype=torch.int32, device=dev)
+            if new_indptr is None:
+                new_indptr = torch.empty(B + 1, dtype=torch.int32, device=dev)
+            if new_lens is None:
+                new_lens = torch.empty(B, dtype=torch.int32, device=dev)
+            if new_weights is None:
+                new_weights = torch.empty((B, weights.shape[1]), dtype=torch.float32, device=dev)
+    _expect(new_indices, "new_indices", torch.int32, dev)
+    _expect(new_indptr, "new_indptr", torch.int32, dev, (B + 1,))
+    _expect(new_lens, "new_lens", torch.int32, dev, (B,))
+    new_stride = _expect_weights(plan, new_weights, "new_weights", B)
+    st = load_library().mla_verify_evict_kv(
+        plan.handle, B, weights.data_ptr(), stride, budget, sink, recent, kv_indices.data_ptr(),
+        kv_indptr.data_ptr(), kv_lens.data_ptr(), cache, layers, layer_stride, extra_rows,
+        page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), new_indices.data_ptr(),
+        new_indices.numel(), new_indptr.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr(),
+        new_stride, new_weights.shape[1], _stream_ptr(stream))
+    _check(st, "mla_verify_evict_kv")
+    return new_indices, new_indptr, new_lens, new_weights
 
 
 def mla_verify_attn_host(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_lens,

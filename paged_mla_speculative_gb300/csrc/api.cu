@@ -69,12 +69,12 @@ struct mla_verify_plan {
   int max_tiles;
   int* sh_meta;
   int* sh_layout;
-  unsigned* page_bits;    // free_kv, page_size 64: one bit per page of the cache, behind the error word
+  unsigned* page_bits;    // free_kv, evict_kv: one bit per page (or slot) of the cache, behind the error word
   int sh_cut;             // clusters that can share a call's tiles
   mlav::SharedMaps sh_maps;
 };
 
-// The first 256 bytes at mla_verify_plan::err: the error word, and fork_kv's ticket.
+// The first 256 bytes at mla_verify_plan::err: the error word, and fork_kv's and evict_kv's ticket.
 constexpr int kTicketWord = 16;
 
 namespace {
@@ -403,7 +403,7 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
   if (mlav::partial_mma_prepare() != cudaSuccess || mlav::partial_tc_prepare() != cudaSuccess ||
       mlav::partial_pair_prepare() != cudaSuccess || mlav::pack_kv_prepare() != cudaSuccess ||
       mlav::partial_shared_prepare() != cudaSuccess || mlav::page_pool_prepare() != cudaSuccess ||
-      mlav::weigh_prepare() != cudaSuccess)
+      mlav::weigh_prepare() != cudaSuccess || mlav::evict_prepare() != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
 
   mla_verify_plan* pl = new (std::nothrow) mla_verify_plan();
@@ -446,7 +446,7 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
   pl->st_idx_cap = idx_per_req * max_batch;
   const size_t qrows = static_cast<size_t>(max_batch) * pl->R;
 
-  const size_t err_bytes = 256 + (page_size == mlav::PAGE ? static_cast<size_t>(ceil_div(num_slots / mlav::PAGE, 32)) * 4 : 0);
+  const size_t err_bytes = 256 + static_cast<size_t>(ceil_div(num_slots / page_size, 32)) * 4;
 
   bool ok = cudaMalloc(&pl->ws_o, rows * mlav::D_V * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&pl->ws_lse, rows * sizeof(float)) == cudaSuccess &&
@@ -1188,6 +1188,74 @@ int mla_verify_free_kv(mla_verify_plan* pl, int batch, const int32_t* kv_indices
   a.err = pl->err;
   const long long entries = batch * ceil_div(pl->max_kv_len, mlav::PAGE);
   if (mlav::launch_free_kv(a, static_cast<int>(std::min<long long>(entries, INT32_MAX)), static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      note_done(pl, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return MLA_VERIFY_ERR_CUDA;
+  return MLA_VERIFY_OK;
+}
+
+int mla_verify_evict_kv(mla_verify_plan* pl, int batch, const float* weights, int64_t weight_stride, int budget, int sink,
+                        int recent, const int32_t* kv_indices, const int32_t* kv_indptr, const int32_t* kv_lens,
+                        void* kv_cache, int num_layers, int64_t layer_stride, int extra_rows, int32_t* page_refs,
+                        int32_t* free_pages, int32_t* free_count, int32_t* new_indices, int64_t capacity,
+                        int32_t* new_indptr, int32_t* new_lens, float* new_weights, int64_t new_weight_stride,
+                        int64_t new_width, void* stream) {
+  if (!pl || !weights || !kv_indices || !kv_indptr || !kv_lens || !page_refs || !free_pages || !free_count ||
+      !new_indices || !new_indptr || !new_lens || !new_weights || (pl->page_size > 1 && !kv_cache))
+    return MLA_VERIFY_ERR_NULL;
+  if (!aligned16(weights) || !aligned16(kv_indices) || !aligned16(kv_indptr) || !aligned16(kv_lens) || !aligned16(kv_cache) ||
+      !aligned16(page_refs) || !aligned16(free_pages) || !aligned16(free_count) || !aligned16(new_indices) ||
+      !aligned16(new_indptr) || !aligned16(new_lens) || !aligned16(new_weights))
+    return MLA_VERIFY_ERR_ALIGN;
+  if (!pl->shared_ok) return MLA_VERIFY_ERR_SHAPE;
+  if (batch < 1 || batch > pl->max_batch) return MLA_VERIFY_ERR_BATCH;
+  const int64_t most = INT64_MAX / 8 / batch;
+  if (budget < 0 || sink < 0 || recent < 0 || static_cast<int64_t>(sink) + recent > budget || extra_rows < 0 ||
+      extra_rows > pl->max_kv_len || capacity < 0 || capacity > INT32_MAX || weight_stride < pl->max_kv_len ||
+      weight_stride > most || new_width < pl->max_kv_len || new_weight_stride < new_width || new_weight_stride > most)
+    return MLA_VERIFY_ERR_ARG;
+  if (pl->page_size > 1 && (num_layers < 1 || num_layers > mlav::FORK_MAX_LAYERS || layer_stride < 0 || layer_stride % 8 ||
+                            (num_layers > 1 && layer_stride < pl->num_slots * mlav::D_QK)))
+    return MLA_VERIFY_ERR_ARG;
+  // Rows are read while others are written.
+  const float* end = weights + (batch - 1) * weight_stride + pl->max_kv_len;
+  const float* new_end = new_weights + (batch - 1) * new_weight_stride + new_width;
+  if ((weights < new_end && new_weights < end) || new_indices == kv_indices || new_indptr == kv_indptr || new_lens == kv_lens)
+    return MLA_VERIFY_ERR_ARG;
+  const int dev_status = check_device(pl);
+  if (dev_status != MLA_VERIFY_OK) return dev_status;
+  mlav::EvictArgs a{};
+  a.weights = weights;
+  a.stride = weight_stride;
+  a.budget = budget;
+  a.sink = sink;
+  a.recent = recent;
+  a.extra = extra_rows;
+  a.batch = batch;
+  a.page = pl->page_size;
+  a.max_kv_len = pl->max_kv_len;
+  a.kv_indices = kv_indices;
+  a.kv_indptr = kv_indptr;
+  a.kv_lens = kv_lens;
+  a.kv_cache = static_cast<uint16_t*>(kv_cache);
+  a.num_layers = num_layers;
+  a.layer_stride = layer_stride;
+  a.num_pages = static_cast<int>(pl->num_slots / pl->page_size);
+  a.page_refs = page_refs;
+  a.free_pages = free_pages;
+  a.free_count = free_count;
+  a.new_indices = new_indices;
+  a.capacity = capacity;
+  a.new_indptr = new_indptr;
+  a.new_lens = new_lens;
+  a.new_weights = new_weights;
+  a.new_stride = new_weight_stride;
+  a.new_width = new_width;
+  a.kept = pl->sh_meta;
+  a.kept_stride = static_cast<int64_t>(pl->pack_blocks) * 128;
+  a.page_bits = pl->page_bits;
+  a.ticket = reinterpret_cast<unsigned*>(pl->err) + kTicketWord;
+  a.err = pl->err;
+  if (mlav::launch_evict_kv(a, pl->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
       note_done(pl, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MLA_VERIFY_ERR_CUDA;
   return MLA_VERIFY_OK;

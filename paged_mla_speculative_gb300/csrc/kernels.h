@@ -235,4 +235,35 @@ struct FreeArgs {
 // `max_entries`: of the tables, as far as the host can tell.
 cudaError_t launch_free_kv(const FreeArgs& a, int max_entries, cudaStream_t stream);
 
+// Eviction of the rows with the smallest weights (evict_kv.cu).
+struct EvictArgs {
+  const float* weights;             // [batch] rows, stride floats apart
+  long long stride;
+  int budget, sink, recent, extra;
+  int batch, page, max_kv_len;      // page: rows of a page, 1 or 64
+  const int32_t* kv_indices;
+  const int32_t* kv_indptr;         // [batch + 1]
+  const int32_t* kv_lens;           // [batch]
+  uint16_t* kv_cache;               // bf16 [num_layers][num_pages * 64][576], layers layer_stride elements apart; pages only
+  int num_layers;
+  long long layer_stride;
+  int num_pages;                    // or slots
+  int32_t* page_refs;               // [num_pages]
+  int32_t* free_pages;              // [num_pages]
+  int32_t* free_count;              // [1]
+  int32_t* new_indices;             // [capacity] out
+  long long capacity;
+  int32_t* new_indptr;              // [batch + 1] out
+  int32_t* new_lens;                // [batch] out
+  float* new_weights;               // [batch] rows of new_width, new_stride floats apart, out
+  long long new_stride, new_width;
+  int32_t* kept;                    // plan workspace: [batch][kept_stride] rows that are kept, of evicted requests
+  long long kept_stride;
+  unsigned* page_bits;              // plan workspace, one bit per page, 0 between calls
+  unsigned* ticket;                 // plan workspace, 0 between calls
+  int* err;
+};
+cudaError_t evict_prepare();
+cudaError_t launch_evict_kv(const EvictArgs& a, int num_sms, cudaStream_t stream);
+
 }  // namespace mlav

@@ -26,9 +26,8 @@
 #include "common.cuh"
 #include "copy_ring.h"
 #include "kernels.h"
+#include "page_pool.cuh"
 #include "tc_ptx.cuh"
-
-#include <cooperative_groups.h>
 
 #include <algorithm>
 
@@ -250,7 +249,7 @@ __global__ void __launch_bounds__(FORK_THREADS) fork_kv_kernel(const ForkArgs a,
 // One cluster: counts lowered (the one thread that takes a count from 1 to 0
 // marks the page in a bit map), then the bit map read in order, so the pushed
 // pages ascend whatever order the counts fell in, and cleared for the next call.
-constexpr int FREE_THREADS = 1024;
+constexpr int FREE_THREADS = POOL_THREADS;
 constexpr int FREE_MAX_CTAS = 8;
 
 __global__ void __launch_bounds__(FREE_THREADS) free_kv_kernel(const FreeArgs a) {
@@ -259,7 +258,7 @@ __global__ void __launch_bounds__(FREE_THREADS) free_kv_kernel(const FreeArgs a)
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ int s_warp[FREE_THREADS / 32];
   __shared__ int s_total, s_bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x;
   const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
   if (tid == 0) s_bad = 0;
   __syncthreads();
@@ -275,69 +274,11 @@ __global__ void __launch_bounds__(FREE_THREADS) free_kv_kernel(const FreeArgs a)
   if (refused || !count_ok) return;   // the same in every CTA of the cluster
   int bad = 0;
   for (long long i = first + static_cast<long long>(rank) * FREE_THREADS + tid; i < end;
-       i += static_cast<long long>(ctas) * FREE_THREADS) {
-    const int page = a.kv_indices[i];
-    if (page < 0 || page >= a.num_pages) {
-      bad |= ERR_SLOT;
-      continue;
-    }
-    const int had = atomicSub(a.page_refs + page, 1);
-    if (had == 1) {
-      atomicOr(a.page_bits + (page >> 5), 1u << (page & 31));
-    } else if (had <= 0) {   // never raises a count to 1, so "1 to 0" stays unique
-      atomicAdd(a.page_refs + page, 1);
-      bad |= ERR_REF;
-    }
-  }
+       i += static_cast<long long>(ctas) * FREE_THREADS)
+    bad |= release_page(a.kv_indices[i], a.num_pages, a.page_refs, a.page_bits);
   if (bad) atomicOr(a.err, bad);
   cluster.sync();
-  // (Volatile: the words were set by other SMs' atomics.)
-  const volatile unsigned* bits = a.page_bits;
-  // This CTA's words of the bit map, in order: `per` consecutive ones per thread.
-  const int words = (a.num_pages + 31) / 32;
-  const int per = (words + ctas * FREE_THREADS - 1) / (ctas * FREE_THREADS);
-  const long long w0 = (static_cast<long long>(rank) * FREE_THREADS + tid) * per;
-  int mine = 0;
-  for (int k = 0; k < per; ++k)
-    if (w0 + k < words) mine += __popc(bits[w0 + k]);
-  int x = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_warp[warp] = x;
-  __syncthreads();
-  int before = 0, total = 0;
-  for (int w = 0; w < FREE_THREADS / 32; ++w) {
-    if (w < warp) before += s_warp[w];
-    total += s_warp[w];
-  }
-  if (tid == 0) s_total = total;
-  cluster.sync();
-  long long at = count + before + x - mine, all = 0;
-  for (int r = 0; r < ctas; ++r) {
-    const int t = *cluster.map_shared_rank(&s_total, r);
-    if (r < rank) at += t;
-    all += t;
-  }
-  if (mine)
-    for (int k = 0; k < per; ++k) {
-      if (w0 + k >= words) break;
-      unsigned w = bits[w0 + k];
-      if (w) a.page_bits[w0 + k] = 0;
-      while (w) {
-        const int bit = __ffs(static_cast<int>(w)) - 1;
-        w &= w - 1;
-        if (at < a.num_pages) a.free_pages[at] = static_cast<int32_t>((w0 + k) * 32 + bit);
-        ++at;
-      }
-    }
-  if (rank == 0 && tid == 0) {
-    if (count + all > a.num_pages) atomicOr(a.err, ERR_CAPACITY);
-    *a.free_count = static_cast<int32_t>(min(count + all, static_cast<long long>(a.num_pages)));
-  }
-  cluster.sync();   // no CTA leaves while another reads its total
+  push_marked(a.page_bits, a.num_pages, count, a.free_pages, a.free_count, a.err, s_warp, s_total);
 }
 
 }  // namespace
