@@ -7,8 +7,8 @@
 // evict_select_kernel, a cluster of CTAs per request: the weights as ordered
 // 32-bit keys in shared memory; the key of the last row that is kept by three
 // histograms (11, 11 and 10 bits) that the cluster's CTAs add up through
-// distributed shared memory; then one scan gives every kept row its new place
-// (rows above that key, rows equal to it, both in order).  Every CTA scans all
+// distributed shared memory; then one scan of the warps' counts gives every kept
+// row its new place (rows above that key, rows equal to it, both in order).  Every CTA scans all
 // requests' lengths itself for its place in the new tables and on the stack of
 // free pages, as fork_kv does: how many entries stay follows from the lengths
 // alone.  Pages of 64: those that hold protected leading rows alone stay, the
@@ -16,8 +16,9 @@
 // requests are not written, and no row is read after it was overwritten), all
 // others of the table are given back.  Single slots: kept slots stay, no row
 // moves.
-// evict_copy_kernel: the kept rows of every layer into the fresh pages.
-// evict_push_kernel: pages whose count fell to 0, in ascending order.
+// evict_copy_kernel: the kept rows of every layer into the fresh pages, and
+// beside it the pages whose count fell to 0, in ascending order, onto the stack
+// (evict_push_kernel where nothing is copied).
 //
 // The copies are bound by HBM (1152 bytes read and written a row and layer);
 // the rest is a chain of dependent loads and cluster barriers.
@@ -38,7 +39,10 @@ constexpr int THREADS = 1024;
 constexpr int WARPS = THREADS / 32;
 constexpr int BINS = 2048;
 constexpr int MAX_CTAS = 8;                // per request
+constexpr int ROWS_PER_CTA = 12288;        // from which a request gets another CTA, where SMs are left: a cluster barrier is ~1 us
 constexpr int MAX_CACHED = 24576;          // keys that a CTA holds in shared memory
+constexpr int GROUP = 32;                  // strips of THREADS rows placed by one scan
+constexpr int FLIGHT = 4;                  // strips whose loads and atomics are under way together
 
 // Larger weights have larger keys; -0 is 0, NaN is below every number.
 __device__ __forceinline__ unsigned ordered(float w) {
@@ -52,7 +56,7 @@ __device__ __forceinline__ unsigned ordered(float w) {
 struct Item {
   int n, m, ip0, entries;     // rows, kept rows, the table
   int stay;                   // entries that stay, in order: the first ones (pages), the kept ones (slots)
-  long long total, fresh;     // entries of the new table, of them fresh
+  int total, fresh;           // entries of the new table, of them fresh
   int bad;
 };
 __device__ __forceinline__ Item load_item(const EvictArgs& a, int b) {
@@ -68,16 +72,13 @@ __device__ __forceinline__ Item load_item(const EvictArgs& a, int b) {
     x.entries = static_cast<int>(p1 - x.ip0);
     x.m = min(x.n, a.budget);
     x.stay = a.page == 1 ? x.m : x.n <= a.budget ? (x.n + a.page - 1) / a.page : a.sink / a.page;
-    x.total = (static_cast<long long>(x.m) + a.extra + a.page - 1) / a.page;
+    x.total = static_cast<int>((static_cast<long long>(x.m) + a.extra + a.page - 1) / a.page);
     x.fresh = x.total - x.stay;
   }
   if (x.bad) x.n = 0;
   return x;
 }
 
-struct Sums {
-  long long total, fresh;
-};
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -86,64 +87,75 @@ __device__ __forceinline__ long long warp_scan(long long x, int lane) {
   }
   return x;
 }
-// Inclusive scan over the CTA's threads; `all` receives the total.
+// Inclusive scan over a CTA of T threads; `all` receives the total.
+template <int T>
 __device__ __forceinline__ long long cta_scan(long long x, long long* s_warp, long long& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   x = warp_scan(x, lane);
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  all = 0;
-  for (int w = 0; w < WARPS; ++w) {
-    if (w == warp) x += all;
-    all += s_warp[w];
+  if (warp == 0) {
+    const long long y = warp_scan(lane < T / 32 ? s_warp[lane] : 0, lane);
+    if (lane < T / 32) s_warp[lane] = y;
   }
-  return x;
+  __syncthreads();
+  all = s_warp[T / 32 - 1];
+  return x + (warp ? s_warp[warp - 1] : 0);
 }
+// Two counts below 2^32 in one word.
+__device__ __forceinline__ long long pair_of(int hi, int lo) { return static_cast<long long>(hi) << 32 | static_cast<unsigned>(lo); }
+__device__ __forceinline__ long long high(long long x) { return x >> 32; }
+__device__ __forceinline__ long long low(long long x) { return x & 0xffffffffll; }
 
-// grid: `ctas` CTAs (a cluster) per request.
+// grid: `ctas` CTAs (a cluster) per request.  (The sums of all requests'
+// entries stay below 2^31: so does max_batch * max_kv_len.)
 __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArgs a, int cached) {
   extern __shared__ unsigned s_keys[];
   __shared__ int s_hist[BINS];
-  __shared__ long long s_warp[WARPS];
-  __shared__ Sums s_mine, s_fit;
+  __shared__ long long s_warp[WARPS], s_place[GROUP * WARPS];
+  __shared__ long long s_mine, s_fit, s_count;
   __shared__ unsigned long long s_last[2];
   __shared__ Item s_item;
   __shared__ int s_bin, s_above;
-  __shared__ long long s_count;
   asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), ctas = static_cast<int>(cluster.num_blocks());
-  const int b = blockIdx.x / ctas, tid = threadIdx.x;
+  auto sync = [&]() {
+    if (ctas > 1) cluster.sync();
+    else __syncthreads();
+  };
+  const int b = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float* row = a.weights + b * a.stride;
   const int height = *a.free_count;
+  Item item{};
+  if (tid < a.batch) item = load_item(a, tid);
+  // A CTA that has the request alone loads the weights before it knows how many.
+  const bool alone = ctas == 1 && a.max_kv_len <= cached;
+  if (alone)
+    for (int i = tid; i < a.max_kv_len; i += THREADS) s_keys[i] = ordered(row[i]);
   const bool height_ok = height >= 0 && height <= a.num_pages;
   const long long left = height_ok ? height : -1;   // a stack that is out of order serves nobody
   if (tid < 2) s_last[tid] = 0;
-  Sums before{0, 0};
+  long long before = 0;                             // entries, of them fresh
   for (int base = 0; base < a.batch; base += THREADS) {
     const int i = base + tid;
-    Sums x{0, 0};
+    if (base > 0) item = i < a.batch ? load_item(a, i) : Item{};
+    if (i == b) s_item = item;
+    const long long own = pair_of(item.total, item.fresh);
+    long long all;
+    const long long x = before + cta_scan<THREADS>(own, s_warp, all);
     if (i < a.batch) {
-      const Item it = load_item(a, i);
-      x = Sums{it.total, it.fresh};
-      if (i == b) s_item = it;
-    }
-    const Sums own = x;
-    Sums all;
-    x.total = before.total + cta_scan(x.total, s_warp, all.total);
-    x.fresh = before.fresh + cta_scan(x.fresh, s_warp, all.fresh);
-    if (i < a.batch) {
-      if (x.total <= a.capacity && x.fresh <= left) {   // ends never fall: the largest that fits
-        if (i <= b) atomicMax(&s_last[0], static_cast<unsigned long long>(x.total));
-        atomicMax(&s_last[1], static_cast<unsigned long long>(x.fresh));
+      if (high(x) <= a.capacity && low(x) <= left) {   // ends never fall: the largest that fits
+        if (i <= b) atomicMax(&s_last[0], static_cast<unsigned long long>(high(x)));
+        atomicMax(&s_last[1], static_cast<unsigned long long>(low(x)));
       }
       if (i == b) {
-        s_mine = Sums{x.total - own.total, x.fresh - own.fresh};
+        s_mine = x - own;
         s_fit = x;
       }
     }
-    before.total += all.total;
-    before.fresh += all.fresh;
+    before += all;
   }
   __syncthreads();
   if (tid == 0) {   // the last CTA that has read the height lowers it
@@ -155,7 +167,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
     }
   }
   const Item it = s_item;
-  const bool fits = s_fit.total <= a.capacity && s_fit.fresh <= left;
+  const bool fits = high(s_fit) <= a.capacity && low(s_fit) <= left;
   const bool served = fits && !it.bad;
   if (rank == 0 && tid == 0) {
     if (it.bad) atomicOr(a.err, it.bad);
@@ -172,118 +184,17 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
 
   const int n = it.n;
   const bool over = n > a.budget;
-  const float* row = a.weights + b * a.stride;
   const int32_t* held = a.kv_indices + it.ip0;
-  int32_t* table = a.new_indices + s_mine.total;
-  const int lo = a.sink, hi = n - a.recent;    // rows lo .. hi - 1 are chosen among, when the request is over the budget
-  // This CTA's rows: `per` consecutive ones per thread (an odd number, so that
-  // a warp's keys lie in different banks).
-  const int per = static_cast<int>((n + all_threads - 1) / all_threads) | 1;
-  const long long first = static_cast<long long>(rank) * THREADS * per;
-  const int count = static_cast<int>(max(0LL, min(static_cast<long long>(THREADS) * per, n - first)));
-  const int j0 = static_cast<int>(min(first, static_cast<long long>(n)));
-  const bool in_smem = count <= cached;
-  int k = a.budget - a.sink - a.recent;        // to be chosen
-  unsigned cut = 0xffffffffu;                  // the key of the last one chosen
-  int equal = 0;                               // of the rows with that key, how many
-  if (over) {
-    auto key_at = [&](int i) { return in_smem ? s_keys[i] : ordered(row[j0 + i]); };
-    if (in_smem)
-      for (int i = tid; i < count; i += THREADS) s_keys[i] = ordered(row[j0 + i]);
-    if (k > 0) {
-      unsigned prefix = 0;
-      for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        for (int i = tid; i < BINS; i += THREADS) s_hist[i] = 0;
-        __syncthreads();
-        for (int i0 = 0; i0 < count; i0 += THREADS) {
-          const int i = i0 + tid, j = j0 + i;
-          bool mine = i < count && j >= lo && j < hi;
-          const unsigned key = mine ? key_at(i) : 0;
-          mine = mine && (pass == 0 || (key >> (shift + bits)) == prefix);
-          const int bin = mine ? static_cast<int>((key >> shift) & ((1u << bits) - 1)) : -1;
-          int same;
-          __match_all_sync(0xffffffffu, bin, &same);
-          if (same) {   // (many rows of one weight: one addition for the warp)
-            if (bin >= 0 && (tid & 31) == 0) atomicAdd(s_hist + bin, 32);
-          } else if (bin >= 0) {
-            atomicAdd(s_hist + bin, 1);
-          }
-        }
-        cluster.sync();
-        // The bin, from the top, in which the k-th row lies: two bins per thread.
-        const int top = BINS - 1 - 2 * tid;
-        int h0 = 0, h1 = 0;
-        for (int r = 0; r < ctas; ++r) {
-          const int* h = cluster.map_shared_rank(s_hist, r);
-          h0 += h[top];
-          h1 += h[top - 1];
-        }
-        long long all;
-        const long long end = cta_scan(h0 + h1, s_warp, all), start = end - h0 - h1;
-        if (start < k && k <= end) {
-          const bool upper = k <= start + h0;
-          s_bin = upper ? top : top - 1;
-          s_above = static_cast<int>(upper ? start : start + h0);
-        }
-        cluster.sync();   // histograms are read, s_bin is set
-        prefix = (prefix << bits) | static_cast<unsigned>(s_bin);
-        k -= s_above;
-      }
-      cut = prefix;
-      equal = k;
-    }
-    __syncthreads();
-  }
-  // Rows above the cut (or protected) and rows equal to it, before each
-  // thread's, in order: its kept rows' new places.
-  int above = 0, ties = 0;
-  const int t0 = min(tid * per, count), t1 = min(t0 + per, count);
-  auto kind = [&](int i) {   // 1: kept, 2: kept while there are fewer than `equal`, 0: not
-    const int j = j0 + i;
-    if (!over || j < lo || j >= hi) return 1;
-    const unsigned key = in_smem ? s_keys[i] : ordered(row[j]);
-    return equal > 0 && key == cut ? 2 : equal > 0 && key > cut ? 1 : 0;
-  };
-  for (int i = t0; i < t1; ++i) {
-    const int x = kind(i);
-    above += x == 1;
-    ties += x == 2;
-  }
-  long long all;
-  const long long mine = static_cast<long long>(above) << 32 | static_cast<unsigned>(ties);
-  long long place = cta_scan(mine, s_warp, all) - mine;
-  if (tid == 0) s_count = all;
-  cluster.sync();
-  for (int r = 0; r < rank; ++r) place += *cluster.map_shared_rank(&s_count, r);
-  int a0 = static_cast<int>(place >> 32), e0 = static_cast<int>(place & 0xffffffffll), errs = 0;
-  for (int i = t0; i < t1; ++i) {
-    const int x = kind(i), j = j0 + i;
-    const bool kept = x == 1 || (x == 2 && e0 < equal);
-    const int to = a0 + min(e0, equal);
-    if (kept) {
-      new_row[to] = row[j];
-      if (a.page > 1) {
-        if (over) a.kept[b * a.kept_stride + to] = j;
-      } else {
-        const int slot = held[j];
-        table[to] = slot;
-        if (slot < 0 || slot >= a.num_pages) errs |= ERR_SLOT;
-      }
-    } else if (a.page == 1) {
-      errs |= release_page(held[j], a.num_pages, a.page_refs, a.page_bits);
-    }
-    a0 += x == 1;
-    e0 += x == 2;
-  }
-  // Entries: those that stay, fresh ones, and those that are left.
+  int32_t* table = a.new_indices + high(s_mine);
+  int errs = 0;
+  // Entries: those that stay (pages), fresh ones, and those that are left.
   for (long long e = (a.page == 1 ? it.stay : 0) + me; e < it.total; e += all_threads) {
     int page;
     if (e < it.stay) {
       page = held[e];
       if (page < 0 || page >= a.num_pages) errs |= ERR_SLOT;
     } else {
-      page = a.free_pages[left - 1 - (s_mine.fresh + e - it.stay)];
+      page = a.free_pages[left - 1 - (low(s_mine) + e - it.stay)];
       if (page < 0 || page >= a.num_pages) errs |= ERR_SLOT;
       else if (atomicExch(a.page_refs + page, 1) != 0) errs |= ERR_REF;   // the stack held a page that is in use
     }
@@ -291,18 +202,216 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   }
   for (long long e = (a.page == 1 ? n : it.stay) + me; e < it.entries; e += all_threads)
     errs |= release_page(held[e], a.num_pages, a.page_refs, a.page_bits);
+
+  const int lo = a.sink, hi = n - a.recent;    // rows lo .. hi - 1 are chosen among, when the request is over the budget
+  // This CTA's rows: strips of THREADS rows.
+  const int strips_each = static_cast<int>((n + all_threads - 1) / all_threads);
+  const int j0 = static_cast<int>(min(static_cast<long long>(rank) * strips_each * THREADS, static_cast<long long>(n)));
+  const int count = min(strips_each * THREADS, n - j0), strips = (count + THREADS - 1) / THREADS;
+  const bool in_smem = count <= cached;
+  int k = a.budget - a.sink - a.recent;        // to be chosen
+  unsigned cut = 0xffffffffu;                  // the key of the last one chosen
+  int equal = 0;                               // of the rows with that key, how many
+  auto key_at = [&](int i) { return in_smem ? s_keys[i] : ordered(row[j0 + i]); };
+  if (over && k > 0) {
+    if (!alone && in_smem)
+      for (int i = tid; i < count; i += THREADS) s_keys[i] = ordered(row[j0 + i]);
+    unsigned prefix = 0;
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < BINS; i += THREADS) s_hist[i] = 0;
+      __syncthreads();
+      for (int s = 0; s < strips; ++s) {
+        const int i = s * THREADS + tid, j = j0 + i;
+        bool mine = i < count && j >= lo && j < hi;
+        const unsigned key = mine ? key_at(i) : 0;
+        mine = mine && (pass == 0 || (key >> (shift + bits)) == prefix);
+        const int bin = mine ? static_cast<int>((key >> shift) & ((1u << bits) - 1)) : -1;
+        int same;
+        __match_all_sync(0xffffffffu, bin, &same);
+        if (same) {   // (many rows of one weight: one addition for the warp)
+          if (bin >= 0 && lane == 0) atomicAdd(s_hist + bin, 32);
+        } else if (bin >= 0) {
+          atomicAdd(s_hist + bin, 1);
+        }
+      }
+      sync();
+      // The bin, from the top, in which the k-th row lies: two bins per thread.
+      const int top = BINS - 1 - 2 * tid;
+      int h0 = 0, h1 = 0;
+      for (int r = 0; r < ctas; ++r) {
+        const int* h = ctas > 1 ? cluster.map_shared_rank(s_hist, r) : s_hist;
+        h0 += h[top];
+        h1 += h[top - 1];
+      }
+      long long all;
+      const long long end = cta_scan<THREADS>(h0 + h1, s_warp, all), start = end - h0 - h1;
+      if (start < k && k <= end) {
+        const bool upper = k <= start + h0;
+        s_bin = upper ? top : top - 1;
+        s_above = static_cast<int>(upper ? start : start + h0);
+      }
+      sync();   // histograms are read, s_bin is set
+      prefix = (prefix << bits) | static_cast<unsigned>(s_bin);
+      k -= s_above;
+    }
+    cut = prefix;
+    equal = k;
+  }
+  // 1: kept, 2: kept while there are fewer than `equal`, 0: not (nor is there a row).
+  auto kind = [&](int i) {
+    const int j = j0 + i;
+    if (i >= count) return 0;
+    if (!over || j < lo || j >= hi) return 1;
+    if (equal == 0) return 0;
+    const unsigned key = key_at(i);
+    return key == cut ? 2 : key > cut ? 1 : 0;
+  };
+  // Rows above the cut (or protected) and rows equal to it that lie before the
+  // CTA's, then before each strip's and warp's: the kept rows' new places.
+  long long base = 0;
+  if (ctas > 1) {
+    int above = 0, ties = 0;
+    for (int s = 0; s < strips; ++s) {
+      const int x = kind(s * THREADS + tid);
+      above += x == 1;
+      ties += x == 2;
+    }
+    long long all;
+    cta_scan<THREADS>(pair_of(above, ties), s_warp, all);
+    if (tid == 0) s_count = all;
+    cluster.sync();
+    for (int r = 0; r < rank; ++r) base += *cluster.map_shared_rank(&s_count, r);
+  }
+  for (int g0 = 0; g0 < strips; g0 += GROUP) {
+    const int g1 = min(strips, g0 + GROUP), entries = (g1 - g0) * WARPS;
+    __syncthreads();
+    for (int s = g0; s < g1; ++s) {
+      const int x = kind(s * THREADS + tid);
+      const unsigned above = __ballot_sync(0xffffffffu, x == 1), ties = __ballot_sync(0xffffffffu, x == 2);
+      if (lane == 0) s_place[(s - g0) * WARPS + warp] = pair_of(__popc(above), __popc(ties));
+    }
+    __syncthreads();
+    const long long mine = tid < entries ? s_place[tid] : 0;
+    long long all;
+    const long long end = cta_scan<THREADS>(mine, s_warp, all);
+    if (tid < entries) s_place[tid] = base + end - mine;
+    base += all;
+    __syncthreads();
+    for (int s0 = g0; s0 < g1; s0 += FLIGHT) {
+      int to[FLIGHT], slot[FLIGHT], had[FLIGHT];   // to: the new place, -1 dropped, -2 no row
+      float w[FLIGHT];
+#pragma unroll
+      for (int u = 0; u < FLIGHT; ++u) {
+        const int s = s0 + u, i = s * THREADS + tid;
+        const int x = s < g1 ? kind(i) : 0;
+        const unsigned above = __ballot_sync(0xffffffffu, x == 1), ties = __ballot_sync(0xffffffffu, x == 2);
+        const unsigned lower = (1u << lane) - 1;
+        const long long place = s < g1 ? s_place[(s - g0) * WARPS + warp] : 0;
+        const int e = static_cast<int>(low(place)) + __popc(ties & lower);
+        to[u] = s >= g1 || i >= count                       ? -2
+                : x == 1 || (x == 2 && e < equal) ? static_cast<int>(high(place)) + __popc(above & lower) + min(e, equal)
+                                                  : -1;
+        w[u] = to[u] >= 0 ? row[j0 + i] : 0.f;
+        slot[u] = a.page == 1 && to[u] != -2 ? held[j0 + i] : 0;
+      }
+      if (a.page > 1) {
+#pragma unroll
+        for (int u = 0; u < FLIGHT; ++u)
+          if (to[u] >= 0) {
+            new_row[to[u]] = w[u];
+            if (over) a.kept[b * a.kept_stride + to[u]] = j0 + (s0 + u) * THREADS + tid;
+          }
+        continue;
+      }
+#pragma unroll
+      for (int u = 0; u < FLIGHT; ++u) {
+        had[u] = 2;
+        if (to[u] == -2) continue;
+        if (slot[u] < 0 || slot[u] >= a.num_pages) errs |= ERR_SLOT;
+        else if (to[u] == -1) had[u] = atomicSub(a.page_refs + slot[u], 1);
+        if (to[u] >= 0) {
+          new_row[to[u]] = w[u];
+          table[to[u]] = slot[u];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < FLIGHT; ++u) errs |= mark_released(slot[u], had[u], a.page_refs, a.page_bits);
+    }
+  }
   if (errs) atomicOr(a.err, errs);
-  cluster.sync();   // no CTA leaves while another reads its count
+  if (ctas > 1) cluster.sync();   // no CTA leaves while another reads its count
+}
+
+// By `parts` CTAs of T threads: the marked pages, in order, on the stack of
+// height `count`.  Each CTA adds up the words before its own; the last one
+// done clears the bit map for the next call and raises the height.
+template <int T>
+__device__ __forceinline__ void push_marked_part(const EvictArgs& a, int part, int parts, long long count, long long* s_warp, int& s_done) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int words = a.num_pages / 32 + (a.num_pages % 32 != 0);
+  const int each = ((words + parts - 1) / parts + 3) / 4 * 4;
+  const int w0 = static_cast<int>(min(static_cast<long long>(part) * each, static_cast<long long>(words))), w1 = min(words, w0 + each);
+  int sum = 0;
+  for (int w = 4 * tid; w < w0; w += 4 * T) {   // (w0 is a multiple of four)
+    const uint4 x = __ldcg(reinterpret_cast<const uint4*>(a.page_bits + w));
+    sum += __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w);
+  }
+  long long before = 0, all = 0;
+  if (part > 0) cta_scan<T>(sum, s_warp, before);
+  for (int w = w0; w < w1; w += T) {
+    const unsigned word = w + tid < w1 ? __ldcg(a.page_bits + w + tid) : 0;
+    const int mine = __popc(word);
+    long long these;
+    const long long at = count + before + all + cta_scan<T>(mine, s_warp, these) - mine;
+    all += these;
+    // A warp writes out its 32 words one by one, a lane per bit.
+    for (unsigned some = __ballot_sync(0xffffffffu, word != 0); some; some &= some - 1) {
+      const int k = __ffs(static_cast<int>(some)) - 1;
+      const unsigned x = __shfl_sync(0xffffffffu, word, k);
+      const long long to = __shfl_sync(0xffffffffu, at, k) + __popc(x & ((1u << lane) - 1));
+      if ((x >> lane & 1u) && to < a.num_pages) a.free_pages[to] = (w + warp * 32 + k) * 32 + lane;
+    }
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int done = 1;
+    if (parts > 1) {
+      atomicAdd(a.ticket + 2, static_cast<unsigned>(all));
+      __threadfence();
+      done = atomicAdd(a.ticket + 1, 1u) == static_cast<unsigned>(parts) - 1;
+      __threadfence();
+    }
+    s_done = done;
+    if (done) {
+      const long long pushed = parts > 1 ? static_cast<long long>(atomicExch(a.ticket + 2, 0u)) : all;
+      a.ticket[1] = 0;
+      if (count + pushed > a.num_pages) atomicOr(a.err, ERR_CAPACITY);
+      *a.free_count = static_cast<int32_t>(min(count + pushed, static_cast<long long>(a.num_pages)));
+    }
+  }
+  __syncthreads();
+  if (s_done)
+    for (int w = tid; w < words; w += T) a.page_bits[w] = 0;
 }
 
 // Rows of an evicted request, COPY_ROWS at a time, in some of the layers: nine
 // 16-byte granules in flight per lane (a warp takes four rows).
 constexpr int COPY_THREADS = 256, COPY_ROWS = COPY_THREADS / 32 * 4;
 
+// The grid's last column in x pushes the marked pages while the others copy.
 __global__ void __launch_bounds__(COPY_THREADS) evict_copy_kernel(const EvictArgs a, int layers_each) {
   __shared__ long long s_src[COPY_ROWS], s_dst[COPY_ROWS];
+  __shared__ long long s_warp[COPY_THREADS / 32];
+  __shared__ int s_done;
   asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
   const int tid = threadIdx.x;
+  if (blockIdx.x == gridDim.x - 1) {
+    const long long count = *a.free_count;
+    if (blockIdx.y == 0 && blockIdx.z == 0 && count >= 0 && count <= a.num_pages)   // (else reported, and nothing was given back)
+      push_marked_part<COPY_THREADS>(a, 0, 1, count, s_warp, s_done);
+    return;
+  }
   const int stay = a.sink / PAGE;
   const int i0 = stay * PAGE + static_cast<int>(blockIdx.x) * COPY_ROWS;
   for (int b = blockIdx.y; b < a.batch; b += gridDim.y) {
@@ -344,15 +453,13 @@ __global__ void __launch_bounds__(COPY_THREADS) evict_copy_kernel(const EvictArg
   }
 }
 
-// One cluster.
-__global__ void __launch_bounds__(POOL_THREADS) evict_push_kernel(const EvictArgs a) {
-  __shared__ int s_warp[POOL_THREADS / 32];
-  __shared__ int s_total;
+__global__ void __launch_bounds__(THREADS) evict_push_kernel(const EvictArgs a) {
+  __shared__ long long s_warp[WARPS];
+  __shared__ int s_done;
   asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
   const long long count = *a.free_count;
   if (count < 0 || count > a.num_pages) return;   // (reported, and nothing was given back)
-  cg::this_cluster().sync();                      // (every CTA has read the height)
-  push_marked(a.page_bits, a.num_pages, count, a.free_pages, a.free_count, a.err, s_warp, s_total);
+  push_marked_part<THREADS>(a, blockIdx.x, gridDim.x, count, s_warp, s_done);
 }
 
 }  // namespace
@@ -362,15 +469,16 @@ cudaError_t evict_prepare() {
 }
 
 cudaError_t launch_evict_kv(const EvictArgs& a, int num_sms, cudaStream_t stream) {
-  // CTAs per request: while they fill no SM twice and have two rows per thread.
+  // CTAs per request: more for long ones, while they fill no SM twice.
   int ctas = 1;
-  while (ctas < MAX_CTAS && 2LL * ctas * a.batch <= num_sms && a.max_kv_len > 2LL * THREADS * ctas) ctas *= 2;
-  const long long slice = ((a.max_kv_len + static_cast<long long>(ctas) * THREADS - 1) / (static_cast<long long>(ctas) * THREADS) | 1) * THREADS;
-  const int cached = static_cast<int>(std::min<long long>(slice, MAX_CACHED));
+  while (ctas < MAX_CTAS && 2LL * ctas * a.batch <= num_sms && a.max_kv_len > ROWS_PER_CTA * ctas) ctas *= 2;
+  const long long strips = (a.max_kv_len + static_cast<long long>(ctas) * THREADS - 1) / (static_cast<long long>(ctas) * THREADS);
+  const int cached = static_cast<int>(std::min<long long>(strips * THREADS, MAX_CACHED));
   cudaError_t e = launch_overlapping(evict_select_kernel, dim3(static_cast<unsigned>(ctas) * a.batch), THREADS,
                                      static_cast<size_t>(cached) * 4, stream, static_cast<unsigned>(ctas), a, cached);
+  if (e != cudaSuccess) return e;
   const int moved = std::min(a.budget, a.max_kv_len) - a.sink / PAGE * PAGE;
-  if (e == cudaSuccess && a.page > 1 && moved > 0) {
+  if (a.page > 1 && moved > 0) {
     const unsigned parts = static_cast<unsigned>((moved + COPY_ROWS - 1) / COPY_ROWS);
     const unsigned requests = static_cast<unsigned>(std::min(a.batch, 65535));
     // A CTA's rows are looked up once for several layers, where enough CTAs are left.
@@ -378,12 +486,10 @@ cudaError_t launch_evict_kv(const EvictArgs& a, int num_sms, cudaStream_t stream
     const int each = std::max(static_cast<int>(std::clamp<long long>(ctas_of_a_layer * a.num_layers / (16LL * num_sms), 1, 16)),
                               (a.num_layers + 65534) / 65535);
     const unsigned z = static_cast<unsigned>((a.num_layers + each - 1) / each);
-    e = launch_overlapping(evict_copy_kernel, dim3(parts, requests, z), COPY_THREADS, 0, stream, 1, a, each);
+    return launch_overlapping(evict_copy_kernel, dim3(parts + 1, requests, z), COPY_THREADS, 0, stream, 1, a, each);
   }
-  if (e != cudaSuccess) return e;
-  unsigned push = 1;
-  while (push < 8 && a.num_pages / 32 > 4LL * POOL_THREADS * push) push *= 2;
-  return launch_overlapping(evict_push_kernel, dim3(push), POOL_THREADS, 0, stream, push, a);
+  const unsigned push = static_cast<unsigned>(std::clamp(a.num_pages / 32 / THREADS, 1, 64));
+  return launch_overlapping(evict_push_kernel, dim3(push), THREADS, 0, stream, 1, a);
 }
 
 }  // namespace mlav

@@ -260,7 +260,7 @@ struct EvictArgs {
   int32_t* kept;                    // plan workspace: [batch][kept_stride] rows that are kept, of evicted requests
   long long kept_stride;
   unsigned* page_bits;              // plan workspace, one bit per page, 0 between calls
-  unsigned* ticket;                 // plan workspace, 0 between calls
+  unsigned* ticket;                 // plan workspace: three words, 0 between calls
   int* err;
 };
 cudaError_t evict_prepare();

@@ -10,11 +10,9 @@ namespace mlav {
 
 constexpr int POOL_THREADS = 1024;
 
-// One count less for `page`; the one thread that takes it from 1 to 0 marks it
-// in the bit map.  Returns the error bits.
-__device__ __forceinline__ int release_page(int page, int num_pages, int32_t* page_refs, unsigned* page_bits) {
-  if (page < 0 || page >= num_pages) return ERR_SLOT;
-  const int had = atomicSub(page_refs + page, 1);
+// What follows when a page's count fell from `had`: the one thread that took
+// it from 1 to 0 marks the page in the bit map.  Returns the error bits.
+__device__ __forceinline__ int mark_released(int page, int had, int32_t* page_refs, unsigned* page_bits) {
   if (had == 1) {
     atomicOr(page_bits + (page >> 5), 1u << (page & 31));
   } else if (had <= 0) {   // never raises a count to 1, so "1 to 0" stays unique
@@ -22,6 +20,11 @@ __device__ __forceinline__ int release_page(int page, int num_pages, int32_t* pa
     return ERR_REF;
   }
   return 0;
+}
+// One count less for `page`.
+__device__ __forceinline__ int release_page(int page, int num_pages, int32_t* page_refs, unsigned* page_bits) {
+  if (page < 0 || page >= num_pages) return ERR_SLOT;
+  return mark_released(page, atomicSub(page_refs + page, 1), page_refs, page_bits);
 }
 
 // By a whole cluster of CTAs of POOL_THREADS: the marked pages, in order, on
