@@ -74,8 +74,10 @@ struct mla_verify_plan {
   mlav::SharedMaps sh_maps;
 };
 
-// The first 256 bytes at mla_verify_plan::err: the error word, and fork_kv's and evict_kv's ticket.
-constexpr int kTicketWord = 16;
+// The first kHeaderBytes at mla_verify_plan::err: the error word, fork_kv's and
+// evict_kv's tickets, weigh_kv's counters.
+constexpr int kTicketWord = 16, kArrivedWord = 32;
+constexpr size_t kHeaderBytes = 4 * (kArrivedWord + 2 * mlav::SH_MAX_CLUSTERS);
 
 namespace {
 
@@ -437,7 +439,7 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
   pl->shared_ok = pl->k_plane <= INT32_MAX && 1LL * max_batch * pl->R <= INT32_MAX / 2 && max_batch < mlav::SH_MAX_BATCH;
   // The shared-prefix kernel's partials: two tiles per cluster, where any are cut.
   pl->sh_cut = pl->shared_ok ? shared_cut_clusters(pl) : 1;
-  // mla_verify_weigh_kv's parts and records lie there too.
+  // mla_verify_weigh_kv's parts lie there too.
   const size_t rows = std::max({static_cast<size_t>(cap) * pl->R,
                                 pl->sh_cut > 1 ? static_cast<size_t>(2 * pl->sh_cut) * mlav::SH_ROWS : 0,
                                 mlav::weigh_workspace_bytes(shared_clusters(pl)) / (mlav::D_V * sizeof(float)) + 1});
@@ -446,7 +448,7 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
   pl->st_idx_cap = idx_per_req * max_batch;
   const size_t qrows = static_cast<size_t>(max_batch) * pl->R;
 
-  const size_t err_bytes = 256 + static_cast<size_t>(ceil_div(num_slots / page_size, 32)) * 4;
+  const size_t err_bytes = kHeaderBytes + static_cast<size_t>(ceil_div(num_slots / page_size, 128)) * 16;
 
   bool ok = cudaMalloc(&pl->ws_o, rows * mlav::D_V * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&pl->ws_lse, rows * sizeof(float)) == cudaSuccess &&
@@ -484,7 +486,7 @@ int mla_verify_plan_create(mla_verify_plan** out, int max_batch, int num_drafts,
     return MLA_VERIFY_ERR_OOM;
   }
   pl->ws_bytes = rows * (mlav::D_V + 1) * sizeof(float) + err_bytes + packed_bytes + sync_bytes + shared_bytes;
-  pl->page_bits = reinterpret_cast<unsigned*>(pl->err) + 64;
+  pl->page_bits = reinterpret_cast<unsigned*>(pl->err) + kHeaderBytes / 4;
   if (cudaMemset(pl->err, 0, err_bytes) != cudaSuccess || cudaMemset(pl->pack_sync, 0, sync_bytes) != cudaSuccess ||
       cudaEventCreateWithFlags(&pl->done_ev, cudaEventDisableTiming) != cudaSuccess ||
       cudaStreamCreateWithFlags(&pl->aux, cudaStreamNonBlocking) != cudaSuccess ||
@@ -1039,6 +1041,7 @@ int mla_verify_weigh_kv(mla_verify_plan* pl, int batch, int64_t num_tokens, cons
   const int dev_status = check_device(pl);
   if (dev_status != MLA_VERIFY_OK) return dev_status;
   mlav::WeighParams p{};
+  p.kv = static_cast<const uint16_t*>(kv_cache);
   p.kv_indices = kv_indices;
   p.kv_indptr = kv_indptr;
   p.kv_lens = kv_lens;
@@ -1046,7 +1049,12 @@ int mla_verify_weigh_kv(mla_verify_plan* pl, int batch, int64_t num_tokens, cons
   p.lse = lse;
   p.weights = weights;
   p.stride = weight_stride;
-  p.scale_log2 = scale * mlav::kLog2e;
+  // The tensor cores cut what they have summed so far, towards zero, to fp32:
+  // as measured, a score of magnitude s comes out 3.8 2^-23 s too small on
+  // average (half a unit in the last place for each 32 of its dims).  Scores
+  // are raised by that much: weights are then off by 0.4e-6 of themselves where
+  // they were by 3.0e-6.
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * (1.0 + 3.8 / 8388608.0));
   p.batch = batch;
   p.num_tokens = static_cast<int>(num_tokens);
   p.H = pl->H;
@@ -1055,7 +1063,7 @@ int mla_verify_weigh_kv(mla_verify_plan* pl, int batch, int64_t num_tokens, cons
   p.max_kv_len = pl->max_kv_len;
   p.clusters = shared_clusters(pl);
   p.part = pl->ws_o;
-  p.cut = reinterpret_cast<mlav::WeighCut*>(pl->ws_o + static_cast<size_t>(p.clusters) * 2 * 256);
+  p.arrived = reinterpret_cast<unsigned*>(pl->err) + kArrivedWord;
   p.err = pl->err;
   mlav::WeighMaps maps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -95,13 +95,10 @@ __device__ __forceinline__ long long cta_scan(long long x, long long* s_warp, lo
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    const long long y = warp_scan(lane < T / 32 ? s_warp[lane] : 0, lane);
-    if (lane < T / 32) s_warp[lane] = y;
-  }
-  __syncthreads();
-  all = s_warp[T / 32 - 1];
-  return x + (warp ? s_warp[warp - 1] : 0);
+  const long long y = warp_scan(lane < T / 32 ? s_warp[lane] : 0, lane);   // (by every warp: no third barrier)
+  all = __shfl_sync(0xffffffffu, y, T / 32 - 1);
+  const long long before = __shfl_sync(0xffffffffu, y, max(warp - 1, 0));
+  return x + (warp ? before : 0);
 }
 // Two counts below 2^32 in one word.
 __device__ __forceinline__ long long pair_of(int hi, int lo) { return static_cast<long long>(hi) << 32 | static_cast<unsigned>(lo); }
@@ -111,8 +108,8 @@ __device__ __forceinline__ long long low(long long x) { return x & 0xffffffffll;
 // grid: `ctas` CTAs (a cluster) per request.  (The sums of all requests'
 // entries stay below 2^31: so does max_batch * max_kv_len.)
 __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArgs a, int cached) {
-  extern __shared__ unsigned s_keys[];
-  __shared__ int s_hist[BINS];
+  extern __shared__ float s_weights[];
+  __shared__ int s_hist[BINS], s_bins[WARPS];
   __shared__ long long s_warp[WARPS], s_place[GROUP * WARPS];
   __shared__ long long s_mine, s_fit, s_count;
   __shared__ unsigned long long s_last[2];
@@ -133,7 +130,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   // A CTA that has the request alone loads the weights before it knows how many.
   const bool alone = ctas == 1 && a.max_kv_len <= cached;
   if (alone)
-    for (int i = tid; i < a.max_kv_len; i += THREADS) s_keys[i] = ordered(row[i]);
+    for (int i = tid; i < a.max_kv_len; i += THREADS) s_weights[i] = row[i];
   const bool height_ok = height >= 0 && height <= a.num_pages;
   const long long left = height_ok ? height : -1;   // a stack that is out of order serves nobody
   if (tid < 2) s_last[tid] = 0;
@@ -187,21 +184,11 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   const int32_t* held = a.kv_indices + it.ip0;
   int32_t* table = a.new_indices + high(s_mine);
   int errs = 0;
-  // Entries: those that stay (pages), fresh ones, and those that are left.
-  for (long long e = (a.page == 1 ? it.stay : 0) + me; e < it.total; e += all_threads) {
-    int page;
-    if (e < it.stay) {
-      page = held[e];
-      if (page < 0 || page >= a.num_pages) errs |= ERR_SLOT;
-    } else {
-      page = a.free_pages[left - 1 - (low(s_mine) + e - it.stay)];
-      if (page < 0 || page >= a.num_pages) errs |= ERR_SLOT;
-      else if (atomicExch(a.page_refs + page, 1) != 0) errs |= ERR_REF;   // the stack held a page that is in use
-    }
-    table[e] = page;
-  }
-  for (long long e = (a.page == 1 ? n : it.stay) + me; e < it.entries; e += all_threads)
-    errs |= release_page(held[e], a.num_pages, a.page_refs, a.page_bits);
+  // Entries: those that stay (pages), fresh ones, and those that are left.  Each
+  // thread's first of both kinds is loaded here, and used at the end.
+  const long long e0 = (a.page == 1 ? it.stay : 0) + me, l0 = (a.page == 1 ? n : it.stay) + me;
+  auto entry_at = [&](long long e) { return e < it.stay ? held[e] : a.free_pages[left - 1 - (low(s_mine) + e - it.stay)]; };
+  const int first_entry = e0 < it.total ? entry_at(e0) : 0, first_left = l0 < it.entries ? held[l0] : 0;
 
   const int lo = a.sink, hi = n - a.recent;    // rows lo .. hi - 1 are chosen among, when the request is over the budget
   // This CTA's rows: strips of THREADS rows.
@@ -212,10 +199,10 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   int k = a.budget - a.sink - a.recent;        // to be chosen
   unsigned cut = 0xffffffffu;                  // the key of the last one chosen
   int equal = 0;                               // of the rows with that key, how many
-  auto key_at = [&](int i) { return in_smem ? s_keys[i] : ordered(row[j0 + i]); };
+  auto weight_at = [&](int i) { return in_smem ? s_weights[i] : row[j0 + i]; };
   if (over && k > 0) {
-    if (!alone && in_smem)
-      for (int i = tid; i < count; i += THREADS) s_keys[i] = ordered(row[j0 + i]);
+    if (!alone && in_smem)   // (a thread uses the rows that it loaded)
+      for (int i = tid; i < count; i += THREADS) s_weights[i] = row[j0 + i];
     unsigned prefix = 0;
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
@@ -224,7 +211,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
       for (int s = 0; s < strips; ++s) {
         const int i = s * THREADS + tid, j = j0 + i;
         bool mine = i < count && j >= lo && j < hi;
-        const unsigned key = mine ? key_at(i) : 0;
+        const unsigned key = mine ? ordered(weight_at(i)) : 0;
         mine = mine && (pass == 0 || (key >> (shift + bits)) == prefix);
         const int bin = mine ? static_cast<int>((key >> shift) & ((1u << bits) - 1)) : -1;
         int same;
@@ -244,12 +231,32 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
         h0 += h[top];
         h1 += h[top - 1];
       }
-      long long all;
-      const long long end = cta_scan<THREADS>(h0 + h1, s_warp, all), start = end - h0 - h1;
-      if (start < k && k <= end) {
-        const bool upper = k <= start + h0;
-        s_bin = upper ? top : top - 1;
-        s_above = static_cast<int>(upper ? start : start + h0);
+      // (The warp in which it lies, by every warp; the lane, by that one.)
+      const int warp_sum = __reduce_add_sync(0xffffffffu, h0 + h1);
+      if (lane == 0) s_bins[warp] = warp_sum;
+      __syncthreads();
+      int upto = s_bins[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int at = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, upto >= k))) - 1;
+      const int earlier = at > 0 ? __shfl_sync(0xffffffffu, upto, max(at - 1, 0)) : 0;
+      if (warp == at) {
+        int end = h0 + h1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, end, o);
+          if (lane >= o) end += y;
+        }
+        end += earlier;
+        const int start = end - h0 - h1;
+        if (start < k && k <= end) {
+          const bool upper = k <= start + h0;
+          s_bin = upper ? top : top - 1;
+          s_above = upper ? start : start + h0;
+        }
       }
       sync();   // histograms are read, s_bin is set
       prefix = (prefix << bits) | static_cast<unsigned>(s_bin);
@@ -264,7 +271,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
     if (i >= count) return 0;
     if (!over || j < lo || j >= hi) return 1;
     if (equal == 0) return 0;
-    const unsigned key = key_at(i);
+    const unsigned key = ordered(weight_at(i));
     return key == cut ? 2 : key > cut ? 1 : 0;
   };
   // Rows above the cut (or protected) and rows equal to it that lie before the
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
         to[u] = s >= g1 || i >= count                       ? -2
                 : x == 1 || (x == 2 && e < equal) ? static_cast<int>(high(place)) + __popc(above & lower) + min(e, equal)
                                                   : -1;
-        w[u] = to[u] >= 0 ? row[j0 + i] : 0.f;
+        w[u] = to[u] >= 0 ? (over && a.budget > a.sink + a.recent ? weight_at(i) : row[j0 + i]) : 0.f;
         slot[u] = a.page == 1 && to[u] != -2 ? held[j0 + i] : 0;
       }
       if (a.page > 1) {
@@ -339,6 +346,14 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
       for (int u = 0; u < FLIGHT; ++u) errs |= mark_released(slot[u], had[u], a.page_refs, a.page_bits);
     }
   }
+  for (long long e = e0; e < it.total; e += all_threads) {
+    const int page = e == e0 ? first_entry : entry_at(e);
+    table[e] = page;
+    if (page < 0 || page >= a.num_pages) errs |= ERR_SLOT;
+    else if (e >= it.stay && atomicExch(a.page_refs + page, 1) != 0) errs |= ERR_REF;   // the stack held a page that is in use
+  }
+  for (long long e = l0; e < it.entries; e += all_threads)
+    errs |= release_page(e == l0 ? first_left : held[e], a.num_pages, a.page_refs, a.page_bits);
   if (errs) atomicOr(a.err, errs);
   if (ctas > 1) cluster.sync();   // no CTA leaves while another reads its count
 }
@@ -353,6 +368,7 @@ __device__ __forceinline__ void push_marked_part(const EvictArgs& a, int part, i
   const int each = ((words + parts - 1) / parts + 3) / 4 * 4;
   const int w0 = static_cast<int>(min(static_cast<long long>(part) * each, static_cast<long long>(words))), w1 = min(words, w0 + each);
   int sum = 0;
+#pragma unroll 8
   for (int w = 4 * tid; w < w0; w += 4 * T) {   // (w0 is a multiple of four)
     const uint4 x = __ldcg(reinterpret_cast<const uint4*>(a.page_bits + w));
     sum += __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w);
@@ -392,7 +408,8 @@ __device__ __forceinline__ void push_marked_part(const EvictArgs& a, int part, i
   }
   __syncthreads();
   if (s_done)
-    for (int w = tid; w < words; w += T) a.page_bits[w] = 0;
+    for (int w = 4 * tid; w < words; w += 4 * T)   // (the map is padded to 16 bytes)
+      *reinterpret_cast<uint4*>(a.page_bits + w) = make_uint4(0, 0, 0, 0);
 }
 
 // Rows of an evicted request, COPY_ROWS at a time, in some of the layers: nine

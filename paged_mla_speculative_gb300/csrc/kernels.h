@@ -142,13 +142,8 @@ cudaError_t launch_chunk_prepare(const SharedParams& p, int num_sms, cudaStream_
 cudaError_t launch_chunk_join(const SharedParams& p, cudaStream_t stream);
 
 // The attention weight given to cached rows (weigh_kv.cu).
-struct WeighCut {                   // what a cluster shares with others of its first and its last block
-  int first_request, first_block, last_request, last_block;
-  int continues, goes_on;           // its first block began, its last ends in another cluster
-  int last_slot;                    // its last block is not its first
-  int pad;
-};
 struct WeighParams {
+  const uint16_t* kv;               // bf16 [num_slots][576]
   const int32_t* kv_indices;
   const int32_t* kv_indptr;         // [batch + 1]
   const int32_t* kv_lens;           // [batch]
@@ -161,15 +156,15 @@ struct WeighParams {
   long long num_slots;
   int max_kv_len;
   int clusters;
-  WeighCut* cut;                    // [clusters]
-  float* part;                      // [2 * clusters][256]
+  float* part;                      // [2 * clusters][256]: sums of a cluster's first and last block
+  unsigned* arrived;                // [clusters][2], 0 between calls: clusters done with the block that this one shares first
   int* err;
 };
 struct WeighMaps {
-  CUtensorMap kv, q;                // rows of 576 bf16: the cache (boxes of a page, or of one slot) and the queries
+  CUtensorMap kv, q, q_full;        // rows of 576 bf16: the cache (boxes of a page) and the queries (32 and 128 rows)
 };
 constexpr size_t weigh_workspace_bytes(int clusters) {
-  return static_cast<size_t>(clusters) * (sizeof(WeighCut) + 2 * 256 * sizeof(float));
+  return static_cast<size_t>(clusters) * 2 * 256 * sizeof(float);
 }
 cudaError_t make_weigh_maps(WeighMaps* maps, const void* kv, long long num_slots, int page_size, const void* q, long long q_rows);
 cudaError_t weigh_prepare();

@@ -340,16 +340,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
       "l"(tmap), "r"(x), "r"(y), "r"(cluster_mbar)
       : "memory");
 }
-// Four rows of a 2-D tensor, one after another in shared memory, for a CTA
-// pair (the map's box is one row high).  Every lane that gets here issues its own.
-__device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const void* tmap, int x, int y0, int y1, int y2, int y3,
-                                                 uint32_t cluster_mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(cluster_mbar)
-      : "memory");
-}
 // TMA tile load of a 2-D tensor for this CTA alone, signalled on a barrier of its own.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t mbar) {
   asm volatile(

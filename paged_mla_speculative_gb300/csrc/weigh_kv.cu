@@ -12,22 +12,23 @@
 //     S^T[key, row] = K_block[256 x 576] . Q_tile[256 x 576]^T   in bf16, fp32 sums
 // so a key is a lane of tensor memory and its weight a sum in a thread's
 // register: no shuffles, no atomics, one order.  Keys come straight from the
-// cache (TMA boxes of a page, or tile::gather4 of four slots), in nine slots
+// cache (TMA boxes of a page, or 16-byte copies of single slots' rows), in nine slots
 // of 64 dims of which each is refilled as soon as the block's last tile has
 // read it; queries come through a ring of four slots of 64 dims.  bf16
 // products are exact and nothing is widened, so no value is out of range.
 // The steps (a tile against a block) of all requests are divided evenly over
 // the clusters in closed form (weigh_steps.h), by every CTA for itself.
 //
-// Where clusters share a block their sums meet in weigh_join_kernel, in
-// cluster order.
+// Where clusters share a block, the last of them to be done adds up all sums,
+// in cluster order (a launch for that took 2.5 us).
 //
 // What bounds it: with many query rows the tensor cores and the queries' way
 // from L2 (16 KB a slot and CTA for 256 x 256 x 64 products), with few the
 // keys' bytes.
 //
-// Roles (19 warps per CTA): warps 0-15 take the scores, warp 16 issues MMAs
-// (even CTA), warp 17 loads queries, warp 18 keys.  Every wait is bounded; a
+// Roles (24 warps per CTA): warps 0-15 take the scores, warp 16 issues MMAs
+// (even CTA), warp 17 loads queries, warps 18 and 19 keys, warps 20-23 hand
+// gathered keys over.  Every wait is bounded; a
 // pair whose wait runs out leaves NaN in all of its blocks.
 #include "kernels.h"
 #include "pair_common.cuh"
@@ -41,28 +42,32 @@ namespace {
 constexpr int KEYS = 256, TILE = 256;       // keys of a block, query rows of a tile
 constexpr int HKEYS = KEYS / 2;             // keys of a CTA
 constexpr int SCORE_WARPS = 16, MMA_WARP = 16, Q_WARP = 17, K_WARP = 18;
-constexpr int NTHREADS = 19 * 32;
+constexpr int K_WARPS = 2;                  // that gather slots; a page's boxes are loaded by the first
+constexpr int RELAY_WARP = K_WARP + K_WARPS, RELAYS = 4;   // that hand gathered chunks over
+constexpr int NWARPS = RELAY_WARP + RELAYS, NTHREADS = NWARPS * 32;
 constexpr int NCHUNK = 9;                   // chunks of 64 dims
 constexpr int K_SLOT = HKEYS * 128;         // 16 KB: 128 keys x 64 dims
 constexpr int Q_SLOT = (TILE / 2) * 128;    // 16 KB: 128 rows x 64 dims
 constexpr int NQ = 4;
-constexpr int Q_BOX = 32;                   // rows of a query load
+constexpr int Q_BOX = 32, Q_FULL = TILE / 2;   // rows of a query load: of part of a tile's half, of all of it
 constexpr int OFF_K = 0;
 constexpr int OFF_Q = OFF_K + NCHUNK * K_SLOT;
 constexpr int OFF_LSE = OFF_Q + NQ * Q_SLOT;                // float [16 warps][64] log-sum-exps of a warp's columns
 constexpr int OFF_SUM = OFF_LSE + SCORE_WARPS * 64 * 4;     // float [2][4][128] a block's sums by column group
 constexpr int OFF_MBAR = OFF_SUM + 2 * 4 * HKEYS * 4;
-constexpr int MB_KF = 0;     // [9] even CTA: key slot landed in both CTAs
+constexpr int MB_KF = 0;     // [9] even CTA: key slot landed in both CTAs (see MB_KL)
 constexpr int MB_KE = 9;     // [9] key slot read by its block's last MMAs
 constexpr int MB_QF = 18;    // [4] even CTA: query slot landed in both CTAs
 constexpr int MB_QE = 22;    // [4] query slot read
 constexpr int MB_SF = 26;    // [2] scores of a step done
 constexpr int MB_SE = 28;    // [2] even CTA: scores of a step read by both CTAs' warps
 constexpr int MB_DONE = 30;  // after an abort: every MMA issued is done
-constexpr int NMBAR = 31;
-constexpr int OFF_MISC = OFF_MBAR + NMBAR * 8 + 8;          // tmem base, abort flag, the peer's
-constexpr int OFF_PLAN = OFF_MISC + 16;                     // start of the share
-constexpr int SMEM_TOTAL = OFF_PLAN + 32 + 32 * 8;
+constexpr int MB_KL = 31;    // [9] gathered keys: the slot's copies landed in this CTA (MB_KF: in the odd one)
+constexpr int NMBAR = 40;
+constexpr int OFF_MISC = OFF_MBAR + NMBAR * 8;              // tmem base, abort flag, the peer's, "the last to be done"
+constexpr int OFF_PLAN = OFF_MISC + 16;                     // Cursor: the start of the share
+constexpr int OFF_SCAN = OFF_PLAN + 128;                    // long long [warps]
+constexpr int SMEM_TOTAL = OFF_SCAN + 32 * 8;
 static_assert(SMEM_TOTAL <= 232448, "shared memory budget");
 static_assert(OFF_MISC % 16 == 0 && OFF_PLAN % 16 == 0, "alignment");
 constexpr int TMEM_COLS = 512;              // two buffers of 256 columns
@@ -98,49 +103,35 @@ __device__ __forceinline__ bool load_request(const WeighParams& p, int b, Reques
   return false;
 }
 
-// A share of the work: `steps` steps from step `step` of the requests' steps
-// from request `request` on.
-struct Share {
-  long long step, steps;
-  int request;
-};
-
 // Where a role is: tile `t` of block `kb` of request `b`, whose first tile for
 // this cluster was t0.
 struct Cursor {
   Request r;
-  long long left;   // steps, this one among them
+  long long left;   // steps, this one among them; 0: the cluster has none
+  long long done, total;   // steps of the call before t0, and all
   int b, kb, t, t0;
-  // Moves to the request that has steps at or after b.
-  __device__ __forceinline__ void start(const WeighParams& p, const Share& sh) {
-    b = sh.request;
-    left = sh.steps;
-    if (left <= 0) return;
-    int errs = 0;
-    load_request(p, b, r, errs);
-    kb = static_cast<int>(r.s.block_at(sh.step));
-    t = t0 = static_cast<int>(r.s.first(kb) + sh.step - r.s.before(kb));
-  }
   // Tiles of this block that are the cluster's: t0 .. end - 1.
   __device__ __forceinline__ int end() const {
     return static_cast<int>(min(r.s.tiles, static_cast<long long>(t) + left));
   }
   // To the next block (the tiles up to end() are done); false at the end.
   __device__ __forceinline__ bool next_block(const WeighParams& p) {
-    left -= end() - t;
+    const int tiles = end() - t;
+    left -= tiles;
+    done += tiles;
     if (left <= 0) return false;
     if (++kb == r.s.blocks) {
       int errs = 0;
-      do ++b;
-      while (b < p.batch - 1 && !load_request_at(p, errs));
-      if (b == p.batch - 1) load_request(p, b, r, errs);
+      do {
+        if (++b >= p.batch) return false;   // (there is one: `left` says so)
+      } while (!load_request(p, b, r, errs));
       kb = 0;
     }
     t = t0 = static_cast<int>(r.s.first(kb));
     return true;
   }
-  __device__ __forceinline__ bool load_request_at(const WeighParams& p, int& errs) { return load_request(p, b, r, errs); }
 };
+static_assert(sizeof(Cursor) <= OFF_SCAN - OFF_PLAN, "shared memory");
 
 __device__ __forceinline__ uint32_t idesc(int rows) {   // bf16, both K-major
   return tc::idesc_f16(KEYS, 0, 1, 0, 0) | static_cast<uint32_t>(rows >> 3) << 17;
@@ -150,59 +141,76 @@ __device__ __forceinline__ int tile_columns(const Request& r, int H, int t) {
   return static_cast<int>(min(static_cast<long long>(TILE), (static_cast<long long>(r.c) * H - static_cast<long long>(t) * TILE + 31) / 32 * 32));
 }
 
-// The division: every CTA adds up all requests' steps itself (a few loads per
-// thread) and takes its cluster's even share.
-__device__ void plan_share(const WeighParams& p, int cluster, Share* share, long long* s_warp, bool report) {
+// The division: every CTA adds up all requests' steps itself (one round of
+// loads per NTHREADS requests) and takes its cluster's even share.
+__device__ __forceinline__ void plan_share(const WeighParams& p, int cluster, Cursor* start, long long* s_warp, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long total = 0, from = 0, to = 0;
+  Request r;
   int errs = 0;
+  long long own = 0;
+  auto load = [&](int b) {
+    own = 0;
+    if (b < p.batch && load_request(p, b, r, errs)) own = r.s.total();
+  };
+  // Inclusive sum over the CTA's threads.
+  auto scan = [&](long long x, long long& all) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    all = 0;
+    for (int w = 0; w < NWARPS; ++w) {
+      if (w == warp) x += all;
+      all += s_warp[w];
+    }
+    return x;
+  };
+  load(tid);
   // (tokens that are not divided: nothing is weighed)
   bool bad = false;
   for (int b = tid; b < p.batch; b += NTHREADS) {
     const int q0 = p.q_indptr[b], q1 = p.q_indptr[b + 1];
     bad |= q0 < 0 || q1 < q0 || q1 > p.num_tokens;
   }
-  if (tid == 0) *share = Share{0, 0, 0};
+  if (tid == 0) start->left = 0;
   if (__syncthreads_or(bad)) {
     if (report && tid == 0) atomicOr(p.err, ERR_INDPTR);
     return;
   }
-  for (int pass = 0; pass < 2; ++pass) {   // the total, then the place of `from` in it
-    long long before = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += NTHREADS) {
-      const int b = b0 + tid;
-      long long x = 0;
-      if (b < p.batch) {
-        Request r;
-        if (load_request(p, b, r, errs)) x = r.s.total();
-      }
-      const long long own = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      __syncthreads();
-      if (lane == 31) s_warp[warp] = x;
-      __syncthreads();
-      long long all = 0;
-      for (int w = 0; w < NTHREADS / 32; ++w) {
-        if (w == warp) x += all;
-        all += s_warp[w];
-      }
-      if (pass == 0) total += all;
-      x += before;   // inclusive
-      if (pass == 1 && own > 0 && x - own <= from && from < x) *share = Share{from - (x - own), to - from, b};
-      before += all;
-    }
-    if (pass == 0) {
-      const long long used = min(static_cast<long long>(p.clusters), total);
-      if (cluster >= used) break;
-      from = total * cluster / used;
-      to = total * (cluster + 1) / used;
-    }
+  long long all, total, sum = scan(own, total);
+  for (int b0 = NTHREADS; b0 < p.batch; b0 += NTHREADS) {
+    load(b0 + tid);
+    scan(own, all);
+    total += all;
   }
   if (report && errs) atomicOr(p.err, errs);
+  const long long used = min(static_cast<long long>(p.clusters), total);
+  if (cluster >= used) return;
+  const long long from = total * cluster / used, to = total * (cluster + 1) / used;
+  long long before = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += NTHREADS) {
+    if (p.batch > NTHREADS) {
+      load(b0 + tid);
+      sum = before + scan(own, all);
+      before += all;
+    }
+    if (own > 0 && sum - own <= from && from < sum) {   // one thread: the share starts in its request
+      Cursor c;
+      c.r = r;
+      c.left = to - from;
+      c.done = from;
+      c.total = total;
+      c.b = b0 + tid;
+      const long long step = from - (sum - own);
+      c.kb = static_cast<int>(r.s.block_at(step));
+      c.t = c.t0 = static_cast<int>(r.s.first(c.kb) + step - r.s.before(c.kb));
+      *start = c;
+    }
+  }
 }
 
 // Bounded wait of a warp; PEER: for barriers that the peer's threads arrive on.
@@ -223,19 +231,22 @@ __device__ __forceinline__ void wait_bar(uint32_t mbar, uint32_t parity, volatil
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
-    weigh_kernel(const WeighParams p, const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_q) {
+    weigh_kernel(const WeighParams p, const __grid_constant__ CUtensorMap tm_kv, const __grid_constant__ CUtensorMap tm_q,
+                 const __grid_constant__ CUtensorMap tm_q_full) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t rank = tc::cluster_rank(), peer = rank ^ 1u;
   const int cluster = blockIdx.x >> 1;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
-  Share* s_share = reinterpret_cast<Share*>(smem + OFF_PLAN);
+  volatile int* s_last = reinterpret_cast<volatile int*>(smem + OFF_MISC + 12);
+  Cursor* s_start = reinterpret_cast<Cursor*>(smem + OFF_PLAN);
   const uint32_t sbase = smem_u32(smem);
   const uint32_t mbar0 = sbase + OFF_MBAR;
   auto mbar = [&](int i) { return mbar0 + 8u * static_cast<uint32_t>(i); };
   if (tid == 0) {
-    for (int i = 0; i < NMBAR; ++i) tc::mbar_init(mbar(i), i == MB_SE || i == MB_SE + 1 ? 2 * SCORE_WARPS : 1);
+    for (int i = 0; i < NMBAR; ++i)
+      tc::mbar_init(mbar(i), i == MB_SE || i == MB_SE + 1 ? 2 * SCORE_WARPS : i >= MB_KL ? K_WARPS * 32 : i < MB_KF + NCHUNK && p.page_size == 1 ? 2 : 1);
     tc::mbar_fence_init();
     s_abort[0] = s_abort[1] = 0;
   }
@@ -249,21 +260,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
   auto even_mbar = [&](int i) { return even_mbar0 + 8u * static_cast<uint32_t>(i); };
   // Everything read from here on may have been written by the kernel before.
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  plan_share(p, cluster, s_share, reinterpret_cast<long long*>(smem + OFF_PLAN + 32), blockIdx.x == 0);
+  plan_share(p, cluster, s_start, reinterpret_cast<long long*>(smem + OFF_SCAN), blockIdx.x == 0);
   __syncthreads();
-  Share share = *s_share;
-  if (sbase & 1023) {   // the swizzled tiles need it (uniform over the pair)
-    if (tid == 0) {
-      atomicOr(p.err, ERR_INTERNAL);
-      *s_abort = 1;
-    }
-    __syncthreads();
-    share.steps = 0;
+  Cursor at = *s_start;
+  const bool working = at.left > 0 && !(sbase & 1023);
+  if (sbase & 1023 && tid == 0) {   // the swizzled tiles need it (uniform over the pair)
+    atomicOr(p.err, ERR_INTERNAL);
+    *s_abort = 1;
   }
-  Cursor at;
-  at.start(p, share);
 
-  if (share.steps > 0) {
+  if (working) {
     if (warp == Q_WARP) {
       int n = 0;   // slots filled
       do {
@@ -281,46 +287,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
               if (lane == 0) tc::mbar_arrive_expect(mbar(MB_QF + slot), 2 * boxes * Q_BOX * 128);
               __syncwarp();
             }
-            for (int x = 0; x < boxes; ++x)
-              tc::tma_load_2d_pair(sbase + OFF_Q + slot * Q_SLOT + x * Q_BOX * 128, &tm_q, 64 * c, row0 + x * Q_BOX,
-                                   even_mbar(MB_QF + slot));
+            if (half == Q_FULL)
+              tc::tma_load_2d_pair(sbase + OFF_Q + slot * Q_SLOT, &tm_q_full, 64 * c, row0, even_mbar(MB_QF + slot));
+            else
+              for (int x = 0; x < boxes; ++x)
+                tc::tma_load_2d_pair(sbase + OFF_Q + slot * Q_SLOT + x * Q_BOX * 128, &tm_q, 64 * c, row0 + x * Q_BOX,
+                                     even_mbar(MB_QF + slot));
           }
         }
       } while (!*s_abort && at.next_block(p));
-    } else if (warp == K_WARP) {
-      int blk = 0;
-      // Lane i's rows: four slots (page size 1), or its page's first (lanes 0
-      // and 1).  Rows behind the request's last and bad slots: row 0, whose
-      // scores nobody takes.
-      do {
-        int row[4];
-        const int j0 = at.kb * KEYS + static_cast<int>(rank) * HKEYS;
-        bool bad = false;
-        if (p.page_size == 1) {
+    } else if (warp >= RELAY_WARP) {
+      // Gathered chunks, once they landed, to the even CTA's MMA warp, in turn.
+      // The fence that shows ordinary writes to the tensor cores takes some
+      // 1500 cycles beside copies under way: by the MMA warp itself, chunk by
+      // chunk, it was the bound (16 decoding requests 80 us).
+      if (p.page_size == 1) {
+        int n = warp - RELAY_WARP;   // the chunk in the cluster's share
+        int blk = 0;
+        do {
+          for (; n < (blk + 1) * NCHUNK && !*s_abort; n += RELAYS) {
+            const int c = n % NCHUNK;
+            wait_bar<false>(mbar(MB_KL + c), static_cast<uint32_t>(blk & 1), s_abort, p.err);
+            tc::fence_async_smem();
+            if (lane == 0 && *s_abort == 0) tc::mbar_arrive_cluster(even_mbar(MB_KF + c));
+            __syncwarp();
+          }
+          ++blk;
+        } while (!*s_abort && at.next_block(p));
+      }
+    } else if (warp >= K_WARP && p.page_size == 1) {
+      // Slots, gathered by 16-byte copies: a warp has 64 of the CTA's 128 keys,
+      // eight lanes a row of 128 bytes, four rows at a time.  (tile::gather4,
+      // four rows an instruction, took 80 cycles each: 12 us a block.)  A
+      // thread's copies arrive on the slot's barrier by themselves.
+      constexpr int ROWS = HKEYS / K_WARPS, COPIES = ROWS / 4;
+      static_assert(ROWS == 64, "two rows per lane");
+      const int kw = warp - K_WARP, r4 = lane >> 3, col = lane & 7;
+      int next[2];   // the slots of the block's rows kw * 64 + lane, + 32
+      auto look_up = [&](const Cursor& c) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = j0 + 4 * lane + i;
-            long long s = j < at.r.n ? p.kv_indices[at.r.ip0 + j] : 0;
-            if (s < 0 || s >= p.num_slots) {
-              bad = true;
-              s = 0;
-            }
-            row[i] = static_cast<int>(s);
-          }
-        } else {
-          const int j = j0 + (lane & 1) * PAGE;
-          long long s = j < at.r.n ? p.kv_indices[at.r.ip0 + j / PAGE] : 0;
-          if (s < 0 || s >= p.num_slots / PAGE) {
-            bad = true;
-            s = 0;
-          }
-          row[0] = static_cast<int>(s) * PAGE;
-          row[1] = row[2] = row[3] = 0;
+        for (int i = 0; i < 2; ++i) {
+          const int j = c.kb * KEYS + static_cast<int>(rank) * HKEYS + kw * ROWS + 32 * i + lane;
+          next[i] = j < c.r.n ? p.kv_indices[c.r.ip0 + j] : 0;
         }
-        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, ERR_SLOT);
-        const int page0 = __shfl_sync(0xffffffffu, row[0], 0), page1 = __shfl_sync(0xffffffffu, row[0], 1);
+      };
+      look_up(at);
+      int blk = 0;
+      bool more = true;
+      while (more) {
+        // Rows behind the request's last and bad slots: row 0, whose scores
+        // nobody takes.
+        const bool bad0 = next[0] < 0 || next[0] >= p.num_slots, bad1 = next[1] < 0 || next[1] >= p.num_slots;
+        if (__any_sync(0xffffffffu, bad0 || bad1) && lane == 0) atomicOr(p.err, ERR_SLOT);
+        if (bad0) next[0] = 0;
+        if (bad1) next[1] = 0;
+        int slot[COPIES];   // of rows 4 i + r4
+#pragma unroll
+        for (int i = 0; i < COPIES; ++i) slot[i] = __shfl_sync(0xffffffffu, next[i >= COPIES / 2], (4 * i + r4) & 31);
+        more = at.next_block(p);
+        if (more) look_up(at);   // (arrives while this block's rows are on their way)
 #pragma unroll 1
         for (int c = 0; c < NCHUNK; ++c) {
+          if (blk > 0) wait_bar<false>(mbar(MB_KE + c), static_cast<uint32_t>((blk - 1) & 1), s_abort, p.err);
+          if (*s_abort) break;
+          // Rows 4 i + r4: their swizzle alternates.
+          const uint32_t dst = sbase + OFF_K + c * K_SLOT + kw * ROWS * 128 + r4 * 128;
+          const uint32_t even = (col ^ r4) << 4, odd = (col ^ (r4 + 4)) << 4;
+          const uint16_t* src = p.kv + 64 * c + 8 * col;
+#pragma unroll
+          for (int i = 0; i < COPIES; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst + i * 512 + (i & 1 ? odd : even)),
+                         "l"(src + static_cast<long long>(slot[i]) * D_QK)
+                         : "memory");
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(mbar(MB_KL + c)) : "memory");
+        }
+        if (*s_abort) break;
+        ++blk;
+      }
+      asm volatile("cp.async.wait_all;\n" ::: "memory");
+    } else if (warp == K_WARP) {
+      // Pages: two boxes a chunk.  Pages behind the request's last and bad
+      // ones: page 0, whose scores nobody takes.
+      int blk = 0, next;   // the block's page, of lanes 0 and 1
+      auto look_up = [&](const Cursor& c) {
+        const int j = c.kb * KEYS + static_cast<int>(rank) * HKEYS + (lane & 1) * PAGE;
+        next = j < c.r.n ? p.kv_indices[c.r.ip0 + j / PAGE] : 0;
+      };
+      look_up(at);
+      bool more = true;
+      while (more) {
+        const bool bad = next < 0 || next >= p.num_slots / PAGE;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, ERR_SLOT);
+        const int row = bad ? 0 : next * PAGE;
+        const int row0 = __shfl_sync(0xffffffffu, row, 0), row1 = __shfl_sync(0xffffffffu, row, 1);
+        more = at.next_block(p);
+        if (more) look_up(at);
+#pragma unroll 1
+        for (int c = 0; c < NCHUNK; ++c) {
+          if (c == 1 && more) {   // the next block's pages into L2, a lane per 1/9 of one
+            const int page = __shfl_sync(0xffffffffu, next, lane >= NCHUNK ? 1 : 0);
+            if (lane < 2 * NCHUNK && page >= 0 && page < p.num_slots / PAGE)
+              tc::prefetch_l2(p.kv + static_cast<long long>(page) * PAGE * D_QK + (lane % NCHUNK) * (PAGE * 64), PAGE * 128);
+            __syncwarp();
+          }
           if (blk > 0) wait_bar<false>(mbar(MB_KE + c), static_cast<uint32_t>((blk - 1) & 1), s_abort, p.err);
           if (*s_abort) break;
           if (rank == 0) {
@@ -328,16 +397,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
             __syncwarp();
           }
           const uint32_t dst = sbase + OFF_K + c * K_SLOT;
-          if (p.page_size == 1) {
-            tc::tma_gather4_pair(dst + lane * 512, &tm_kv, 64 * c, row[0], row[1], row[2], row[3], even_mbar(MB_KF + c));
-            __syncwarp();
-          } else {
-            tc::tma_load_2d_pair(dst, &tm_kv, 64 * c, page0, even_mbar(MB_KF + c));
-            tc::tma_load_2d_pair(dst + K_SLOT / 2, &tm_kv, 64 * c, page1, even_mbar(MB_KF + c));
-          }
+          tc::tma_load_2d_pair(dst, &tm_kv, 64 * c, row0, even_mbar(MB_KF + c));
+          tc::tma_load_2d_pair(dst + K_SLOT / 2, &tm_kv, 64 * c, row1, even_mbar(MB_KF + c));
         }
+        if (*s_abort) break;
         ++blk;
-      } while (!*s_abort && at.next_block(p));
+      }
     } else if (warp == MMA_WARP && rank == 0) {
       int n = 0, g = 0, blk = 0;   // query slots, steps, blocks so far
       do {
@@ -350,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll 1
           for (int c = 0; c < NCHUNK; ++c, ++n) {
             const int slot = n % NQ;
-            if (t == at.t) wait_bar<false>(mbar(MB_KF + c), static_cast<uint32_t>(blk & 1), s_abort, p.err);
+            if (t == at.t) wait_bar<true>(mbar(MB_KF + c), static_cast<uint32_t>(blk & 1), s_abort, p.err);
             wait_bar<false>(mbar(MB_QF + slot), static_cast<uint32_t>((n / NQ) & 1), s_abort, p.err);
             if (*s_abort) break;
             tc::fence_after_sync();
@@ -450,37 +515,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         s_sum[grp * HKEYS + key] = sum;
         named_sync(1, SCORE_WARPS * 32);
         if (grp == 0) {
-          const float v = (s_sum[key] + s_sum[HKEYS + key]) + (s_sum[2 * HKEYS + key] + s_sum[3 * HKEYS + key]);
-          if (!whole)
-            p.part[(2 * cluster + (blk > 0 ? 1 : 0)) * KEYS + static_cast<int>(rank) * HKEYS + key] = valid ? v : 0.f;
-          else if (valid)
-            *weight = had + v;
+          float v = (s_sum[key] + s_sum[HKEYS + key]) + (s_sum[2 * HKEYS + key] + s_sum[3 * HKEYS + key]);
+          if (*s_abort != 0) v = __int_as_float(0x7fc00000);
+          if (whole) {
+            if (valid) *weight = had + v;
+          } else {
+            // The block's steps are s0 .. s1 - 1 of the call: clusters first ..
+            // last have some of them, each in its first block, but the first
+            // of them in its last.
+            const long long s0 = at.done - (at.t0 - at.r.s.first(at.kb)), s1 = s0 + at.r.s.tiles - at.r.s.first(at.kb);
+            const long long used = min(static_cast<long long>(p.clusters), at.total);
+            const int first = static_cast<int>(((s0 + 1) * used - 1) / at.total), last = static_cast<int>((s1 * used - 1) / at.total);
+            const bool own = at.total * first / used < s0;   // it has another block before this one
+            float* part = p.part + static_cast<int>(rank) * HKEYS + key;
+            part[(2 * cluster + (blk > 0 ? 1 : 0)) * KEYS] = v;
+            __threadfence();
+            named_sync(2, HKEYS);
+            if (key == 0) *s_last = atomicAdd(p.arrived + 2 * first + rank, 1u) == static_cast<unsigned>(last - first);
+            named_sync(2, HKEYS);
+            if (*s_last) {
+              __threadfence();
+              float sum = __ldcg(part + (2 * first + (own ? 1 : 0)) * KEYS);
+              for (int c = first + 1; c <= last; ++c) sum += __ldcg(part + 2 * c * KEYS);
+              if (valid) *weight += sum;
+              if (key == 0) p.arrived[2 * first + rank] = 0;
+            }
+          }
         }
         ++blk;
       } while (at.next_block(p));
     }
   }
 
-  // Which blocks the cluster shares with others, for the merge.
-  if (rank == 0 && tid == 0) {
-    WeighCut cut{};
-    if (share.steps > 0) {
-      Cursor c;
-      c.start(p, share);
-      cut.first_request = c.b;
-      cut.first_block = c.kb;
-      cut.continues = c.t0 > c.r.s.first(c.kb);
-      int blocks = 0;
-      do {
-        cut.last_request = c.b;
-        cut.last_block = c.kb;
-        cut.goes_on = c.end() < c.r.s.tiles;
-        cut.last_slot = blocks > 0;
-        blocks = 1;
-      } while (c.next_block(p));
-    }
-    p.cut[cluster] = cut;
-  }
   tc::fence_before_sync();
   __syncthreads();
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -495,41 +561,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
       if (rank == 0) tc::commit_pair(mbar(MB_DONE));
       wait_drain(mbar(MB_DONE), 0, p.err);
     }
-    if (share.steps > 0 && tid < HKEYS) {
+    if (working && tid < HKEYS) {
       const float nan = __int_as_float(0x7fc00000);
-      Cursor c;
-      c.start(p, share);
-      int blk = 0;
+      Cursor c = *s_start;
       do {
         const int j = c.kb * KEYS + static_cast<int>(rank) * HKEYS + tid;
-        if (c.t0 != c.r.s.first(c.kb) || c.end() != c.r.s.tiles)
-          p.part[(2 * cluster + (blk > 0 ? 1 : 0)) * KEYS + static_cast<int>(rank) * HKEYS + tid] = nan;
-        else if (j < c.r.n)
+        if (c.t0 == c.r.s.first(c.kb) && c.end() == c.r.s.tiles && j < c.r.n)   // (shared blocks have it from their sums)
           p.weights[static_cast<long long>(c.b) * p.stride + j] = nan;
-        ++blk;
       } while (c.next_block(p));
     }
     tc::cluster_sync();
     tc::fence_after_sync();
   }
   if (warp == MMA_WARP) tc::tmem_dealloc_pair<TMEM_COLS>(tmem);
-}
-
-// CTA c adds up the parts of the block that cluster c is the first of several
-// to hold, in cluster order; a thread per key.
-__global__ void __launch_bounds__(KEYS) weigh_join_kernel(const WeighParams p) {
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int c = blockIdx.x, key = threadIdx.x;
-  const WeighCut cut = p.cut[c];
-  if (!cut.goes_on || (cut.continues && !cut.last_slot)) return;
-  const int b = cut.last_request, j = cut.last_block * KEYS + key;
-  float sum = p.part[(2 * c + cut.last_slot) * KEYS + key];
-  for (int i = c + 1; i < p.clusters; ++i) {
-    const WeighCut next = p.cut[i];
-    if (!next.continues || next.first_request != b || next.first_block != cut.last_block) break;
-    sum += p.part[2 * i * KEYS + key];
-  }
-  if (j < p.kv_lens[b]) p.weights[static_cast<long long>(b) * p.stride + j] += sum;
 }
 
 }  // namespace
@@ -548,9 +592,9 @@ cudaError_t make_weigh_maps(WeighMaps* maps, const void* kv, long long num_slots
                                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
-  // (tile::gather4: the box is one row high)
+  // (slots are gathered without a map)
   if (rows_of(&maps->kv, kv, num_slots, page_size == 1 ? 1 : PAGE) != CUDA_SUCCESS ||
-      rows_of(&maps->q, q, q_rows, Q_BOX) != CUDA_SUCCESS)
+      rows_of(&maps->q, q, q_rows, Q_BOX) != CUDA_SUCCESS || rows_of(&maps->q_full, q, q_rows, Q_FULL) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   return cudaSuccess;
 }
@@ -562,8 +606,7 @@ cudaError_t weigh_prepare() {
 }
 
 cudaError_t launch_weigh_kv(const WeighParams& p, const WeighMaps& maps, cudaStream_t stream) {
-  const cudaError_t e = launch_overlapping(weigh_kernel, dim3(2 * p.clusters), NTHREADS, SMEM_TOTAL, stream, 1, p, maps.kv, maps.q);
-  return e != cudaSuccess ? e : launch_overlapping(weigh_join_kernel, dim3(p.clusters), KEYS, 0, stream, 1, p);
+  return launch_overlapping(weigh_kernel, dim3(2 * p.clusters), NTHREADS, SMEM_TOTAL, stream, 1, p, maps.kv, maps.q, maps.q_full);
 }
 
 }  // namespace mlav

@@ -16,16 +16,16 @@
 namespace mlav {
 
 struct WeighSteps {
-  long long H, A, tiles, blocks;
+  long long H, A, k0, tiles, blocks;   // first(k0) is 0, first(k0 + 1) is not
 
-  MLAV_HD WeighSteps() : H(1), A(0), tiles(0), blocks(0) {}
+  MLAV_HD WeighSteps() : H(1), A(0), k0(0), tiles(0), blocks(0) {}
   MLAV_HD WeighSteps(int n, int c, int heads)
-      : H(heads), A(((static_cast<long long>(n) - c) * heads + 255) / 256), tiles((static_cast<long long>(c) * heads + 255) / 256),
-        blocks(c > 0 ? (static_cast<long long>(n) + 255) / 256 : 0) {}
+      : H(heads), A(((static_cast<long long>(n) - c) * heads + 255) / 256), k0(A / heads),
+        tiles((static_cast<long long>(c) * heads + 255) / 256), blocks(c > 0 ? (static_cast<long long>(n) + 255) / 256 : 0) {}
   MLAV_HD long long first(long long kb) const { return kb * H > A ? kb * H - A : 0; }
   // Steps of the blocks before kb.
   MLAV_HD long long before(long long kb) const {
-    const long long k0 = A / H, m = kb - 1;   // first(k0) is 0, first(k0 + 1) is not
+    const long long m = kb - 1;
     const long long skipped = m > k0 ? H * (m * (m + 1) / 2 - k0 * (k0 + 1) / 2) - A * (m - k0) : 0;
     return kb * tiles - skipped;
   }

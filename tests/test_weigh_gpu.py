@@ -119,6 +119,9 @@ def test_a_long_context(page):
 def test_blocks_that_many_clusters_share():
     check(make([400], [600], 64, 64, seed=4))
     check(make([1, 500], [10, 500], 64, 1, seed=5))
+    for page in (1, 64):   # shares of a part, a whole block and a part
+        check(make([8], [33000], 64, page, seed=20))
+        check(make([12, 5], [20000, 13000], 64, page, seed=21))
 
 
 def test_many_requests():
