@@ -356,9 +356,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         phase_of(f, s.steps, is_s, i);
         const int hb0 = 2 * (s.sa + i);
         int count;
-        if (CAUSAL && cw == 0 && f == 2 * s.steps - 1) {
+        if (CAUSAL && cw == 0 && f == max(2 * s.steps - 2, 1)) {
           // The next tile's queries, as soon as the last S^T of this one is
-          // done: its last O^T units, next in order, would wait for that too.
+          // done: the units that come next wait for slots that it reads, too.
           ahead.t = s.t;
           if (next_segment<CAUSAL>(p, share, from, to, s.tile + 1, ahead)) {
             wait_own(mbar(MB_QE), static_cast<uint32_t>(k & 1), s_abort, p.err);
@@ -768,6 +768,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         // The step's row sums over this warp's 32 keys, off the way to O^T.
         lrun = lrun * alpha + reduce_rows<true>(y, lane);
       }
+      // ---- the segment's end: row sums over the group's warps, then the peer's
+      const int eb = (g & 1) * ROWS;   // the halves of s_red and s_m that the last step did not use
+      s_red[(eb + row) * 4 + quad] = lrun;
+      group_sync();
+      float* s_l = s_m + eb;
+      const size_t part0 = static_cast<size_t>(part_slot(cluster, s.first)) * ROWS;
+      float ls = 0.f;
+      if (quad == 0) {
+        const float4 q4 = *reinterpret_cast<const float4*>(s_red + (eb + row) * 4);
+        ls = (q4.x + q4.y) + (q4.z + q4.w);
+        if (*s_abort == 0) {
+          tc::st_async_b32(tc::peer_addr(sbase + OFF_XSUM + row * 4, peer), __float_as_uint(ls), peer_mbar(MB_XS));
+          if (tid == 0) tc::mbar_arrive_expect(mbar(MB_XS), ROWS * 4);
+        }
+      }
       if (CAUSAL) {
         // The next tile's queries, while the last O^T is computed: its first
         // S^T follows without a pause.
@@ -775,19 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         ahead.t = s.t;
         if (next_segment<CAUSAL>(p, share, from, to, s.tile + 1, ahead)) take_queries(k + 1, ahead.t.nrows);
       }
-      // ---- the segment's end: row sums over the group's warps, then the peer's
-      const int eb = (g & 1) * ROWS;   // the halves of s_red and s_m that the last step did not use
-      s_red[(eb + row) * 4 + quad] = lrun;
-      group_sync();
-      float* s_l = s_m + eb;
-      const size_t part0 = static_cast<size_t>(part_slot(cluster, s.first)) * ROWS;
       if (quad == 0) {
-        const float4 q4 = *reinterpret_cast<const float4*>(s_red + (eb + row) * 4);
-        const float ls = (q4.x + q4.y) + (q4.z + q4.w);
-        if (*s_abort == 0) {
-          tc::st_async_b32(tc::peer_addr(sbase + OFF_XSUM + row * 4, peer), __float_as_uint(ls), peer_mbar(MB_XS));
-          if (tid == 0) tc::mbar_arrive_expect(mbar(MB_XS), ROWS * 4);
-        }
         wait_peer(mbar(MB_XS), static_cast<uint32_t>(k & 1), s_abort, p.err);
         // Both CTAs add the two halves in the same order.
         const float lo = rank == 0 ? ls : s_xsum[row];
@@ -805,32 +808,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         }
       }
       group_sync();
-      // ---- O^T out of TMEM; thread = value dim, each warp store 32
-      // consecutive dims of a row.
+      // ---- O^T out of TMEM.
       wait_own(mbar(MB_OT), static_cast<uint32_t>((g - 1) & 1), s_abort, p.err);
       tc::fence_after_sync();
       const int rows = s.t.nrows - c0;
       const size_t out0 = (s.whole ? static_cast<size_t>(s.t.q_row0) : part0) + c0;
+      if (s.whole && p.out_bf16) {
+        // As the scores: lane t has dims t / 4 + 8 k and, of each, rows 8 i + 2
+        // (t % 4) + e.  An 8 x 8 block of pairs of rows is transposed to pairs
+        // of dims of row 8 i + t / 4, and four lanes exchange theirs so that
+        // each stores eight dims: 8 stores of 16 bytes a warp (64 of 2 bytes,
+        // with a dim per lane, took 2.6 us of a tile's end).
 #pragma unroll 1
-      for (int t = 0; t < 2; ++t) {
-        float v[32];
-        tc::tmem_ld32f(tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * t + c0, v);
-        tc::tmem_wait_ld();
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t o_addr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * t + c0;
+          float v[32];
+          tc::tmem_ld16x32f(o_addr, v);
+          tc::tmem_ld16x32f(o_addr + (16u << 16), v + 16);
+          tc::tmem_wait_ld();
+          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + (out0 + key) * D_V + t * 256 + static_cast<int>(rank) * 128 +
+                             quad * 32 + 8 * (lane & 3);
+          const bool odd = lane & 1, upper = lane & 2;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float4 i4 = *reinterpret_cast<const float4*>(s_l + c0 + 4 * q);
-          v[4 * q] = i4.x == 0.f ? 0.f : v[4 * q] * i4.x;
-          v[4 * q + 1] = i4.y == 0.f ? 0.f : v[4 * q + 1] * i4.y;
-          v[4 * q + 2] = i4.z == 0.f ? 0.f : v[4 * q + 2] * i4.z;
-          v[4 * q + 3] = i4.w == 0.f ? 0.f : v[4 * q + 3] * i4.w;
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = *reinterpret_cast<const float2*>(s_l + c0 + 8 * i + pair);
+            uint32_t w[4];
+#pragma unroll
+            for (int k8 = 0; k8 < 4; ++k8) {
+              const int n = 16 * (k8 >> 1) + 4 * i + 2 * (k8 & 1);
+              const __nv_bfloat162 both = __floats2bfloat162_rn(f.x == 0.f ? 0.f : v[n] * f.x, f.y == 0.f ? 0.f : v[n + 1] * f.y);
+              w[k8] = tc::transpose8x8(*reinterpret_cast<const uint32_t*>(&both));
+            }
+            const uint32_t r01 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1);
+            const uint32_t r23 = __shfl_xor_sync(0xffffffffu, odd ? w[2] : w[3], 1);
+            const uint32_t u0 = odd ? r01 : w[0], u1 = odd ? w[1] : r01, v0 = odd ? r23 : w[2], v1 = odd ? w[3] : r23;
+            const uint32_t g0 = __shfl_xor_sync(0xffffffffu, upper ? u0 : v0, 2);
+            const uint32_t g1 = __shfl_xor_sync(0xffffffffu, upper ? u1 : v1, 2);
+            if (8 * i + key < rows)
+              *reinterpret_cast<uint4*>(o + 8 * i * D_V) = upper ? make_uint4(g0, g1, v0, v1) : make_uint4(u0, u1, g0, g1);
+          }
         }
-        const size_t at = out0 * D_V + t * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
-        if (s.whole && p.out_bf16) {
-          __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+      } else {
+        // Thread = value dim, each warp store 32 consecutive dims of a row.
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+          float v[32];
+          tc::tmem_ld32f(tmem + (static_cast<uint32_t>(quad * 32) << 16) + 128u * t + c0, v);
+          tc::tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c < rows) o[c * D_V] = __float2bfloat16_rn(v[c]);
-        } else {
+          for (int q = 0; q < 8; ++q) {
+            const float4 i4 = *reinterpret_cast<const float4*>(s_l + c0 + 4 * q);
+            v[4 * q] = i4.x == 0.f ? 0.f : v[4 * q] * i4.x;
+            v[4 * q + 1] = i4.y == 0.f ? 0.f : v[4 * q + 1] * i4.y;
+            v[4 * q + 2] = i4.z == 0.f ? 0.f : v[4 * q + 2] * i4.z;
+            v[4 * q + 3] = i4.w == 0.f ? 0.f : v[4 * q + 3] * i4.w;
+          }
+          const size_t at = out0 * D_V + t * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
           float* o = (s.whole ? reinterpret_cast<float*>(p.out) : p.part_o) + at;
 #pragma unroll
           for (int c = 0; c < 32; ++c)

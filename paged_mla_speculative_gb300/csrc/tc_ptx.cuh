@@ -156,6 +156,12 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t* r) {
                "r"(r[2]), "r"(r[3])
                : "memory");
 }
+// An 8x8 matrix of 16-bit values, a row's pairs in four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(w));
+  return r;
+}
 // One TMEM column for the warp's 32 lanes.
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
