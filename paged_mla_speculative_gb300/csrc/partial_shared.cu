@@ -240,6 +240,19 @@ __device__ __forceinline__ void widen_queries(uint8_t* q, int rows, int tid, int
     uint4 v[FLIGHT];
 #pragma unroll
     for (int u = 0; u < FLIGHT; ++u) v[u] = reinterpret_cast<const uint4*>(q)[tid + (u0 + u) * THREADS];
+    // The largest magnitude tells whether any value left fp16's range (one
+    // operation a pair; looked at pair by pair it took as long as the rest).
+    __half2 most = __float2half2_rn(0.f);
+    auto widen = [&](uint32_t w) {
+      const __half2 h = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+      most = __hmax2_nan(most, __habs2(h));
+      return *reinterpret_cast<const uint32_t*>(&h);
+    };
+#pragma unroll
+    for (int u = 0; u < FLIGHT; ++u)
+      reinterpret_cast<uint4*>(q)[tid + (u0 + u) * THREADS] = make_uint4(widen(v[u].x), widen(v[u].y), widen(v[u].z), widen(v[u].w));
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(&most);
+    if ((m & 0x7c00u) != 0x7c00u && (m & 0x7c000000u) != 0x7c000000u) continue;
 #pragma unroll
     for (int u = 0; u < FLIGHT; ++u) {
       const int e = tid + (u0 + u) * THREADS;
@@ -247,9 +260,9 @@ __device__ __forceinline__ void widen_queries(uint8_t* q, int rows, int tid, int
       uint4 w = widen_bf16x8(v[u], bad);
       if (bad) {   // NaN, so that no score of the row is a number (an infinity might pass for a masked key)
         w.x = nan_for_inf(w.x), w.y = nan_for_inf(w.y), w.z = nan_for_inf(w.z), w.w = nan_for_inf(w.w);
+        reinterpret_cast<uint4*>(q)[e] = w;
         out_of_range |= (e >> 3) % HROWS < rows;   // (rows behind the tile's are not its own)
       }
-      reinterpret_cast<uint4*>(q)[e] = w;
     }
   }
   report_range(out_of_range, err);
@@ -566,6 +579,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
         return meta0[key + (shared ? 0 : meta_gap)];
       };
       int meta = load_meta(0);
+      int next_rows = 0;   // CAUSAL: rows of the next tile, if there is one
+      if (CAUSAL) {
+        Segment ahead;
+        ahead.t = s.t;
+        if (next_segment<CAUSAL>(p, share, from, to, s.tile + 1, ahead)) next_rows = ahead.t.nrows;
+      }
       group_sync();   // the previous segment's rows are read
       if (quad == 0) {
         int2 of = make_int2(-1, 0);
@@ -783,13 +802,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           if (tid == 0) tc::mbar_arrive_expect(mbar(MB_XS), ROWS * 4);
         }
       }
-      if (CAUSAL) {
-        // The next tile's queries, while the last O^T is computed: its first
-        // S^T follows without a pause.
-        Segment ahead;
-        ahead.t = s.t;
-        if (next_segment<CAUSAL>(p, share, from, to, s.tile + 1, ahead)) take_queries(k + 1, ahead.t.nrows);
-      }
+      // CAUSAL: the next tile's queries, while the last O^T is computed: its
+      // first S^T follows without a pause.
+      if (CAUSAL && next_rows > 0) take_queries(k + 1, next_rows);
       if (quad == 0) {
         wait_peer(mbar(MB_XS), static_cast<uint32_t>(k & 1), s_abort, p.err);
         // Both CTAs add the two halves in the same order.
@@ -832,11 +847,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 f = *reinterpret_cast<const float2*>(s_l + c0 + 8 * i + pair);
+            if (__any_sync(0xffffffffu, f.x == 0.f || f.y == 0.f)) {   // rows without keys: 0, whatever O^T holds
+#pragma unroll
+              for (int k8 = 0; k8 < 4; ++k8) {
+                const int n = 16 * (k8 >> 1) + 4 * i + 2 * (k8 & 1);
+                if (f.x == 0.f) v[n] = 0.f;
+                if (f.y == 0.f) v[n + 1] = 0.f;
+              }
+            }
             uint32_t w[4];
 #pragma unroll
             for (int k8 = 0; k8 < 4; ++k8) {
               const int n = 16 * (k8 >> 1) + 4 * i + 2 * (k8 & 1);
-              const __nv_bfloat162 both = __floats2bfloat162_rn(f.x == 0.f ? 0.f : v[n] * f.x, f.y == 0.f ? 0.f : v[n + 1] * f.y);
+              const __nv_bfloat162 both = __floats2bfloat162_rn(v[n] * f.x, v[n + 1] * f.y);
               w[k8] = tc::transpose8x8(*reinterpret_cast<const uint32_t*>(&both));
             }
             const uint32_t r01 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[1], 1);
