@@ -25,6 +25,11 @@ constexpr int SMALL = 512;     // requests laid out in shared memory
 // What totals[2] and the scan say of a call.
 constexpr int CHUNK_BAD_REQUEST = 1, CHUNK_BAD_TOKENS = 2;
 
+__device__ __forceinline__ ChunkSteps chunk_steps(int n, int c, int H) {
+  const bool cold = static_cast<long long>(c) * H <= CHUNK_COLD_TILES * SH_ROWS;
+  return ChunkSteps(n, c, H, cold ? CHUNK_COLD_STEP : CHUNK_STEP, CHUNK_SEGMENT);
+}
+
 struct ChunkLayout {
   int base[SMALL + 1], own[SMALL], tile0[SMALL + 1];
   long long cost[SMALL + 1];
@@ -63,11 +68,11 @@ __device__ __forceinline__ int scan_chunks(const SharedParams& p, int* base, int
       const bool ptr_ok = ip0 >= 0 && ip1 >= ip0 && ip1 <= ipn && static_cast<long long>(ip1) - ip0 == need;
       if (tokens_ok && !(len_ok && ptr_ok)) errs |= len_ok ? ERR_INDPTR : ERR_LEN;
       if (tokens_ok && len_ok && ptr_ok && c > 0) {
-        const ChunkSteps s(n, c, p.H, SH_SEGMENT_COST);
+        const ChunkSteps s = chunk_steps(n, c, p.H);
         mine = n;
         rows = static_cast<int>(s.tiles);
         sum = s.total();
-        largest = max(largest, static_cast<int>(s.last) + SH_SEGMENT_COST);
+        largest = max(largest, static_cast<int>(s.last) * s.unit + CHUNK_SEGMENT);
       }
       own[b] = mine;
     }
@@ -117,13 +122,14 @@ __device__ void plan_chunks(const SharedParams& p, ChunkLayout& s, bool small, v
     p.totals[2] = bad;
   }
   // Even division over as many clusters as get two steps or more each.
-  // Starts lie at least SH_SEGMENT_COST + 2 apart, so no two start in one
-  // tile's leading cost; those of clusters without partials move up to a
+  // Starts lie at least LEAST apart, so no two start in one tile's leading cost
+  // or in one step; those of clusters without partials move up to a
   // tile's border (and some clusters may be left without work).  Where every
   // tile can have a cluster of its own and the longest takes no more than an
   // even share, cut tiles starting twice, and the merge, tiles stay whole.
-  const int used = static_cast<int>(max(1LL, min(static_cast<long long>(p.clusters), total / (SH_SEGMENT_COST + 2))));
-  const bool whole = tiles <= p.clusters && s_most <= total / p.clusters + SH_SEGMENT_COST + SH_JOIN_COST;
+  constexpr int LEAST = CHUNK_SEGMENT + 2 * CHUNK_COLD_STEP;
+  const int used = static_cast<int>(max(1LL, min(static_cast<long long>(p.clusters), total / LEAST)));
+  const bool whole = tiles <= p.clusters && s_most <= total / p.clusters + CHUNK_SEGMENT + SH_JOIN_COST * CHUNK_STEP;
   for (int c = tid; c < p.clusters; c += PACK_THREADS) {
     SharedShare sh{};
     int first = 0;   // request of the first tile
@@ -137,10 +143,10 @@ __device__ void plan_chunks(const SharedParams& p, ChunkLayout& s, bool small, v
         const long long x = total * k / used;
         request = last_not_above(cost, B, x);
         const int q0 = p.q_indptr[request];
-        const ChunkSteps st(p.kv_lens[request], p.q_indptr[request + 1] - q0, p.H, SH_SEGMENT_COST);
+        const ChunkSteps st = chunk_steps(p.kv_lens[request], p.q_indptr[request + 1] - q0, p.H);
         const long long t = st.tile_at(x - cost[request]);
         at.tile = tile0[request] + static_cast<int>(t);
-        at.step = static_cast<int>(max(0LL, x - cost[request] - st.before(t) - SH_SEGMENT_COST));
+        at.step = static_cast<int>(max(0LL, x - cost[request] - st.before(t) - CHUNK_SEGMENT) / st.unit);
         if (at.step > 0 && k >= p.cut_clusters) {
           at = SharedPos{at.tile + 1, 0};
           request = at.tile < tiles ? last_not_above(tile0, B, at.tile) : B;

@@ -25,11 +25,12 @@ namespace mlav {
 
 struct ChunkSteps {
   long long m, u, tiles, last;   // last: steps of the last tile
-  int per_tile;                  // added to every tile's steps
+  int unit, per_tile;            // what a step costs, and a tile beside its steps
 
-  MLAV_HD ChunkSteps(int n, int c, int H, int added)
+  MLAV_HD ChunkSteps(int n, int c, int H, int step_cost, int tile_cost)
       : m(2LL * H), u((127 + (static_cast<long long>(n) - c + 256) * H) / 128),
-        tiles((static_cast<long long>(c) * H + 127) / 128), last((static_cast<long long>(n) + 255) / 256), per_tile(added) {}
+        tiles((static_cast<long long>(c) * H + 127) / 128), last((static_cast<long long>(n) + 255) / 256), unit(step_cost),
+        per_tile(tile_cost) {}
   MLAV_HD long long steps(long long t) const { return t + 1 < tiles ? (t + u) / m : last; }
   // Sum of y / m over 0 <= y < x.
   MLAV_HD long long quotients(long long x) const {
@@ -40,7 +41,7 @@ struct ChunkSteps {
   MLAV_HD long long before(long long t) const {
     if (t <= 0) return 0;
     const long long whole = t < tiles ? t : tiles - 1;
-    return quotients(whole + u) - quotients(u) + (t < tiles ? 0 : last) + per_tile * t;
+    return unit * (quotients(whole + u) - quotients(u) + (t < tiles ? 0 : last)) + per_tile * t;
   }
   MLAV_HD long long total() const { return before(tiles); }
   // The tile in which cost x lies, 0 <= x < total().

@@ -42,7 +42,7 @@ constexpr int MAX_CTAS = 8;                // per request
 constexpr int ROWS_PER_CTA = 12288;        // from which a request gets another CTA, where SMs are left: a cluster barrier is ~1 us
 constexpr int MAX_CACHED = 24576;          // keys that a CTA holds in shared memory
 constexpr int GROUP = 32;                  // strips of THREADS rows placed by one scan
-constexpr int FLIGHT = 4;                  // strips whose loads and atomics are under way together
+constexpr int FLIGHT = 6;                  // strips whose loads and atomics are under way together
 
 // Larger weights have larger keys; -0 is 0, NaN is below every number.
 __device__ __forceinline__ unsigned ordered(float w) {
@@ -50,6 +50,8 @@ __device__ __forceinline__ unsigned ordered(float w) {
   const unsigned u = __float_as_uint(w == 0.f ? 0.f : w);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+// The weight of a key (a NaN for NaN, 0 for -0).
+__device__ __forceinline__ float weight_of(unsigned key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
 
 // A request's rows and entries; nothing, with the error bit that says why, for
 // one that is out of order.
@@ -108,8 +110,9 @@ __device__ __forceinline__ long long low(long long x) { return x & 0xffffffffll;
 // grid: `ctas` CTAs (a cluster) per request.  (The sums of all requests'
 // entries stay below 2^31: so does max_batch * max_kv_len.)
 __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArgs a, int cached) {
-  extern __shared__ float s_weights[];
-  __shared__ int s_hist[BINS], s_bins[WARPS];
+  extern __shared__ unsigned s_keys[];
+  __shared__ __align__(8) int s_hist[BINS];
+  __shared__ int s_bins[WARPS];
   __shared__ long long s_warp[WARPS], s_place[GROUP * WARPS];
   __shared__ long long s_mine, s_fit, s_count;
   __shared__ unsigned long long s_last[2];
@@ -130,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   // A CTA that has the request alone loads the weights before it knows how many.
   const bool alone = ctas == 1 && a.max_kv_len <= cached;
   if (alone)
-    for (int i = tid; i < a.max_kv_len; i += THREADS) s_weights[i] = row[i];
+    for (int i = tid; i < a.max_kv_len; i += THREADS) s_keys[i] = ordered(row[i]);
   const bool height_ok = height >= 0 && height <= a.num_pages;
   const long long left = height_ok ? height : -1;   // a stack that is out of order serves nobody
   if (tid < 2) s_last[tid] = 0;
@@ -155,14 +158,6 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
     before += all;
   }
   __syncthreads();
-  if (tid == 0) {   // the last CTA that has read the height lowers it
-    __threadfence();
-    if (atomicAdd(a.ticket, 1u) == gridDim.x - 1) {
-      *a.ticket = 0;
-      if (height_ok) *a.free_count = static_cast<int32_t>(left - static_cast<long long>(s_last[1]));
-      else atomicOr(a.err, ERR_CAPACITY);
-    }
-  }
   const Item it = s_item;
   const bool fits = high(s_fit) <= a.capacity && low(s_fit) <= left;
   const bool served = fits && !it.bad;
@@ -177,7 +172,19 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   float* new_row = a.new_weights + b * a.new_stride;
   // Behind the kept rows: 0.
   for (long long j = (served ? it.m : 0) + me; j < a.new_width; j += all_threads) new_row[j] = 0.f;
-  if (!served) return;   // the whole cluster
+  // The last CTA that has read the height lowers it.
+  auto lower = [&]() {
+    if (tid != 0) return;
+    __threadfence();
+    if (atomicAdd(a.ticket, 1u) != gridDim.x - 1) return;
+    *a.ticket = 0;
+    if (height_ok) *a.free_count = static_cast<int32_t>(left - static_cast<long long>(s_last[1]));
+    else atomicOr(a.err, ERR_CAPACITY);
+  };
+  if (!served) {   // the whole cluster
+    lower();
+    return;
+  }
 
   const int n = it.n;
   const bool over = n > a.budget;
@@ -199,24 +206,23 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   int k = a.budget - a.sink - a.recent;        // to be chosen
   unsigned cut = 0xffffffffu;                  // the key of the last one chosen
   int equal = 0;                               // of the rows with that key, how many
-  auto weight_at = [&](int i) { return in_smem ? s_weights[i] : row[j0 + i]; };
+  auto key_at = [&](int i) { return in_smem ? s_keys[i] : ordered(row[j0 + i]); };
   if (over && k > 0) {
     if (!alone && in_smem)   // (a thread uses the rows that it loaded)
-      for (int i = tid; i < count; i += THREADS) s_weights[i] = row[j0 + i];
+      for (int i = tid; i < count; i += THREADS) s_keys[i] = ordered(row[j0 + i]);
     unsigned prefix = 0;
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       for (int i = tid; i < BINS; i += THREADS) s_hist[i] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int s = 0; s < strips; ++s) {
         const int i = s * THREADS + tid, j = j0 + i;
         bool mine = i < count && j >= lo && j < hi;
-        const unsigned key = mine ? ordered(weight_at(i)) : 0;
+        const unsigned key = mine ? key_at(i) : 0;
         mine = mine && (pass == 0 || (key >> (shift + bits)) == prefix);
         const int bin = mine ? static_cast<int>((key >> shift) & ((1u << bits) - 1)) : -1;
-        int same;
-        __match_all_sync(0xffffffffu, bin, &same);
-        if (same) {   // (many rows of one weight: one addition for the warp)
+        if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {   // (many rows of one weight: one addition for the warp)
           if (bin >= 0 && lane == 0) atomicAdd(s_hist + bin, 32);
         } else if (bin >= 0) {
           atomicAdd(s_hist + bin, 1);
@@ -226,10 +232,16 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
       // The bin, from the top, in which the k-th row lies: two bins per thread.
       const int top = BINS - 1 - 2 * tid;
       int h0 = 0, h1 = 0;
-      for (int r = 0; r < ctas; ++r) {
-        const int* h = ctas > 1 ? cluster.map_shared_rank(s_hist, r) : s_hist;
-        h0 += h[top];
-        h1 += h[top - 1];
+      if (ctas == 1) {
+        const int2 h = *reinterpret_cast<const int2*>(s_hist + top - 1);
+        h0 = h.y, h1 = h.x;
+      } else {
+#pragma unroll
+        for (int r = 0; r < MAX_CTAS; ++r) {
+          if (r >= ctas) continue;
+          const int2 h = *reinterpret_cast<const int2*>(cluster.map_shared_rank(s_hist, r) + top - 1);
+          h0 += h.y, h1 += h.x;
+        }
       }
       // (The warp in which it lies, by every warp; the lane, by that one.)
       const int warp_sum = __reduce_add_sync(0xffffffffu, h0 + h1);
@@ -265,13 +277,14 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
     cut = prefix;
     equal = k;
   }
+  const bool have_keys = in_smem && (alone || (over && a.budget > a.sink + a.recent));
   // 1: kept, 2: kept while there are fewer than `equal`, 0: not (nor is there a row).
   auto kind = [&](int i) {
     const int j = j0 + i;
     if (i >= count) return 0;
     if (!over || j < lo || j >= hi) return 1;
     if (equal == 0) return 0;
-    const unsigned key = ordered(weight_at(i));
+    const unsigned key = key_at(i);
     return key == cut ? 2 : key > cut ? 1 : 0;
   };
   // Rows above the cut (or protected) and rows equal to it that lie before the
@@ -319,7 +332,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
         to[u] = s >= g1 || i >= count                       ? -2
                 : x == 1 || (x == 2 && e < equal) ? static_cast<int>(high(place)) + __popc(above & lower) + min(e, equal)
                                                   : -1;
-        w[u] = to[u] >= 0 ? (over && a.budget > a.sink + a.recent ? weight_at(i) : row[j0 + i]) : 0.f;
+        w[u] = to[u] >= 0 ? (have_keys ? weight_of(s_keys[i]) : row[j0 + i]) : 0.f;
         slot[u] = a.page == 1 && to[u] != -2 ? held[j0 + i] : 0;
       }
       if (a.page > 1) {
@@ -355,6 +368,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   for (long long e = l0; e < it.entries; e += all_threads)
     errs |= release_page(e == l0 ? first_left : held[e], a.num_pages, a.page_refs, a.page_bits);
   if (errs) atomicOr(a.err, errs);
+  lower();
   if (ctas > 1) cluster.sync();   // no CTA leaves while another reads its count
 }
 

@@ -25,6 +25,9 @@ constexpr int SH_TAIL = 128;       // zeroed keys behind the packed space: a hal
 // A tile's cost in steps is its steps plus this: what a segment costs beside
 // them (queries in, pipeline fill, last O^T, readout: ~8 us against 3.7 us a step).
 constexpr int SH_SEGMENT_COST = 2;
+// The same of a chunk's tile, in quarters of a step; and a step's cost, that of
+// a request whose keys few tiles read being higher: they come from memory.
+constexpr int CHUNK_STEP = 4, CHUNK_COLD_STEP = 5, CHUNK_COLD_TILES = 2, CHUNK_SEGMENT = 4;
 // What the merge of cut tiles costs, in steps (~7 us).
 constexpr int SH_JOIN_COST = 2;
 

@@ -14,7 +14,7 @@ HARNESS = r"""
 int main() {
   long long n, c, H;
   while (std::scanf("%lld %lld %lld", &n, &c, &H) == 3) {
-    mlav::ChunkSteps s(n, c, H, 2);
+    mlav::ChunkSteps s(n, c, H, 3, 2);
     long long sum = 0;
     const long long tiles = (c * H + 127) / 128;
     bool ok = s.tiles == tiles && s.before(0) == 0;
@@ -22,8 +22,8 @@ int main() {
       const long long end = 128 * t + 128 < c * H ? 128 * t + 128 : c * H;   // of its rows
       const long long keys = n - c + (end - 1) / H + 1;
       const long long steps = (keys + 255) / 256;
-      ok = ok && s.steps(t) == steps && s.tile_at(sum) == t && s.tile_at(sum + steps + 1) == t;
-      sum += steps + 2;
+      ok = ok && s.steps(t) == steps && s.tile_at(sum) == t && s.tile_at(sum + 3 * steps + 1) == t;
+      sum += 3 * steps + 2;
       ok = ok && s.before(t + 1) == sum;
     }
     ok = ok && s.total() == sum;
