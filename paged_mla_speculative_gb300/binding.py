@@ -548,6 +548,11 @@ def mla_verify_attn_chunk(plan: Plan, q, kv_cache, kv_indices, kv_indptr, kv_len
 
 def _expect_weights(plan: Plan, weights, name: str, batch: int):
     """Rows of fp32 weights; returns their stride."""
+    if (type(weights) is torch.Tensor and weights.dtype is torch.float32 and weights.dim() == 2 and weights.is_contiguous()
+            and weights.device == plan.torch_device):
+        rows, width = weights.shape
+        if rows == batch and width >= plan.max_kv_len:
+            return width
     if not isinstance(weights, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if weights.dtype != torch.float32:

@@ -130,36 +130,38 @@ __device__ void plan_chunks(const SharedParams& p, ChunkLayout& s, bool small, v
   constexpr int LEAST = CHUNK_SEGMENT + 2 * CHUNK_COLD_STEP;
   const int used = static_cast<int>(max(1LL, min(static_cast<long long>(p.clusters), total / LEAST)));
   const bool whole = tiles <= p.clusters && s_most <= total / p.clusters + CHUNK_SEGMENT + SH_JOIN_COST * CHUNK_STEP;
+  // Starts, and the requests of their tiles.
+  __shared__ SharedPos s_start[SH_MAX_CLUSTERS + 1];
+  __shared__ int s_request[SH_MAX_CLUSTERS + 1];
+  for (int c = tid; c <= p.clusters; c += PACK_THREADS) {
+    SharedPos at{tiles, 0};
+    int request = B;
+    if (whole) {
+      at.tile = min(c, tiles);
+      if (at.tile < tiles) request = last_not_above(tile0, B, at.tile);
+    } else if (c < used && total > 0) {
+      const long long x = total * c / used;
+      request = last_not_above(cost, B, x);
+      const int q0 = p.q_indptr[request];
+      const ChunkSteps st = chunk_steps(p.kv_lens[request], p.q_indptr[request + 1] - q0, p.H);
+      const long long t = st.tile_at(x - cost[request]);
+      at.tile = tile0[request] + static_cast<int>(t);
+      at.step = static_cast<int>(max(0LL, x - cost[request] - st.before(t) - CHUNK_SEGMENT) / st.unit);
+      if (at.step > 0 && c >= p.cut_clusters) {
+        at = SharedPos{at.tile + 1, 0};
+        request = at.tile < tiles ? last_not_above(tile0, B, at.tile) : B;
+      }
+    }
+    s_start[c] = at;
+    s_request[c] = request;
+  }
+  __syncthreads();
   for (int c = tid; c < p.clusters; c += PACK_THREADS) {
     SharedShare sh{};
-    int first = 0;   // request of the first tile
-    auto start = [&](int k, int& request) {
-      SharedPos at{tiles, 0};
-      request = B;
-      if (whole) {
-        at.tile = min(k, tiles);
-        if (at.tile < tiles) request = last_not_above(tile0, B, at.tile);
-      } else if (k < used) {
-        const long long x = total * k / used;
-        request = last_not_above(cost, B, x);
-        const int q0 = p.q_indptr[request];
-        const ChunkSteps st = chunk_steps(p.kv_lens[request], p.q_indptr[request + 1] - q0, p.H);
-        const long long t = st.tile_at(x - cost[request]);
-        at.tile = tile0[request] + static_cast<int>(t);
-        at.step = static_cast<int>(max(0LL, x - cost[request] - st.before(t) - CHUNK_SEGMENT) / st.unit);
-        if (at.step > 0 && k >= p.cut_clusters) {
-          at = SharedPos{at.tile + 1, 0};
-          request = at.tile < tiles ? last_not_above(tile0, B, at.tile) : B;
-        }
-      }
-      return at;
-    };
-    int after;
-    if (total > 0) {
-      sh.from = start(c, first);
-      sh.to = start(c + 1, after);
-      if (sh.from.tile < tiles) sh.first = chunk_tile(p, first, sh.from.tile - tile0[first], base[first]);
-    }
+    sh.from = s_start[c];
+    sh.to = s_start[c + 1];
+    const int request = s_request[c];
+    if (sh.from.tile < tiles) sh.first = chunk_tile(p, request, sh.from.tile - tile0[request], base[request]);
     p.share[c] = sh;
   }
 }

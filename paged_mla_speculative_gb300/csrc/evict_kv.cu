@@ -175,9 +175,11 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   // The last CTA that has read the height lowers it.
   auto lower = [&]() {
     if (tid != 0) return;
-    __threadfence();
-    if (atomicAdd(a.ticket, 1u) != gridDim.x - 1) return;
-    *a.ticket = 0;
+    if (gridDim.x > 1) {
+      __threadfence();
+      if (atomicAdd(a.ticket, 1u) != gridDim.x - 1) return;
+      *a.ticket = 0;
+    }
     if (height_ok) *a.free_count = static_cast<int32_t>(left - static_cast<long long>(s_last[1]));
     else atomicOr(a.err, ERR_CAPACITY);
   };
@@ -287,6 +289,19 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
     const unsigned key = key_at(i);
     return key == cut ? 2 : key > cut ? 1 : 0;
   };
+  // (Each thread's first entries: their counts answer while rows are placed.)
+  auto put_entry = [&](long long e, int page) {   // the count that a fresh entry had
+    table[e] = page;
+    if (page < 0 || page >= a.num_pages) errs |= ERR_SLOT;
+    else if (e >= it.stay) return atomicExch(a.page_refs + page, 1);
+    return 0;
+  };
+  const int exchanged = e0 < it.total ? put_entry(e0, first_entry) : 0;
+  int left_had = 2;
+  if (l0 < it.entries) {
+    if (first_left < 0 || first_left >= a.num_pages) errs |= ERR_SLOT;
+    else left_had = atomicSub(a.page_refs + first_left, 1);
+  }
   // Rows above the cut (or protected) and rows equal to it that lie before the
   // CTA's, then before each strip's and warp's: the kept rows' new places.
   long long base = 0;
@@ -359,14 +374,12 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
       for (int u = 0; u < FLIGHT; ++u) errs |= mark_released(slot[u], had[u], a.page_refs, a.page_bits);
     }
   }
-  for (long long e = e0; e < it.total; e += all_threads) {
-    const int page = e == e0 ? first_entry : entry_at(e);
-    table[e] = page;
-    if (page < 0 || page >= a.num_pages) errs |= ERR_SLOT;
-    else if (e >= it.stay && atomicExch(a.page_refs + page, 1) != 0) errs |= ERR_REF;   // the stack held a page that is in use
-  }
-  for (long long e = l0; e < it.entries; e += all_threads)
-    errs |= release_page(e == l0 ? first_left : held[e], a.num_pages, a.page_refs, a.page_bits);
+  if (exchanged != 0) errs |= ERR_REF;   // the stack held a page that is in use
+  for (long long e = e0 + all_threads; e < it.total; e += all_threads)
+    if (put_entry(e, entry_at(e)) != 0) errs |= ERR_REF;
+  errs |= mark_released(first_left, left_had, a.page_refs, a.page_bits);
+  for (long long e = l0 + all_threads; e < it.entries; e += all_threads)
+    errs |= release_page(held[e], a.num_pages, a.page_refs, a.page_bits);
   if (errs) atomicOr(a.err, errs);
   lower();
   if (ctas > 1) cluster.sync();   // no CTA leaves while another reads its count
@@ -379,7 +392,7 @@ template <int T>
 __device__ __forceinline__ void push_marked_part(const EvictArgs& a, int part, int parts, long long count, long long* s_warp, int& s_done) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int words = a.num_pages / 32 + (a.num_pages % 32 != 0);
-  const int each = ((words + parts - 1) / parts + 3) / 4 * 4;
+  const int each = ((words + parts - 1) / parts + T - 1) / T * T;
   const int w0 = static_cast<int>(min(static_cast<long long>(part) * each, static_cast<long long>(words))), w1 = min(words, w0 + each);
   int sum = 0;
 #pragma unroll 8
@@ -484,13 +497,13 @@ __global__ void __launch_bounds__(COPY_THREADS) evict_copy_kernel(const EvictArg
   }
 }
 
-__global__ void __launch_bounds__(THREADS) evict_push_kernel(const EvictArgs a) {
-  __shared__ long long s_warp[WARPS];
+__global__ void __launch_bounds__(COPY_THREADS) evict_push_kernel(const EvictArgs a) {
+  __shared__ long long s_warp[COPY_THREADS / 32];
   __shared__ int s_done;
   asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
   const long long count = *a.free_count;
   if (count < 0 || count > a.num_pages) return;   // (reported, and nothing was given back)
-  push_marked_part<THREADS>(a, blockIdx.x, gridDim.x, count, s_warp, s_done);
+  push_marked_part<COPY_THREADS>(a, blockIdx.x, gridDim.x, count, s_warp, s_done);
 }
 
 }  // namespace
@@ -519,8 +532,9 @@ cudaError_t launch_evict_kv(const EvictArgs& a, int num_sms, cudaStream_t stream
     const unsigned z = static_cast<unsigned>((a.num_layers + each - 1) / each);
     return launch_overlapping(evict_copy_kernel, dim3(parts + 1, requests, z), COPY_THREADS, 0, stream, 1, a, each);
   }
-  const unsigned push = static_cast<unsigned>(std::clamp(a.num_pages / 32 / THREADS, 1, 64));
-  return launch_overlapping(evict_push_kernel, dim3(push), THREADS, 0, stream, 1, a);
+  // A word per thread, as long as the words before a CTA's are soon added up.
+  const unsigned push = static_cast<unsigned>(std::clamp(a.num_pages / 32 / COPY_THREADS, 1, 128));
+  return launch_overlapping(evict_push_kernel, dim3(push), COPY_THREADS, 0, stream, 1, a);
 }
 
 }  // namespace mlav

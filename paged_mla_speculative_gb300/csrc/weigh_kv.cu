@@ -152,6 +152,43 @@ __device__ __forceinline__ void plan_share(const WeighParams& p, int cluster, Cu
     own = 0;
     if (b < p.batch && load_request(p, b, r, errs)) own = r.s.total();
   };
+  // The cluster's share starts in request b, `sum` - own steps of the call
+  // before it: one thread's.
+  auto place = [&](int b, long long sum, long long total) {
+    const long long used = min(static_cast<long long>(p.clusters), total);
+    if (cluster >= used) return;
+    const long long from = total * cluster / used, to = total * (cluster + 1) / used;
+    if (own == 0 || sum - own > from || from >= sum) return;
+    Cursor c;
+    c.r = r;
+    c.left = to - from;
+    c.done = from;
+    c.total = total;
+    c.b = b;
+    const long long step = from - (sum - own);
+    c.kb = static_cast<int>(r.s.block_at(step));
+    c.t = c.t0 = static_cast<int>(r.s.first(c.kb) + step - r.s.before(c.kb));
+    *start = c;
+  };
+  if (p.batch <= 32) {   // a warp's work, and no barrier
+    if (warp != 0) return;
+    load(lane);
+    if (lane == 0) start->left = 0;
+    const bool undivided = lane < p.batch && (r.q0 < 0 || r.c < 0 || r.q0 > p.num_tokens - r.c);
+    if (__any_sync(0xffffffffu, undivided)) {
+      if (report && lane == 0) atomicOr(p.err, ERR_INDPTR);
+      return;
+    }
+    if (report && errs) atomicOr(p.err, errs);
+    long long sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    place(lane, sum, __shfl_sync(0xffffffffu, sum, 31));
+    return;
+  }
   // Inclusive sum over the CTA's threads.
   auto scan = [&](long long x, long long& all) {
 #pragma unroll
@@ -188,9 +225,6 @@ __device__ __forceinline__ void plan_share(const WeighParams& p, int cluster, Cu
     total += all;
   }
   if (report && errs) atomicOr(p.err, errs);
-  const long long used = min(static_cast<long long>(p.clusters), total);
-  if (cluster >= used) return;
-  const long long from = total * cluster / used, to = total * (cluster + 1) / used;
   long long before = 0;
   for (int b0 = 0; b0 < p.batch; b0 += NTHREADS) {
     if (p.batch > NTHREADS) {
@@ -198,18 +232,7 @@ __device__ __forceinline__ void plan_share(const WeighParams& p, int cluster, Cu
       sum = before + scan(own, all);
       before += all;
     }
-    if (own > 0 && sum - own <= from && from < sum) {   // one thread: the share starts in its request
-      Cursor c;
-      c.r = r;
-      c.left = to - from;
-      c.done = from;
-      c.total = total;
-      c.b = b0 + tid;
-      const long long step = from - (sum - own);
-      c.kb = static_cast<int>(r.s.block_at(step));
-      c.t = c.t0 = static_cast<int>(r.s.first(c.kb) + step - r.s.before(c.kb));
-      *start = c;
-    }
+    place(b0 + tid, sum, total);
   }
 }
 
