@@ -228,11 +228,12 @@ int mla_verify_plan_set_profile_events(mla_verify_plan* plan, void* after_pack,
  * on use the tags 2^32 - 2, 2^32 - 1, 2^32, .. (the epoch and the tags are
  * 64-bit: they do not wrap); every result must stay exact.  The value is
  * written by a pageable host copy: not for a call under stream capture.
- * MLA_VERIFY_FAULT_EVEN_GIVES_UP / _ODD_GIVES_UP (mla_verify_attn_shared):
- * that CTA of every pair with two steps or more stops in its second one, as
- * after a wait that ran out; its peer's waits run out (about a second), the
- * pair's rows come out NaN, MLA_VERIFY_DEV_TIMEOUT is set and the context
- * stays usable.
+ * MLA_VERIFY_FAULT_EVEN_GIVES_UP / _ODD_GIVES_UP (mla_verify_attn_shared,
+ * mla_verify_attn_chunk, mla_verify_weigh_kv): that CTA of every pair with two
+ * steps or more stops in its second one, as after a wait that ran out; its
+ * peer's waits run out (about a second), the pair's rows (mla_verify_weigh_kv:
+ * the weights of its keys) come out NaN, MLA_VERIFY_DEV_TIMEOUT is set and the
+ * context stays usable.
  * MLA_VERIFY_OK, or MLA_VERIFY_ERR_ARG for an unknown fault.
  */
 #define MLA_VERIFY_FAULT_NONE         0
@@ -421,8 +422,9 @@ int mla_verify_attn_chunk(mla_verify_plan* plan, int batch, int64_t num_tokens, 
  *            places whose slot is bad (BAD_SLOT).  If q_indptr is out of order
  *            (BAD_INDPTR) nothing is added at all.
  *
- * Products in bf16 (exact), sums in fp32: a score of magnitude s is off by
- * about 1e-6 s, and so its weight by that relative amount times scale.  A NaN
+ * Products in bf16 (exact), sums in fp32: a score dot(q, k) of magnitude s is
+ * off by about 1e-7 to 3e-7 s, and so its weight by scale times that of itself.
+ * A NaN
  * or infinite value in a query reaches the rows that it sees, one in a cached
  * row that row alone.  Sums are made in one order: equal inputs give equal
  * weights.  num_tokens as for mla_verify_attn_chunk; a weight_stride below

@@ -733,6 +733,8 @@ def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, k
     """
     B = kv_lens.shape[0]
     dev = plan.torch_device
+    if max(budget, sink, recent, extra_rows) > 0x7fffffff:   # (ctypes would cut them off)
+        raise ValueError("budget, sink, recent and extra_rows must be below 2^31")
     stride = _expect_weights(plan, weights, "weights", B)
     _expect(kv_indices, "kv_indices", torch.int32, dev)
     _expect(kv_indptr, "kv_indptr", torch.int32, dev, (B + 1,))

@@ -1064,6 +1064,8 @@ int mla_verify_weigh_kv(mla_verify_plan* pl, int batch, int64_t num_tokens, cons
   p.clusters = shared_clusters(pl);
   p.part = pl->ws_o;
   p.arrived = reinterpret_cast<unsigned*>(pl->err) + kArrivedWord;
+  p.fault_rank = pl->fault == MLA_VERIFY_FAULT_EVEN_GIVES_UP ? 0 : pl->fault == MLA_VERIFY_FAULT_ODD_GIVES_UP ? 1 : -1;
+  pl->fault = MLA_VERIFY_FAULT_NONE;
   p.err = pl->err;
   mlav::WeighMaps maps;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

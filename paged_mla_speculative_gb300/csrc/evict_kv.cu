@@ -320,9 +320,11 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   }
   for (int g0 = 0; g0 < strips; g0 += GROUP) {
     const int g1 = min(strips, g0 + GROUP), entries = (g1 - g0) * WARPS;
+    unsigned long long kinds = 0;   // two bits a strip
     __syncthreads();
     for (int s = g0; s < g1; ++s) {
       const int x = kind(s * THREADS + tid);
+      kinds |= static_cast<unsigned long long>(x) << (2 * (s - g0));
       const unsigned above = __ballot_sync(0xffffffffu, x == 1), ties = __ballot_sync(0xffffffffu, x == 2);
       if (lane == 0) s_place[(s - g0) * WARPS + warp] = pair_of(__popc(above), __popc(ties));
     }
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
 #pragma unroll
       for (int u = 0; u < FLIGHT; ++u) {
         const int s = s0 + u, i = s * THREADS + tid;
-        const int x = s < g1 ? kind(i) : 0;
+        const int x = s < g1 ? static_cast<int>(kinds >> (2 * (s - g0)) & 3) : 0;
         const unsigned above = __ballot_sync(0xffffffffu, x == 1), ties = __ballot_sync(0xffffffffu, x == 2);
         const unsigned lower = (1u << lane) - 1;
         const long long place = s < g1 ? s_place[(s - g0) * WARPS + warp] : 0;
@@ -409,11 +411,19 @@ __device__ __forceinline__ void push_marked_part(const EvictArgs& a, int part, i
     const long long at = count + before + all + cta_scan<T>(mine, s_warp, these) - mine;
     all += these;
     // A warp writes out its 32 words one by one, a lane per bit.
-    for (unsigned some = __ballot_sync(0xffffffffu, word != 0); some; some &= some - 1) {
-      const int k = __ffs(static_cast<int>(some)) - 1;
+    const long long warp_at = __shfl_sync(0xffffffffu, at, 0);
+    const int off = static_cast<int>(at - warp_at);
+    auto put = [&](int k) {
       const unsigned x = __shfl_sync(0xffffffffu, word, k);
-      const long long to = __shfl_sync(0xffffffffu, at, k) + __popc(x & ((1u << lane) - 1));
+      const long long to = warp_at + __shfl_sync(0xffffffffu, off, k) + __popc(x & ((1u << lane) - 1));
       if ((x >> lane & 1u) && to < a.num_pages) a.free_pages[to] = (w + warp * 32 + k) * 32 + lane;
+    };
+    unsigned some = __ballot_sync(0xffffffffu, word != 0);
+    if (__popc(some) > 8) {
+#pragma unroll 8
+      for (int k = 0; k < 32; ++k) put(k);
+    } else {
+      for (; some; some &= some - 1) put(__ffs(static_cast<int>(some)) - 1);
     }
   }
   __syncthreads();

@@ -157,6 +157,7 @@ struct WeighParams {
   int max_kv_len;
   int clusters;
   float* part;                      // [2 * clusters][256]: sums of a cluster's first and last block
+  int fault_rank;                   // testing: the CTA of each pair that gives up in mid-call, -1 for none
   unsigned* arrived;                // [clusters][2], 0 between calls: clusters done with the block that this one shares first
   int* err;
 };

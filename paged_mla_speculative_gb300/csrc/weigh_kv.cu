@@ -74,6 +74,10 @@ constexpr int TMEM_COLS = 512;              // two buffers of 256 columns
 constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);   // stride 1024 bytes, 128-byte swizzle
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFF) | (16u >> 4) << 16; }
 
+// Testing: the query slot before which WeighParams::fault_rank's CTA gives up
+// (in the second step of its share).
+constexpr int FAULT_SLOT = NCHUNK + 3;
+
 // A request as every role derives it.
 struct Request {
   int n, c, cached, ip0, q0;
@@ -305,6 +309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
           for (int c = 0; c < NCHUNK; ++c, ++n) {
             const int slot = n % NQ;
             if (n >= NQ) wait_bar<false>(mbar(MB_QE + slot), static_cast<uint32_t>((n / NQ - 1) & 1), s_abort, p.err);
+            if (n == FAULT_SLOT && p.fault_rank == static_cast<int>(rank)) *s_abort = 1;   // (testing)
             if (*s_abort) break;
             if (rank == 0) {
               if (lane == 0) tc::mbar_arrive_expect(mbar(MB_QF + slot), 2 * boxes * Q_BOX * 128);

@@ -275,7 +275,6 @@ def test_captured_and_replayed_and_default_outputs():
 
 def test_refusals():
     case = Case([200, 300], 64, 40, layers=2, seed=11)
-    n = 2
     with case.plan() as plan:
         w = case.weights
         args = dict(weights=w, budget=100, kv_indices=_i32(case.indices), kv_indptr=_i32(case.indptr), kv_lens=_i32(case.lens),
@@ -292,6 +291,8 @@ def test_refusals():
                     dict(kv_cache=case.cache[0].expand(2, 40 * 64, 576))):
             with pytest.raises(mb.MlaVerifyError):
                 mb.evict_kv(plan, **dict(args, **bad))
+        for bad in (dict(budget=1 << 32), dict(budget=(1 << 32) + 100), dict(sink=1 << 40), dict(extra_rows=1 << 33)):
+            with pytest.raises(ValueError):
+                mb.evict_kv(plan, **dict(args, **bad))
         torch.cuda.synchronize()
         assert plan.get_error() == 0 and args["page_refs"].tolist() == case.refs
-    assert n == len(case.lens)

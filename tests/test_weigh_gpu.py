@@ -297,6 +297,31 @@ def test_captured_and_replayed_and_on_another_stream():
     compare(d, g["weights"])
 
 
+@pytest.mark.parametrize("page", [1, 64])
+@pytest.mark.parametrize("fault", [mb.FAULT_EVEN_GIVES_UP, mb.FAULT_ODD_GIVES_UP])
+@pytest.mark.parametrize("new,lens,H", [([1] * 40, [1500] * 40, 16), ([40], [9000], 64)])
+def test_weights_of_a_pair_that_gave_up_are_nan(new, lens, H, fault, page):
+    """One CTA of each pair stops in its second step, the other's waits run out:
+    a weight is NaN, or right where its block was done before or is shared with
+    nobody who stopped.  The next call is right."""
+    d = make(new, lens, H, page, seed=22)
+    with C.plan_for(d) as plan:
+        g = C.to_cuda(d)
+        plan.inject_fault(fault)
+        weigh(plan, g)
+        torch.cuda.synchronize()
+        assert plan.get_error() == mb.DEV_TIMEOUT
+        got = g["weights"].double().cpu().numpy()
+        w, tol = reference(d)
+        lost = np.isnan(got)
+        assert lost.mean() > 0.5 and (lost | (np.abs(np.where(lost, 0, got) - w) <= tol)).all()
+        g = C.to_cuda(d)
+        weigh(plan, g)
+        torch.cuda.synchronize()
+        assert plan.get_error() == 0
+    compare(d, g["weights"])
+
+
 def test_no_tokens_and_refusals():
     d = make([2, 1], [70, 5], 16, 64, seed=19)
     g = C.to_cuda(d)
