@@ -305,6 +305,16 @@ def _expect(t: torch.Tensor, name: str, dtype, device=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _expect_int32(device, *tensors):
+    """_expect for (tensor, name, shape or None) in turn, int32 on the CUDA
+    device: with ten of them in a call its own calls were half the time."""
+    index = device.index
+    for t, name, shape in tensors:
+        if not (type(t) is torch.Tensor and t.dtype is torch.int32 and t.get_device() == index
+                and t.is_contiguous() and (shape is None or t.shape == shape)):
+            _expect(t, name, torch.int32, device, shape)
+
+
 def _expect_strided(t: torch.Tensor, name: str, dtype, device, shape):
     """A tensor whose vectors (last dim) are contiguous and 16-byte strided;
     returns its other strides (0 for a dim of one vector)."""
@@ -712,6 +722,17 @@ def free_kv(plan: Plan, kv_indices, kv_indptr, page_refs, free_pages, free_count
     _check(st, "mla_verify_free_kv")
 
 
+def _expect_layers(plan: Plan, kv_cache):
+    """A cache of one layer or several; returns (pointer, layers, stride)."""
+    layers = kv_cache.shape[0] if kv_cache.dim() == 3 else 1
+    if not (kv_cache.dim() == 3 and layers > 0 and kv_cache.dtype is torch.bfloat16
+            and kv_cache.shape[1:] == (plan.num_slots, 576) and kv_cache.stride()[1:] == (576, 1)
+            and kv_cache.device == plan.torch_device):      # (a view of a layer takes over 1 us)
+        layer = kv_cache if kv_cache.dim() == 2 else kv_cache[0]
+        _expect(layer, "kv_cache", torch.bfloat16, plan.torch_device, (plan.num_slots, 576))
+    return kv_cache.data_ptr(), layers, kv_cache.stride(0) if layers > 1 else 0
+
+
 def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, kv_cache, page_refs,
              free_pages, free_count, sink: int = 0, recent: int = 0, extra_rows: int = 0,
              new_indices=None, new_indptr=None, new_lens=None, new_weights=None, stream=None):
@@ -736,19 +757,8 @@ def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, k
     if max(budget, sink, recent, extra_rows) > 0x7fffffff:   # (ctypes would cut them off)
         raise ValueError("budget, sink, recent and extra_rows must be below 2^31")
     stride = _expect_weights(plan, weights, "weights", B)
-    _expect(kv_indices, "kv_indices", torch.int32, dev)
-    _expect(kv_indptr, "kv_indptr", torch.int32, dev, (B + 1,))
-    _expect(kv_lens, "kv_lens", torch.int32, dev, (B,))
     units = plan.num_slots // plan.page_size
-    _expect(page_refs, "page_refs", torch.int32, dev, (units,))
-    _expect(free_pages, "free_pages", torch.int32, dev, (units,))
-    _expect(free_count, "free_count", torch.int32, dev, (1,))
-    cache, layers, layer_stride = None, 1, 0
-    if kv_cache is not None:
-        layers = 1 if kv_cache.dim() == 2 else kv_cache.shape[0]
-        layer = kv_cache if kv_cache.dim() == 2 else kv_cache[0]
-        _expect(layer, "kv_cache", torch.bfloat16, dev, (plan.num_slots, 576))
-        cache, layer_stride = kv_cache.data_ptr(), kv_cache.stride(0) if layers > 1 else 0
+    cache, layers, layer_stride = (None, 1, 0) if kv_cache is None else _expect_layers(plan, kv_cache)
     if new_indices is None or new_indptr is None or new_lens is None or new_weights is None:
         with _allocating_on(stream, dev):
             if new_indices is None:
@@ -760,9 +770,9 @@ def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, k
                 new_lens = torch.empty(B, dtype=torch.int32, device=dev)
             if new_weights is None:
                 new_weights = torch.empty((B, weights.shape[1]), dtype=torch.float32, device=dev)
-    _expect(new_indices, "new_indices", torch.int32, dev)
-    _expect(new_indptr, "new_indptr", torch.int32, dev, (B + 1,))
-    _expect(new_lens, "new_lens", torch.int32, dev, (B,))
+    _expect_int32(dev, (kv_indices, "kv_indices", None), (kv_indptr, "kv_indptr", (B + 1,)), (kv_lens, "kv_lens", (B,)),
+                  (page_refs, "page_refs", (units,)), (free_pages, "free_pages", (units,)), (free_count, "free_count", (1,)),
+                  (new_indices, "new_indices", None), (new_indptr, "new_indptr", (B + 1,)), (new_lens, "new_lens", (B,)))
     new_stride = _expect_weights(plan, new_weights, "new_weights", B)
     st = load_library().mla_verify_evict_kv(
         plan.handle, B, weights.data_ptr(), stride, budget, sink, recent, kv_indices.data_ptr(),

@@ -1,12 +1,32 @@
-// What the two CTA-pair attention kernels (partial_pair.cu and
-// partial_shared.cu) have in common: bounded waits, the shuffle reduction and
-// the order of the ring units.
+// What the CTA-pair kernels (partial_pair.cu, partial_shared.cu, weigh_kv.cu)
+// have in common: bounded waits, the shuffle reduction and the order of the
+// ring units; and two instructions that tc_ptx.cuh does not have.
 #pragma once
 
 #include "common.cuh"
 #include "tc_ptx.cuh"
 
 namespace mlav {
+namespace tc {
+
+// TMA tile load of a 2-D tensor for this CTA alone, signalled on a barrier of
+// its own.  Warp-collective; the elected lane issues.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t mbar) {
+  asm volatile(
+      "{\n.reg .pred e;\n"
+      "elect.sync _|e, 0xffffffff;\n"
+      "@e cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(mbar)
+      : "memory");
+}
+// An 8x8 matrix of 16-bit values, a row's pairs in four lanes, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(w));
+  return r;
+}
+
+}  // namespace tc
 
 constexpr long long WAIT_LIMIT = 1LL << 31;     // cycles before a wait gives up
 

@@ -156,12 +156,6 @@ __device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t* r) {
                "r"(r[2]), "r"(r[3])
                : "memory");
 }
-// An 8x8 matrix of 16-bit values, a row's pairs in four lanes, transposed.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(w));
-  return r;
-}
 // One TMEM column for the warp's 32 lanes.
 __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
   uint32_t r;
@@ -346,16 +340,7 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
       "l"(tmap), "r"(x), "r"(y), "r"(cluster_mbar)
       : "memory");
 }
-// TMA tile load of a 2-D tensor for this CTA alone, signalled on a barrier of its own.
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t mbar) {
-  asm volatile(
-      "{\n.reg .pred e;\n"
-      "elect.sync _|e, 0xffffffff;\n"
-      "@e cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
-      "l"(tmap), "r"(x), "r"(y), "r"(mbar)
-      : "memory");
-}
-// TMA tile load of a 3-D tensor (planes z of rows y) for a CTA pair.
+// The same for a 3-D tensor (planes z of rows y).
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap, int x, int y, int z,
                                                  uint32_t cluster_mbar) {
   asm volatile(
