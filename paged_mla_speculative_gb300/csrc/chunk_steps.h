@@ -31,10 +31,14 @@ struct ChunkSteps {
       : m(2LL * H), u((127 + (static_cast<long long>(n) - c + 256) * H) / 128),
         tiles((static_cast<long long>(c) * H + 127) / 128), last((static_cast<long long>(n) + 255) / 256), unit(step_cost),
         per_tile(tile_cost) {}
-  MLAV_HD long long steps(long long t) const { return t + 1 < tiles ? (t + u) / m : last; }
+  MLAV_HD long long steps(long long t) const { return t + 1 < tiles ? divide(t + u, m) : last; }
+  // (A 64-bit division takes several times as long as a 32-bit one.)
+  static MLAV_HD long long divide(long long x, long long by) {
+    return x >> 32 ? x / by : static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(by));
+  }
   // Sum of y / m over 0 <= y < x.
   MLAV_HD long long quotients(long long x) const {
-    const long long q = x / m, r = x - q * m;
+    const long long q = divide(x, m), r = x - q * m;
     return m * (q * (q - 1) / 2) + r * q;
   }
   // Cost of the first t tiles (t <= tiles).
