@@ -507,13 +507,13 @@ __global__ void __launch_bounds__(COPY_THREADS) evict_copy_kernel(const EvictArg
   }
 }
 
-__global__ void __launch_bounds__(COPY_THREADS) evict_push_kernel(const EvictArgs a) {
-  __shared__ long long s_warp[COPY_THREADS / 32];
+__global__ void __launch_bounds__(THREADS) evict_push_kernel(const EvictArgs a) {
+  __shared__ long long s_warp[WARPS];
   __shared__ int s_done;
   asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;\n" ::: "memory");
   const long long count = *a.free_count;
   if (count < 0 || count > a.num_pages) return;   // (reported, and nothing was given back)
-  push_marked_part<COPY_THREADS>(a, blockIdx.x, gridDim.x, count, s_warp, s_done);
+  push_marked_part<THREADS>(a, blockIdx.x, gridDim.x, count, s_warp, s_done);
 }
 
 }  // namespace
@@ -543,8 +543,8 @@ cudaError_t launch_evict_kv(const EvictArgs& a, int num_sms, cudaStream_t stream
     return launch_overlapping(evict_copy_kernel, dim3(parts + 1, requests, z), COPY_THREADS, 0, stream, 1, a, each);
   }
   // A word per thread, as long as the words before a CTA's are soon added up.
-  const unsigned push = static_cast<unsigned>(std::clamp(a.num_pages / 32 / COPY_THREADS, 1, 128));
-  return launch_overlapping(evict_push_kernel, dim3(push), COPY_THREADS, 0, stream, 1, a);
+  const unsigned push = static_cast<unsigned>(std::clamp((a.num_pages / 32 + THREADS - 1) / THREADS, 1, 128));
+  return launch_overlapping(evict_push_kernel, dim3(push), THREADS, 0, stream, 1, a);
 }
 
 }  // namespace mlav
