@@ -39,7 +39,10 @@ the shards' partials (pins: tests/test_context_parallel_pins.py).  ``compact_ref
 restates KV compaction into 64-row pages (pins: tests/test_compact_pins.py).
 ``append_ref.append_kv`` restates the write of new tokens' rows and queries,
 ``page_pool_ref.fork_kv`` / ``free_kv`` the branches of cached requests over
-counted pages (pins: tests/test_prompt_pins.py).
+counted pages (pins: tests/test_prompt_pins.py).  ``chunk_ref.chunk_attn``
+restates the causal attention of a request's new tokens, ``evict_ref.weigh`` the
+weight that they give to its rows and ``evict_ref.evict_kv`` the eviction of the
+rows with the smallest (pins: tests/test_evict_pins.py).
 
 Pins (tests/test_oracle_pins.py): pure-Python brute force on tiny inputs, a
 hand-derived closed-form fixture (tests/golden/), one-visible-key, identical
