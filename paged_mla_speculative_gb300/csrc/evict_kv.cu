@@ -54,6 +54,7 @@ __device__ __forceinline__ unsigned ordered(float w) {
   const unsigned u = __float_as_uint(w == 0.f ? 0.f : w);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+constexpr unsigned PROTECTED = 0xffffffffu;   // no weight's key
 // The weight of a key (a NaN for NaN, 0 for -0).
 __device__ __forceinline__ float weight_of(unsigned key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
 
@@ -136,8 +137,10 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   if (tid < a.batch) item = load_item(a, tid);
   // A CTA that has the request alone loads the weights before it knows how many.
   const bool alone = ctas == 1 && a.max_kv_len <= cached;
-  if (alone)
+  if (alone) {
+#pragma unroll 8
     for (int i = tid; i < a.max_kv_len; i += THREADS) s_keys[i] = ordered(row[i]);
+  }
   const bool height_ok = height >= 0 && height <= a.num_pages;
   const long long left = height_ok ? height : -1;   // a stack that is out of order serves nobody
   if (tid < 2) s_last[tid] = 0;
@@ -203,34 +206,44 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   auto entry_at = [&](long long e) { return e < it.stay ? held[e] : a.free_pages[left - 1 - (low(s_mine) + e - it.stay)]; };
   const int first_entry = e0 < it.total ? entry_at(e0) : 0, first_left = l0 < it.entries ? held[l0] : 0;
 
-  const int lo = a.sink, hi = n - a.recent;    // rows lo .. hi - 1 are chosen among, when the request is over the budget
   // This CTA's rows: strips of THREADS rows.
   const int strips_each = static_cast<int>((n + all_threads - 1) / all_threads);
   const int j0 = static_cast<int>(min(static_cast<long long>(rank) * strips_each * THREADS, static_cast<long long>(n)));
   const int count = min(strips_each * THREADS, n - j0), strips = (count + THREADS - 1) / THREADS;
   const bool in_smem = count <= cached;
-  int k = a.budget - a.sink - a.recent;        // to be chosen
-  unsigned cut = 0xffffffffu;                  // the key of the last one chosen
+  // A request over the budget: the `budget` rows with the largest keys are
+  // kept, protected rows having a key above all others.  (The places behind
+  // the last row have the lowest: the rows before them are more than enough.)
+  const int lo = a.sink - j0, hi = n - a.recent - j0;   // rows before lo and from hi on are protected
+  auto key_of = [&](int i) { return i >= count ? 0u : i < lo || i >= hi ? PROTECTED : ordered(row[j0 + i]); };
+  auto key_at = [&](int i) { return in_smem ? s_keys[i] : key_of(i); };
+  int k = a.budget;
+  unsigned cut = PROTECTED;                    // the key of the last row that is kept
   int equal = 0;                               // of the rows with that key, how many
-  auto key_at = [&](int i) { return in_smem ? s_keys[i] : ordered(row[j0 + i]); };
   if (over && k > 0) {
-    if (!alone && in_smem)   // (a thread uses the rows that it loaded)
-      for (int i = tid; i < count; i += THREADS) s_keys[i] = ordered(row[j0 + i]);
+    if (alone) {
+      for (int i = count + tid; i < strips * THREADS; i += THREADS) s_keys[i] = 0;
+      for (int i = tid; i < lo; i += THREADS) s_keys[i] = PROTECTED;
+      for (int i = hi + tid; i < count; i += THREADS) s_keys[i] = PROTECTED;
+    } else if (in_smem) {
+#pragma unroll 8
+      for (int i = tid; i < strips * THREADS; i += THREADS) s_keys[i] = key_of(i);
+    }
     unsigned prefix = 0;
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
       for (int i = tid; i < BINS; i += THREADS) s_hist[i] = 0;
       __syncthreads();
+      const unsigned mask = (1u << bits) - 1;
 #pragma unroll 4
       for (int s = 0; s < strips; ++s) {
-        const int i = s * THREADS + tid, j = j0 + i;
-        bool mine = i < count && j >= lo && j < hi;
-        const unsigned key = mine ? key_at(i) : 0;
-        mine = mine && (pass == 0 || (key >> (shift + bits)) == prefix);
-        const int bin = mine ? static_cast<int>((key >> shift) & ((1u << bits) - 1)) : -1;
-        if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {   // (many rows of one weight: one addition for the warp)
-          if (bin >= 0 && lane == 0) atomicAdd(s_hist + bin, 32);
-        } else if (bin >= 0) {
+        const unsigned key = key_at(s * THREADS + tid);
+        const bool mine = pass == 0 || key >> (shift + bits) == prefix;
+        const unsigned bin = key >> shift & mask;
+        // (Many rows of one weight: one addition for the warp.)
+        if (__all_sync(0xffffffffu, mine) && __all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {
+          if (lane == 0) atomicAdd(s_hist + bin, 32);
+        } else if (mine) {
           atomicAdd(s_hist + bin, 1);
         }
       }
@@ -283,16 +296,6 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
     cut = prefix;
     equal = k;
   }
-  const bool have_keys = in_smem && (alone || (over && a.budget > a.sink + a.recent));
-  // 1: kept, 2: kept while there are fewer than `equal`, 0: not (nor is there a row).
-  auto kind = [&](int i) {
-    const int j = j0 + i;
-    if (i >= count) return 0;
-    if (!over || j < lo || j >= hi) return 1;
-    if (equal == 0) return 0;
-    const unsigned key = key_at(i);
-    return key == cut ? 2 : key > cut ? 1 : 0;
-  };
   // (Each thread's first entries: their counts answer while rows are placed.)
   auto put_entry = [&](long long e, int page) {   // the count that a fresh entry had
     table[e] = page;
@@ -311,10 +314,12 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   long long base = 0;
   if (ctas > 1) {
     int above = 0, ties = 0;
+#pragma unroll 4
     for (int s = 0; s < strips; ++s) {
-      const int x = kind(s * THREADS + tid);
-      above += x == 1;
-      ties += x == 2;
+      const int i = s * THREADS + tid;
+      const unsigned key = over ? key_at(i) : 0;
+      above += over ? key > cut : i < count;
+      ties += over && key == cut;
     }
     long long all;
     cta_scan<THREADS>(pair_of(above, ties), s_warp, all);
@@ -324,12 +329,19 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   }
   for (int g0 = 0; g0 < strips; g0 += GROUP) {
     const int g1 = min(strips, g0 + GROUP), entries = (g1 - g0) * WARPS;
-    unsigned long long kinds = 0;   // two bits a strip
+    // Rows that are kept (above the cut), and those with the cut's key, of
+    // which the first `equal` are.
+    auto strip = [&](int s, unsigned& key, unsigned& above, unsigned& ties) {
+      const int i = s * THREADS + tid;
+      key = over ? key_at(i) : 0;
+      above = __ballot_sync(0xffffffffu, over ? key > cut : i < count);
+      ties = __ballot_sync(0xffffffffu, over && key == cut);
+    };
     __syncthreads();
+#pragma unroll 4
     for (int s = g0; s < g1; ++s) {
-      const int x = kind(s * THREADS + tid);
-      kinds |= static_cast<unsigned long long>(x) << (2 * (s - g0));
-      const unsigned above = __ballot_sync(0xffffffffu, x == 1), ties = __ballot_sync(0xffffffffu, x == 2);
+      unsigned key, above, ties;
+      strip(s, key, above, ties);
       if (lane == 0) s_place[(s - g0) * WARPS + warp] = pair_of(__popc(above), __popc(ties));
     }
     __syncthreads();
@@ -345,15 +357,20 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
 #pragma unroll
       for (int u = 0; u < FLIGHT; ++u) {
         const int s = s0 + u, i = s * THREADS + tid;
-        const int x = s < g1 ? static_cast<int>(kinds >> (2 * (s - g0)) & 3) : 0;
-        const unsigned above = __ballot_sync(0xffffffffu, x == 1), ties = __ballot_sync(0xffffffffu, x == 2);
-        const unsigned lower = (1u << lane) - 1;
-        const long long place = s < g1 ? s_place[(s - g0) * WARPS + warp] : 0;
-        const int e = static_cast<int>(low(place)) + __popc(ties & lower);
-        to[u] = s >= g1 || i >= count                       ? -2
-                : x == 1 || (x == 2 && e < equal) ? static_cast<int>(high(place)) + __popc(above & lower) + min(e, equal)
-                                                  : -1;
-        w[u] = to[u] >= 0 ? (have_keys ? weight_of(s_keys[i]) : row[j0 + i]) : 0.f;
+        to[u] = -2;
+        w[u] = 0.f;
+        if (s < g1) {
+          unsigned key, above, ties;
+          strip(s, key, above, ties);
+          const long long place = s_place[(s - g0) * WARPS + warp];
+          const unsigned lower = (1u << lane) - 1;
+          const int e = static_cast<int>(low(place)) + __popc(ties & lower);
+          if (i < count)
+            to[u] = (above >> lane & 1) || ((ties >> lane & 1) && e < equal)
+                        ? static_cast<int>(high(place)) + __popc(above & lower) + min(e, equal)
+                        : -1;
+          if (to[u] >= 0) w[u] = over && key != PROTECTED ? weight_of(key) : row[j0 + i];
+        }
         slot[u] = a.page == 1 && to[u] != -2 ? held[j0 + i] : 0;
       }
       if (a.page > 1) {
