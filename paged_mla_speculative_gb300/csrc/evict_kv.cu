@@ -21,11 +21,12 @@
 // (evict_push_kernel where nothing is copied).
 //
 // The copies are bound by HBM (1152 bytes read and written a row and layer): 16
-// requests cut to 2048 rows in 16 layers, 1.2 GB, take 175 us, 6.7 TB/s, behind
-// 25 us of choosing (about 1000 instructions a row on an SM per request; a
-// cluster of two for these was no faster, its barriers taking what it gained).
+// requests cut to 2048 rows in 16 layers, 1.2 GB, take 206 us, 5.9 TB/s, of which
+// 24 are the choosing (450 to 500 instructions a row on an SM per request, half
+// of what it can issue in that time, barriers between; a cluster of two for
+// these was no faster, its barriers taking what it gained).
 // Single slots are bound by the atomics on 655000 scattered counts and bits: 32
-// requests of 16 to 32 thousand slots take 37 us and the push 13.
+// requests of 16 to 32 thousand slots take 41 us and the push 14.
 #include "common.cuh"
 #include "kernels.h"
 #include "page_pool.cuh"

@@ -32,8 +32,8 @@
 // the kernel but where a tile's land in shared memory, in place, by the
 // softmax warps while the last O^T of the tile before is computed.  A step
 // takes 3.5 us as in the other calls (2048 tokens of 64 heads behind 30720 rows:
-// 6.08 ms, 1.49 PFLOP/s); a tile's end and beginning 4.3 us more: 1.2 to 1.7 us
-// widening, 1.7 us readout, the rest until the next tile's first scores.
+// 6.1 to 6.3 ms, 1.45 to 1.49 PFLOP/s); a tile's end and beginning 4.3 us more: 1.0
+// to 1.8 us widening, 1.5 to 1.9 us readout, 0.7 us the next tile's first scores.
 //
 // Roles (20 warps per CTA): warps 0-15 softmax, warp 16 MMA issue (even CTA)
 // or P^T hand-off (odd CTA), warps 17-19 the key ring (17 the queries too).

@@ -24,8 +24,8 @@
 //
 // What bounds it: with many query rows the tensor cores and the queries' way
 // from L2 (16 KB a slot and CTA for 256 x 256 x 64 products): 256 tokens of 64
-// heads on 33000 rows take 322 us, 1.92 PFLOP/s, a step 2.4 us.  One load of
-// 16 KB per slot: with four of 4 KB a step took 3.0 us.  With few rows it is
+// heads on 33000 rows take 328 us, 1.89 PFLOP/s, a step 2.85 us.  One load of
+// 16 KB per slot: with four of 4 KB they took 449 us, a step 3.9.  With few rows it is
 // the keys' bytes: 16 decoding requests on 160000 rows take 43 us, 4.3 TB/s,
 // of which some 10 us are the launch, the division and the first block.
 //
