@@ -424,9 +424,8 @@ int mla_verify_attn_chunk(mla_verify_plan* plan, int batch, int64_t num_tokens, 
  *
  * Products in bf16 (exact), sums in fp32: a score dot(q, k) of magnitude s is
  * off by about 1e-7 to 3e-7 s, and so its weight by scale times that of itself.
- * A NaN
- * or infinite value in a query reaches the rows that it sees, one in a cached
- * row that row alone.  Sums are made in one order: equal inputs give equal
+ * A NaN or infinite value in a query reaches the rows that it sees, one in a
+ * cached row that row alone.  Sums are made in one order: equal inputs give equal
  * weights.  num_tokens as for mla_verify_attn_chunk; a weight_stride below
  * max_kv_len gives MLA_VERIFY_ERR_ARG; other errors as for mla_verify_attn.
  * Capturable; allocates nothing; shares the plan's workspace.

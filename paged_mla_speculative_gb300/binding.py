@@ -728,6 +728,8 @@ def _expect_layers(plan: Plan, kv_cache):
     if not (kv_cache.dim() == 3 and layers > 0 and kv_cache.dtype is torch.bfloat16
             and kv_cache.shape[1:] == (plan.num_slots, 576) and kv_cache.stride()[1:] == (576, 1)
             and kv_cache.device == plan.torch_device):      # (a view of a layer takes over 1 us)
+        if layers == 0:
+            raise ValueError("kv_cache must have a layer or more")
         layer = kv_cache if kv_cache.dim() == 2 else kv_cache[0]
         _expect(layer, "kv_cache", torch.bfloat16, plan.torch_device, (plan.num_slots, 576))
     return kv_cache.data_ptr(), layers, kv_cache.stride(0) if layers > 1 else 0
@@ -754,8 +756,8 @@ def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, k
     """
     B = kv_lens.shape[0]
     dev = plan.torch_device
-    if max(budget, sink, recent, extra_rows) > 0x7fffffff:   # (ctypes would cut them off)
-        raise ValueError("budget, sink, recent and extra_rows must be below 2^31")
+    if max(budget, sink, recent, extra_rows) >= 1 << 31 or min(budget, sink, recent, extra_rows) < -1 << 31:
+        raise ValueError("budget, sink, recent and extra_rows must fit in 32 bits")   # (ctypes would cut them off)
     stride = _expect_weights(plan, weights, "weights", B)
     units = plan.num_slots // plan.page_size
     cache, layers, layer_stride = (None, 1, 0) if kv_cache is None else _expect_layers(plan, kv_cache)

@@ -1,10 +1,13 @@
 """Pins of the eviction oracle: small cases by hand, and what must hold of any."""
 import math
 import random
+from types import SimpleNamespace
 
 import pytest
+import torch
 
 from oracle import evict_ref as E
+from paged_mla_speculative_gb300 import binding
 
 
 def test_rows_by_hand():
@@ -82,3 +85,20 @@ def test_what_holds_of_any_case(page):
                 assert [rows[0][at(new[b], i)] for i in range(len(kept))] == [old[at(tables[b], j)] for j in kept]
             else:
                 assert new[b][:len(kept)] == [tables[b][j] for j in kept]
+
+
+@pytest.mark.parametrize("size", [5 - 2**32, -2**31 - 1, 2**31, 2**32 + 5])
+@pytest.mark.parametrize("name", ["budget", "sink", "recent", "extra_rows"])
+def test_sizes_outside_int32_are_refused(name, size):
+    """They would reach the library cut off to 32 bits, as other sizes."""
+    plan = SimpleNamespace(torch_device=torch.device("cpu"))
+    sizes = dict(budget=8, sink=0, recent=0, extra_rows=0) | {name: size}
+    with pytest.raises(ValueError, match="32 bits"):
+        binding.evict_kv(plan, None, sizes.pop("budget"), None, None, torch.zeros(1, dtype=torch.int32), None, None, None, None,
+                         **sizes)
+
+
+def test_a_cache_without_layers_is_refused():
+    plan = SimpleNamespace(torch_device=torch.device("cpu"), num_slots=64)
+    with pytest.raises(ValueError, match="layer"):
+        binding._expect_layers(plan, torch.zeros((0, 64, 576), dtype=torch.bfloat16))
