@@ -16,17 +16,21 @@
 // requests are not written, and no row is read after it was overwritten), all
 // others of the table are given back.  Single slots: kept slots stay, no row
 // moves.
-// evict_copy_kernel: the kept rows of every layer into the fresh pages, and
+// With pages, CTAs of evict_select_kernel that no request needs copy the protected
+// rows meanwhile: those stay whatever the weights, and their places, too, follow
+// from the lengths.
+// evict_copy_kernel: the other kept rows of every layer into the fresh pages, and
 // beside it the pages whose count fell to 0, in ascending order, onto the stack
 // (evict_push_kernel where nothing is copied).
 //
 // The copies are bound by HBM (1152 bytes read and written a row and layer): 16
-// requests cut to 2048 rows in 16 layers, 1.2 GB, take 206 us, 5.9 TB/s, of which
-// 24 are the choosing (450 to 500 instructions a row on an SM per request, half
-// of what it can issue in that time, barriers between; a cluster of two for
-// these was no faster, its barriers taking what it gained).
-// Single slots are bound by the atomics on 655000 scattered counts and bits: 32
-// requests of 16 to 32 thousand slots take 41 us and the push 14.
+// requests cut to 2048 rows in 16 layers, 1.2 GB, take 193 us, 6.3 TB/s, with 256
+// protected rows copied while the others are chosen (206 behind the choosing,
+// which takes 24: 450 to 500 instructions a row on an SM per request, half of
+// what it can issue in that time, barriers between; a cluster of two for these
+// was no faster, its barriers taking what it gained).
+// Single slots: 32 requests of 16 to 32 thousand take 55 us, the choosing 41 and
+// the push 14.  The atomics on 655000 scattered counts and bits are 14 of the 55.
 #include "common.cuh"
 #include "kernels.h"
 #include "page_pool.cuh"
@@ -113,9 +117,62 @@ __device__ __forceinline__ long long pair_of(int hi, int lo) { return static_cas
 __device__ __forceinline__ long long high(long long x) { return x >> 32; }
 __device__ __forceinline__ long long low(long long x) { return x & 0xffffffffll; }
 
-// grid: `ctas` CTAs (a cluster) per request.  (The sums of all requests'
-// entries stay below 2^31: so does max_batch * max_kv_len.)
-__global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArgs a, int cached) {
+// A warp's share, warp `w` of `warps`, of the protected rows of an evicted
+// request that are copied early: those in its first fresh page before copy_from,
+// and its kept rows from copy_to on, four rows of
+// a layer at a time (with four layers, whose pages are looked up once, 16
+// requests took 199 us, not 193).  `top` is the first of its fresh pages on the
+// stack, the others lie below.
+constexpr int EARLY_FLIGHT = 5;
+constexpr long long EARLY_LEAST = 8192;   // rows, in all layers, that make up for the CTAs (260 made a call 2 us slower, 4160 gained nothing)
+constexpr long long EARLY_MOST = 65536;   // that can be copied while rows are chosen: 151 MB (1536 recent ones, all early 205 us, up to here 193)
+__device__ __noinline__ void copy_protected(const EvictArgs& a, int n, const int32_t* held, const int32_t* top, int w, int warps) {
+  const int lane = threadIdx.x & 31, from = a.sink / PAGE * PAGE, lead = a.copy_from - from, rows = lead + a.budget - a.copy_to;
+  const int quads = (rows + 3) / 4;
+  const long long tasks = static_cast<long long>(quads) * a.num_layers;
+  // Lane q, for row 4 quad + q % 4: its old and new page (-1: none), and the rows in them.
+  int src = -1, dst = -1, places = 0;
+  auto look_up = [&](long long task) {
+    const int r = 4 * static_cast<int>(task % quads) + (lane & 3);
+    src = dst = -1;
+    if (task >= tasks || r >= rows) return;
+    const int i = r < lead ? from + r : a.copy_to + r - lead, j = r < lead ? i : n - a.budget + i;
+    const int old_page = held[j / PAGE], new_page = top[from / PAGE - i / PAGE];
+    places = j % PAGE << 8 | i % PAGE;
+    if (new_page >= 0 && new_page < a.num_pages) dst = new_page;
+    if (old_page >= 0 && old_page < a.num_pages) src = old_page;
+    else if (lane < 4) atomicOr(a.err, ERR_SLOT);   // no such page: zeros
+  };
+  look_up(w);
+  for (long long task = w; task < tasks; task += warps) {
+    uint16_t* layer = a.kv_cache + task / quads * a.layer_stride;
+#pragma unroll
+    for (int u0 = 0; u0 < 9; u0 += EARLY_FLIGHT) {
+      uint4 v[EARLY_FLIGHT];
+#pragma unroll
+      for (int u = u0; u < min(u0 + EARLY_FLIGHT, 9); ++u) {
+        const int e = lane + 32 * u, q = e / ROW_CHUNKS;
+        const int page = __shfl_sync(0xffffffffu, src, q), row = __shfl_sync(0xffffffffu, places, q) >> 8;
+        v[u - u0] = page >= 0 ? *(reinterpret_cast<const uint4*>(layer + (static_cast<long long>(page) * PAGE + row) * D_QK) + e % ROW_CHUNKS)
+                              : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = u0; u < min(u0 + EARLY_FLIGHT, 9); ++u) {
+        const int e = lane + 32 * u, q = e / ROW_CHUNKS;
+        const int page = __shfl_sync(0xffffffffu, dst, q), row = __shfl_sync(0xffffffffu, places, q) & 255;
+        if (page >= 0) *(reinterpret_cast<uint4*>(layer + (static_cast<long long>(page) * PAGE + row) * D_QK) + e % ROW_CHUNKS) = v[u - u0];
+      }
+    }
+    look_up(task + warps);
+  }
+}
+
+// grid: `ctas` CTAs (a cluster) per request, then CTAs that copy protected rows,
+// as many for each request.  (The sums of all requests' entries stay below
+// 2^31: so does max_batch * max_kv_len.)  EARLY: whether there are such CTAs (as
+// one kernel, calls without them took 1 to 2 us longer).
+template <bool EARLY>
+__global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const __grid_constant__ EvictArgs a, int cached) {
   extern __shared__ unsigned s_keys[];
   __shared__ __align__(8) int s_hist[BINS];
   __shared__ int s_bins[WARPS];
@@ -131,13 +188,15 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
     if (ctas > 1) cluster.sync();
     else __syncthreads();
   };
-  const int b = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int copier = EARLY ? static_cast<int>(blockIdx.x) - ctas * a.batch : -1;   // 0 and above: one that copies
+  const int b = copier >= 0 ? copier % a.batch : static_cast<int>(blockIdx.x) / ctas;
   const float* row = a.weights + b * a.stride;
   const int height = *a.free_count;
   Item item{};
   if (tid < a.batch) item = load_item(a, tid);
   // A CTA that has the request alone loads the weights before it knows how many.
-  const bool alone = ctas == 1 && a.max_kv_len <= cached;
+  const bool alone = ctas == 1 && a.max_kv_len <= cached && copier < 0;
   if (alone) {
 #pragma unroll 8
     for (int i = tid; i < a.max_kv_len; i += THREADS) s_keys[i] = ordered(row[i]);
@@ -169,7 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   const Item it = s_item;
   const bool fits = high(s_fit) <= a.capacity && low(s_fit) <= left;
   const bool served = fits && !it.bad;
-  if (rank == 0 && tid == 0) {
+  if (rank == 0 && tid == 0 && copier < 0) {
     if (it.bad) atomicOr(a.err, it.bad);
     if (!it.bad && !fits && (it.total > 0 || it.entries > 0)) atomicOr(a.err, ERR_CAPACITY);
     a.new_lens[b] = served ? it.m + a.extra : 0;
@@ -179,7 +238,8 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   const long long all_threads = static_cast<long long>(ctas) * THREADS, me = static_cast<long long>(rank) * THREADS + tid;
   float* new_row = a.new_weights + b * a.new_stride;
   // Behind the kept rows: 0.
-  for (long long j = (served ? it.m : 0) + me; j < a.new_width; j += all_threads) new_row[j] = 0.f;
+  if (copier < 0)
+    for (long long j = (served ? it.m : 0) + me; j < a.new_width; j += all_threads) new_row[j] = 0.f;
   // The last CTA that has read the height lowers it.
   auto lower = [&]() {
     if (tid != 0) return;
@@ -191,7 +251,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
     if (height_ok) *a.free_count = static_cast<int32_t>(left - static_cast<long long>(s_last[1]));
     else atomicOr(a.err, ERR_CAPACITY);
   };
-  if (!served) {   // the whole cluster
+  if (!served || (copier >= 0 && it.n <= a.budget)) {   // the whole cluster
     lower();
     return;
   }
@@ -205,6 +265,12 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictArg
   // thread's first of both kinds is loaded here, and used at the end.
   const long long e0 = (a.page == 1 ? it.stay : 0) + me, l0 = (a.page == 1 ? n : it.stay) + me;
   auto entry_at = [&](long long e) { return e < it.stay ? held[e] : a.free_pages[left - 1 - (low(s_mine) + e - it.stay)]; };
+  if (copier >= 0) {
+    lower();
+    const int part = copier / a.batch, parts = (static_cast<int>(gridDim.x) - ctas * a.batch) / a.batch;
+    copy_protected(a, n, held, a.free_pages + (left - 1 - low(s_mine)), part * WARPS + warp, parts * WARPS);
+    return;
+  }
   const int first_entry = e0 < it.total ? entry_at(e0) : 0, first_left = l0 < it.entries ? held[l0] : 0;
 
   // This CTA's rows: strips of THREADS rows.
@@ -488,12 +554,11 @@ __global__ void __launch_bounds__(COPY_THREADS) evict_copy_kernel(const EvictArg
       push_marked_part<COPY_THREADS>(a, 0, 1, count, s_warp, s_done);
     return;
   }
-  const int stay = a.sink / PAGE;
-  const int i0 = stay * PAGE + static_cast<int>(blockIdx.x) * COPY_ROWS;
+  const int i0 = a.copy_from + static_cast<int>(blockIdx.x) * COPY_ROWS;
   for (int b = blockIdx.y; b < a.batch; b += gridDim.y) {
     // (A request that is not served has length 0; a length of 0 has no rows.)
     if (a.new_lens[b] == 0 || a.kv_lens[b] <= a.budget) continue;
-    const int rows = min(COPY_ROWS, a.budget - i0);
+    const int rows = min(COPY_ROWS, a.copy_to - i0);
     if (rows <= 0) continue;
     __syncthreads();
     if (tid < COPY_ROWS) {
@@ -541,19 +606,35 @@ __global__ void __launch_bounds__(THREADS) evict_push_kernel(const EvictArgs a) 
 }  // namespace
 
 cudaError_t evict_prepare() {
-  return cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_CACHED * 4);
+  const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_CACHED * 4);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, MAX_CACHED * 4);
 }
 
-cudaError_t launch_evict_kv(const EvictArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_evict_kv(const EvictArgs& args, int num_sms, cudaStream_t stream) {
+  EvictArgs a = args;
   // CTAs per request: more for long ones, while they fill no SM twice.
   int ctas = 1;
   while (ctas < MAX_CTAS && 2LL * ctas * a.batch <= num_sms && a.max_kv_len > ROWS_PER_CTA * ctas) ctas *= 2;
   const long long strips = (a.max_kv_len + static_cast<long long>(ctas) * THREADS - 1) / (static_cast<long long>(ctas) * THREADS);
   const int cached = static_cast<int>(std::min<long long>(strips * THREADS, MAX_CACHED));
-  cudaError_t e = launch_overlapping(evict_select_kernel, dim3(static_cast<unsigned>(ctas) * a.batch), THREADS,
-                                     static_cast<size_t>(cached) * 4, stream, static_cast<unsigned>(ctas), a, cached);
+  // The SMs that are left copy protected rows, where those are enough.
+  a.copy_from = a.sink / PAGE * PAGE;
+  a.copy_to = std::min(a.budget, a.max_kv_len);
+  int copiers = 0;
+  if (a.page > 1 && a.budget < a.max_kv_len) {
+    const long long each = static_cast<long long>(a.batch) * a.num_layers;   // rows of the call per row of a request
+    const int lead = a.sink - a.copy_from, early = lead + static_cast<int>(std::min<long long>(a.recent, EARLY_MOST / each));
+    const long long tasks = (early + 3LL) / 4 * a.num_layers, enough = ((tasks + WARPS - 1) / WARPS + ctas - 1) / ctas * ctas;
+    if (early * each >= EARLY_LEAST)
+      copiers = static_cast<int>(std::clamp<long long>((num_sms - ctas * a.batch) / a.batch / ctas * ctas, 0, enough));
+    if (copiers > 0) a.copy_from = a.sink, a.copy_to -= early - lead;
+  }
+  cudaError_t e = launch_overlapping(copiers > 0 ? evict_select_kernel<true> : evict_select_kernel<false>,
+                                     dim3(static_cast<unsigned>(ctas + copiers) * a.batch), THREADS, static_cast<size_t>(cached) * 4,
+                                     stream, static_cast<unsigned>(ctas), a, cached);
   if (e != cudaSuccess) return e;
-  const int moved = std::min(a.budget, a.max_kv_len) - a.sink / PAGE * PAGE;
+  const int moved = a.copy_to - a.copy_from;
   if (a.page > 1 && moved > 0) {
     const unsigned parts = static_cast<unsigned>((moved + COPY_ROWS - 1) / COPY_ROWS);
     const unsigned requests = static_cast<unsigned>(std::min(a.batch, 65535));

@@ -258,6 +258,9 @@ struct EvictArgs {
   unsigned* page_bits;              // plan workspace, one bit per page, 0 between calls
   unsigned* ticket;                 // plan workspace: three words, 0 between calls
   int* err;
+  // Set by the launch: rows [copy_from, copy_to) of an evicted request's kept
+  // ones are copied once all are chosen, the others (protected ones) before.
+  int copy_from, copy_to;
 };
 cudaError_t evict_prepare();
 cudaError_t launch_evict_kv(const EvictArgs& a, int num_sms, cudaStream_t stream);

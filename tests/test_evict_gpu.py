@@ -296,3 +296,39 @@ def test_refusals():
                 mb.evict_kv(plan, **dict(args, **bad))
         torch.cuda.synchronize()
         assert plan.get_error() == 0 and args["page_refs"].tolist() == case.refs
+
+
+# Protected rows enough that they are copied while the others are chosen.
+@pytest.mark.parametrize("lens,budget,sink,recent,extra,layers,max_len", [
+    ([300, 500, 130, 64], 120, 5, 70, 8, 40, None),       # 64 is within the budget
+    ([300, 500, 131, 0], 131, 66, 65, 0, 40, None),       # nothing besides is kept; a page stays; one is equal to the budget
+    ([700], 300, 0, 130, 1, 67, None),                    # no leading row, layers that do not divide
+    ([400, 333], 200, 63, 100, 0, 64, 13000),             # a cluster of two CTAs per request
+    ([333, 400], 250, 1, 200, 0, 300, None),              # more than are copied early: the first of them go with the others
+])
+def test_protected_rows_of_many_layers(lens, budget, sink, recent, extra, layers, max_len):
+    units = sum(-(-n // 64) + -(-(min(n, budget) + extra) // 64) for n in lens) + 3
+    case = Case(lens, 64, units, layers=layers, seed=sum(lens), max_len=max_len, pad=64)
+    with case.plan() as plan:
+        assert case.evict(plan, budget, sink, recent, extra)[0] == 0
+
+
+def test_protected_rows_of_requests_that_are_not_served_or_have_bad_pages():
+    def make():
+        return Case([300, 500, 130], 64, 30, layers=50, seed=10)
+    for capacity in (1, 2, 4, 5):
+        case = make()
+        with case.plan() as plan:
+            assert case.evict(plan, 120, 5, 70, capacity=capacity)[0] == mb.DEV_CAPACITY
+    case = make()
+    case.stack = case.stack[:3]
+    with case.plan() as plan:
+        assert case.evict(plan, 120, 5, 70)[0] == mb.DEV_CAPACITY
+    case = make()
+    case.lens[1] = 9999
+    with case.plan() as plan:
+        assert case.evict(plan, 120, 5, 70)[0] & mb.DEV_BAD_LEN
+    case = make()
+    case.indices[0], case.indices[-1], case.stack[-1] = -1, case.units, case.units + 5
+    with case.plan() as plan:
+        assert case.evict(plan, 120, 5, 70)[0] & mb.DEV_BAD_SLOT
