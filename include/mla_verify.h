@@ -422,8 +422,14 @@ int mla_verify_attn_chunk(mla_verify_plan* plan, int batch, int64_t num_tokens, 
  *            places whose slot is bad (BAD_SLOT).  If q_indptr is out of order
  *            (BAD_INDPTR) nothing is added at all.
  *
- * Products in bf16 (exact), sums in fp32: a score dot(q, k) of magnitude s is
- * off by about 1e-7 to 3e-7 s, and so its weight by scale times that of itself.
+ * Products in bf16 (exact), sums in fp32, cut towards zero: a score dot(q, k) of
+ * magnitude s comes out 4e-7 to 6e-7 s too small where its partial sums lose
+ * bits, exact where they lose none, and never further off than 72 * 2^-23 of
+ * sum |q_d k_d|; its weight is off by scale times that of itself.  The scores of
+ * mla_verify_attn_chunk lose the same: with its lse a query row's weights add up
+ * to 1 to within 4e-7 |lse| + 3e-6 at most; with the lse of more exact scores
+ * they come out those 4e-7 to 6e-7 |scale * s| of themselves too small (negative
+ * scores: too large).
  * A NaN or infinite value in a query reaches the rows that it sees, one in a
  * cached row that row alone.  Sums are made in one order: equal inputs give equal
  * weights.  num_tokens as for mla_verify_attn_chunk; a weight_stride below

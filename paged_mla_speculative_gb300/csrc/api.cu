@@ -1049,12 +1049,9 @@ int mla_verify_weigh_kv(mla_verify_plan* pl, int batch, int64_t num_tokens, cons
   p.lse = lse;
   p.weights = weights;
   p.stride = weight_stride;
-  // The tensor cores cut what they have summed so far, towards zero, to fp32:
-  // as measured, a score of magnitude s comes out 3.8 2^-23 s too small on
-  // average (half a unit in the last place for each 32 of its dims).  Scores
-  // are raised by that much: weights are then off by 0.4e-6 of themselves where
-  // they were by 3.0e-6.
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634 * (1.0 + 3.8 / 8388608.0));
+  // As in the attention calls, whose scores lose the same in their sums: what
+  // the lse is off by cancels.
+  p.scale_log2 = scale * mlav::kLog2e;
   p.batch = batch;
   p.num_tokens = static_cast<int>(num_tokens);
   p.H = pl->H;
