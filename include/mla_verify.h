@@ -383,8 +383,9 @@ int mla_verify_attn_shared(mla_verify_plan* plan, int batch, const void* q, cons
  *   lse       fp32 [num_tokens][H]
  *
  * kv_indices, kv_indptr and kv_lens as for mla_verify_attn, with c_b <= n_b <=
- * max_kv_len; a request without new tokens is not read.  A request whose length
- * or table is out of order comes out NaN (MLA_VERIFY_DEV_BAD_LEN / BAD_INDPTR); a
+ * max_kv_len; of a request without new tokens neither length nor table is looked
+ * at (an idle slot of a captured batch; kv_indptr[batch] bounds the others'
+ * tables all the same).  A request whose length or table is out of order comes out NaN (MLA_VERIFY_DEV_BAD_LEN / BAD_INDPTR); a
  * q_indptr that is out of order makes all num_tokens tokens NaN (BAD_INDPTR).
  * Bad slots are masked (BAD_SLOT); a token none of whose keys is left has out 0
  * and lse -inf.  Values outside the fp16 range (MLA_VERIFY_DEV_RANGE) make the

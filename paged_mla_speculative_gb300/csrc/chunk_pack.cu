@@ -72,8 +72,9 @@ __device__ __forceinline__ int scan_chunks(const SharedParams& p, int* base, int
       const long long need = p.page_size == 1 ? n : (static_cast<long long>(n) + PAGE - 1) / PAGE;
       const bool len_ok = n >= c && n >= 0 && n <= p.max_kv_len;
       const bool ptr_ok = ip0 >= 0 && ip1 >= ip0 && ip1 <= ipn && static_cast<long long>(ip1) - ip0 == need;
-      if (tokens_ok && !(len_ok && ptr_ok)) errs |= len_ok ? ERR_INDPTR : ERR_LEN;
-      if (tokens_ok && len_ok && ptr_ok && c > 0) {
+      // (A request without new tokens may hold anything: an idle slot of a batch.)
+      if (tokens_ok && c > 0 && !(len_ok && ptr_ok)) errs |= len_ok ? ERR_INDPTR : ERR_LEN;
+      if (tokens_ok && c > 0 && len_ok && ptr_ok) {
         const ChunkSteps s = chunk_steps(n, c, p.H);
         mine = n;
         rows = static_cast<int>(s.tiles);
