@@ -385,8 +385,9 @@ int mla_verify_attn_shared(mla_verify_plan* plan, int batch, const void* q, cons
  * kv_indices, kv_indptr and kv_lens as for mla_verify_attn, with c_b <= n_b <=
  * max_kv_len; of a request without new tokens neither length nor table is looked
  * at (an idle slot of a captured batch; kv_indptr[batch] bounds the others'
- * tables all the same).  A request whose length or table is out of order comes out NaN (MLA_VERIFY_DEV_BAD_LEN / BAD_INDPTR); a
- * q_indptr that is out of order makes all num_tokens tokens NaN (BAD_INDPTR).
+ * tables all the same).  A request whose length or table is out of order comes
+ * out NaN (MLA_VERIFY_DEV_BAD_LEN / BAD_INDPTR); a q_indptr that is out of order
+ * makes all num_tokens tokens NaN (BAD_INDPTR).
  * Bad slots are masked (BAD_SLOT); a token none of whose keys is left has out 0
  * and lse -inf.  Values outside the fp16 range (MLA_VERIFY_DEV_RANGE) make the
  * rows that see them NaN and touch no others.  Numerics as for
@@ -419,7 +420,8 @@ int mla_verify_attn_chunk(mla_verify_plan* plan, int batch, int64_t num_tokens, 
  *   lse      fp32 [num_tokens][H]; a row that is not finite adds nothing.
  *   weights  fp32 [batch] rows, weight_stride >= max_kv_len floats apart; places
  *            from kv_lens[b] on are not touched, nor are rows of requests without
- *            new tokens or out of order (MLA_VERIFY_DEV_BAD_LEN / BAD_INDPTR), nor
+ *            new tokens (whatever their length and table hold) or out of order
+ *            (MLA_VERIFY_DEV_BAD_LEN / BAD_INDPTR), nor
  *            places whose slot is bad (BAD_SLOT).  If q_indptr is out of order
  *            (BAD_INDPTR) nothing is added at all.
  *

@@ -99,13 +99,15 @@ __device__ __forceinline__ bool load_request(const WeighParams& p, int b, Reques
   const long long need = p.page_size == 1 ? r.n : (static_cast<long long>(r.n) + PAGE - 1) / PAGE;
   if (r.q0 < 0 || q1 < r.q0 || q1 > p.num_tokens) {
     errs |= ERR_INDPTR;
+  } else if (r.c == 0) {   // may hold anything: an idle slot of a batch
+    return false;
   } else if (r.n < r.c || r.n < 0 || r.n > p.max_kv_len) {
     errs |= ERR_LEN;
   } else if (r.ip0 < 0 || ip1 < r.ip0 || ip1 > ipn || static_cast<long long>(ip1) - r.ip0 != need) {
     errs |= ERR_INDPTR;
   } else {
     r.s = WeighSteps(r.n, r.c, p.H);
-    return r.c > 0;
+    return true;
   }
   return false;
 }
