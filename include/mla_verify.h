@@ -676,7 +676,9 @@ int mla_verify_free_kv(mla_verify_plan* plan, int batch, const int32_t* kv_indic
  * moves, kv_cache may be NULL and num_layers and layer_stride are ignored.
  * The j-th fresh entry of the call, in request order, is free_pages[free_count
  * - 1 - j]; entries whose count falls to 0 are pushed in ascending order.
- * The outputs must not be the inputs, nor may the two weights overlap.
+ * No output (the pool and the caches among them) may lie in an input's memory or
+ * another output's: MLA_VERIFY_ERR_ARG, as far as their sizes are known here (of
+ * kv_indices the first entry is).
  *
  * Device-side problems: a length outside [0, max_kv_len], or whose kept rows
  * with extra_rows exceed max_kv_len (MLA_VERIFY_DEV_BAD_LEN), or a table that does

@@ -735,6 +735,17 @@ def _expect_layers(plan: Plan, kv_cache):
     return kv_cache.data_ptr(), layers, kv_cache.stride(0) if layers > 1 else 0
 
 
+def _expect_apart(table, *written):
+    """No tensor of 32-bit words that a call writes lies in the table (the library
+    knows the table's beginning, not its length)."""
+    first = table.data_ptr()
+    end = first + 4 * table.numel()
+    for t in written:
+        p = t.data_ptr()
+        if p < end and first < p + 4 * t.numel():
+            _check(-9, "outputs in the table that the call reads")
+
+
 def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, kv_cache, page_refs,
              free_pages, free_count, sink: int = 0, recent: int = 0, extra_rows: int = 0,
              new_indices=None, new_indptr=None, new_lens=None, new_weights=None, stream=None):
@@ -751,8 +762,9 @@ def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, k
     int32 are the pool of fork_kv.  The new tables have room for ``extra_rows``
     more rows each (included in new_lens); new_weights [B, W' >= max_kv_len]
     holds the kept rows' weights, 0 behind them.  new_indices defaults to B *
-    (entries of budget + extra_rows); its length is the capacity.  Enqueued on
-    ``stream``, whose memory outputs that are not given come from; no sync.
+    (entries of budget + extra_rows); its length is the capacity.  No output may
+    lie in an input's memory or another output's.  Enqueued on ``stream``, whose
+    memory outputs that are not given come from; no sync.
     """
     B = kv_lens.shape[0]
     dev = plan.torch_device
@@ -776,6 +788,7 @@ def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, k
                   (page_refs, "page_refs", (units,)), (free_pages, "free_pages", (units,)), (free_count, "free_count", (1,)),
                   (new_indices, "new_indices", None), (new_indptr, "new_indptr", (B + 1,)), (new_lens, "new_lens", (B,)))
     new_stride = _expect_weights(plan, new_weights, "new_weights", B)
+    _expect_apart(kv_indices, new_indices, new_indptr, new_lens, page_refs, free_pages, free_count)
     st = load_library().mla_verify_evict_kv(
         plan.handle, B, weights.data_ptr(), stride, budget, sink, recent, kv_indices.data_ptr(),
         kv_indptr.data_ptr(), kv_lens.data_ptr(), cache, layers, layer_stride, extra_rows,

@@ -16,6 +16,7 @@
 
 #include "mla_verify.h"
 #include "kernels.h"
+#include "spans.h"
 
 using mlav::Params;
 
@@ -1223,11 +1224,20 @@ int mla_verify_evict_kv(mla_verify_plan* pl, int batch, const float* weights, in
   if (pl->page_size > 1 && (num_layers < 1 || num_layers > mlav::FORK_MAX_LAYERS || layer_stride < 0 || layer_stride % 8 ||
                             (num_layers > 1 && layer_stride < pl->num_slots * mlav::D_QK)))
     return MLA_VERIFY_ERR_ARG;
-  // Rows are read while others are written.
-  const float* end = weights + (batch - 1) * weight_stride + pl->max_kv_len;
-  const float* new_end = new_weights + (batch - 1) * new_weight_stride + new_width;
-  if ((weights < new_end && new_weights < end) || new_indices == kv_indices || new_indptr == kv_indptr || new_lens == kv_lens)
-    return MLA_VERIFY_ERR_ARG;
+  // Tables, lengths and weights are read while others are written: no output may
+  // lie in an input, nor in another output.  (Of kv_indices only the beginning
+  // is known here; of new_indices no more than the plan's requests can take is.)
+  const int64_t units = pl->num_slots / pl->page_size;
+  const int64_t most_entries = batch * ceil_div(pl->max_kv_len, pl->page_size);
+  const int64_t weight_bytes = pl->max_kv_len * 4LL;
+  const mlav::Span written[] = {
+      mlav::flat_span(new_indices, std::min(capacity, most_entries) * 4), mlav::flat_span(new_indptr, (batch + 1) * 4LL),
+      mlav::flat_span(new_lens, batch * 4LL), mlav::row_span(new_weights, batch, new_weight_stride * 4, new_width * 4),
+      mlav::flat_span(page_refs, units * 4), mlav::flat_span(free_pages, units * 4), mlav::flat_span(free_count, 4),
+      pl->page_size > 1 ? mlav::row_span(kv_cache, num_layers, layer_stride * 2, pl->num_slots * mlav::ROW_BYTES) : mlav::flat_span(nullptr, 0)};
+  const mlav::Span read[] = {mlav::row_span(weights, batch, weight_stride * 4, weight_bytes), mlav::flat_span(kv_indices, 4),
+                             mlav::flat_span(kv_indptr, (batch + 1) * 4LL), mlav::flat_span(kv_lens, batch * 4LL)};
+  if (mlav::any_overlap(written, 8, read, 4)) return MLA_VERIFY_ERR_ARG;
   const int dev_status = check_device(pl);
   if (dev_status != MLA_VERIFY_OK) return dev_status;
   mlav::EvictArgs a{};
