@@ -391,7 +391,8 @@ int mla_verify_attn_shared(mla_verify_plan* plan, int batch, const void* q, cons
  * Bad slots are masked (BAD_SLOT); a token none of whose keys is left has out 0
  * and lse -inf.  Values outside the fp16 range (MLA_VERIFY_DEV_RANGE) make the
  * rows that see them NaN and touch no others.  Numerics as for
- * mla_verify_attn_shared.  num_tokens may be 0 and is not bounded by the plan
+ * mla_verify_attn_shared, but for scores that are raised by 4.5e-7 of
+ * themselves, what the tensor cores cut off on average.  num_tokens may be 0 and is not bounded by the plan
  * (no workspace grows with it); num_tokens * H below 2^31, else
  * MLA_VERIFY_ERR_ARG.  Plans that mla_verify_attn_shared refuses give
  * MLA_VERIFY_ERR_SHAPE.  Otherwise as mla_verify_attn (capturable with q at
@@ -425,14 +426,15 @@ int mla_verify_attn_chunk(mla_verify_plan* plan, int batch, int64_t num_tokens, 
  *            places whose slot is bad (BAD_SLOT).  If q_indptr is out of order
  *            (BAD_INDPTR) nothing is added at all.
  *
- * Products in bf16 (exact), sums in fp32, cut towards zero: a score dot(q, k) of
- * magnitude s comes out 4e-7 to 6e-7 s too small where its partial sums lose
- * bits, exact where they lose none, and never further off than 72 * 2^-23 of
- * sum |q_d k_d|; its weight is off by scale times that of itself.  The scores of
- * mla_verify_attn_chunk lose the same: with its lse a query row's weights add up
- * to 1 to within 4e-7 |lse| + 3e-6 at most; with the lse of more exact scores
- * they come out those 4e-7 to 6e-7 |scale * s| of themselves too small (negative
- * scores: too large).
+ * Products in bf16 (exact), sums in fp32, which the tensor cores cut towards
+ * zero.  Scores are raised by the 4.5e-7 of themselves that ordinary data lose
+ * by this, here and in mla_verify_attn_chunk: they are then off by about 1e-7 to
+ * 3e-7 of themselves, by 4.5e-7 (too large) where their partial sums lose no
+ * bits, and never by more than 72 * 2^-23 of sum |q_d k_d|; a weight is off by
+ * scale times that of itself.  What the lse of mla_verify_attn_chunk is off by
+ * cancels: with it a query row's weights add up to 1 to within 4e-7 |lse| + 3e-6
+ * at most.  mla_verify_attn does not raise its scores: with its lse weights come
+ * out up to 6e-7 |scale * score| too large.
  * A NaN or infinite value in a query reaches the rows that it sees, one in a
  * cached row that row alone.  Sums are made in one order: equal inputs give equal
  * weights.  num_tokens as for mla_verify_attn_chunk; a weight_stride below
