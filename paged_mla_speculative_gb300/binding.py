@@ -735,17 +735,6 @@ def _expect_layers(plan: Plan, kv_cache):
     return kv_cache.data_ptr(), layers, kv_cache.stride(0) if layers > 1 else 0
 
 
-def _expect_apart(table, *written):
-    """No tensor of 32-bit words that a call writes lies in the table (the library
-    knows the table's beginning, not its length)."""
-    first = table.data_ptr()
-    end = first + 4 * table.numel()
-    for t in written:
-        p = t.data_ptr()
-        if p < end and first < p + 4 * t.numel():
-            _check(-9, "outputs in the table that the call reads")
-
-
 def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, kv_cache, page_refs,
              free_pages, free_count, sink: int = 0, recent: int = 0, extra_rows: int = 0,
              new_indices=None, new_indptr=None, new_lens=None, new_weights=None, stream=None):
@@ -788,13 +777,18 @@ def evict_kv(plan: Plan, weights, budget: int, kv_indices, kv_indptr, kv_lens, k
                   (page_refs, "page_refs", (units,)), (free_pages, "free_pages", (units,)), (free_count, "free_count", (1,)),
                   (new_indices, "new_indices", None), (new_indptr, "new_indptr", (B + 1,)), (new_lens, "new_lens", (B,)))
     new_stride = _expect_weights(plan, new_weights, "new_weights", B)
-    _expect_apart(kv_indices, new_indices, new_indptr, new_lens, page_refs, free_pages, free_count)
+    # No output in the table: the library knows the table's beginning, not its end.
+    table, room = kv_indices.data_ptr(), new_indices.numel()
+    end = table + 4 * kv_indices.numel()
+    refs, pages, height = page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr()
+    entries, starts, lens = new_indices.data_ptr(), new_indptr.data_ptr(), new_lens.data_ptr()
+    for at, count in ((refs, units), (pages, units), (height, 1), (entries, room), (starts, B + 1), (lens, B)):
+        if at < end and table < at + 4 * count:
+            _check(-9, "mla_verify_evict_kv: an output in kv_indices")
     st = load_library().mla_verify_evict_kv(
-        plan.handle, B, weights.data_ptr(), stride, budget, sink, recent, kv_indices.data_ptr(),
-        kv_indptr.data_ptr(), kv_lens.data_ptr(), cache, layers, layer_stride, extra_rows,
-        page_refs.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(), new_indices.data_ptr(),
-        new_indices.numel(), new_indptr.data_ptr(), new_lens.data_ptr(), new_weights.data_ptr(),
-        new_stride, new_weights.shape[1], _stream_ptr(stream))
+        plan.handle, B, weights.data_ptr(), stride, budget, sink, recent, table, kv_indptr.data_ptr(),
+        kv_lens.data_ptr(), cache, layers, layer_stride, extra_rows, refs, pages, height, entries, room,
+        starts, lens, new_weights.data_ptr(), new_stride, new_weights.shape[1], _stream_ptr(stream))
     _check(st, "mla_verify_evict_kv")
     return new_indices, new_indptr, new_lens, new_weights
 
