@@ -394,9 +394,15 @@ int mla_verify_attn_shared(mla_verify_plan* plan, int batch, const void* q, cons
  * mla_verify_attn_shared, but for scores that are raised by 4.5e-7 of
  * themselves, what the tensor cores cut off on average.  num_tokens may be 0 and is not bounded by the plan
  * (no workspace grows with it); num_tokens * H below 2^31, else
- * MLA_VERIFY_ERR_ARG.  Plans that mla_verify_attn_shared refuses give
- * MLA_VERIFY_ERR_SHAPE.  Otherwise as mla_verify_attn (capturable with q at
- * the same address, no allocation, the plan's workspace).
+ * MLA_VERIFY_ERR_ARG.  What T does bound is how evenly the work is divided: a
+ * plan holds partials for as many SM pairs as its verify calls (max_batch * T * H
+ * rows on max_kv_len keys) could keep busy, and the other pairs take whole tiles
+ * of 128 query rows.  A plan for one request that is to serve short chunks behind
+ * long caches wants a larger T (32 tokens of 64 heads behind 32768 rows: 448 us
+ * with T = 1, 129 with T = 4; behind 8192: 125 with T = 4, 52 with T = 32).
+ * Plans that mla_verify_attn_shared refuses give MLA_VERIFY_ERR_SHAPE.  Otherwise
+ * as mla_verify_attn (capturable with q at the same address, no allocation, the
+ * plan's workspace).
  */
 int mla_verify_attn_chunk(mla_verify_plan* plan, int batch, int64_t num_tokens, const void* q,
                           const void* kv_cache, const int32_t* kv_indices,

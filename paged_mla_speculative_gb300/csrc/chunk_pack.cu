@@ -3,9 +3,11 @@
 // chunk_prepare_kernel, two jobs side by side: CTA 0 lays out the call on the
 // device (lengths are device data) -- which requests can be served, their
 // place in the packed key space, their query-row tiles, and the division of
-// all tiles' steps over the attention kernel's clusters, even to a step, by
-// sums in closed form (chunk_steps.h), so that neither the workspace nor the
-// time grows with the tokens; the other CTAs gather the requests' rows into
+// all tiles' steps over the attention kernel's clusters, by sums in closed form
+// (chunk_steps.h), so that neither the workspace nor the time grows with the
+// tokens: even to a step among the clusters that the plan has partials for
+// (SharedParams::cut_clusters, by its verify calls' rows, not by a chunk's), by
+// whole tiles among the others; the other CTAs gather the requests' rows into
 // fp16 planes of 64 dims as shared_pack.cu's do (each scans the lengths itself).
 // Queries are not touched here: the attention kernel widens them in place.
 // HBM and L2 are the bound: 1152 bytes read and written a row (117000 rows in
@@ -128,7 +130,10 @@ __device__ void plan_chunks(const SharedParams& p, ChunkLayout& s, bool small, v
     p.totals[1] = tiles;
     p.totals[2] = bad;
   }
-  // Even division over as many clusters as get two steps or more each.
+  // Even division over as many clusters as get two steps or more each, as far
+  // as there are partials: with a plan of few verify rows the last shares are
+  // whole tiles, and few long tiles do not fill the clusters (32 tokens of 64 heads
+  // behind 32768 rows: 448 us with a plan of one draft, 129 with one of four).
   // Starts lie at least LEAST apart, so no two start in one tile's leading cost
   // or in one step; those of clusters without partials move up to a
   // tile's border (and some clusters may be left without work).  Where every

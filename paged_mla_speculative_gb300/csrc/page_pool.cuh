@@ -1,5 +1,7 @@
-// What freeing and evicting have in common: counts of pages that fall, and the
-// pages that reach 0 pushed on the pool's stack in ascending order.
+// What freeing and evicting have in common: counts of pages that fall, and a bit
+// map of the pages that reach 0, pushed on the pool's stack in ascending order
+// (by push_marked in freeing; evict_kv.cu, whose pools of single slots have
+// larger maps, has a push of its own).
 #pragma once
 
 #include "common.cuh"
