@@ -392,9 +392,9 @@ int mla_verify_attn_shared(mla_verify_plan* plan, int batch, const void* q, cons
  * and lse -inf.  Values outside the fp16 range (MLA_VERIFY_DEV_RANGE) make the
  * rows that see them NaN and touch no others.  Numerics as for
  * mla_verify_attn_shared, but for scores that are raised by 4.5e-7 of
- * themselves, what the tensor cores cut off on average.  num_tokens may be 0 and is not bounded by the plan
- * (no workspace grows with it); num_tokens * H below 2^31, else
- * MLA_VERIFY_ERR_ARG.  What T does bound is how evenly the work is divided: a
+ * themselves, what the tensor cores cut off on average.  num_tokens may be 0 and
+ * is not bounded by the plan (no workspace grows with it); num_tokens * H below
+ * 2^31, else MLA_VERIFY_ERR_ARG.  What T does bound is how evenly the work is divided: a
  * plan holds partials for as many SM pairs as its verify calls (max_batch * T * H
  * rows on max_kv_len keys) could keep busy, and the other pairs take whole tiles
  * of 128 query rows.  A plan for one request that is to serve short chunks behind

@@ -1242,7 +1242,7 @@ int mla_verify_evict_kv(mla_verify_plan* pl, int batch, const float* weights, in
       mlav::flat_span(new_indices, std::min(capacity, most_entries) * 4), mlav::flat_span(new_indptr, (batch + 1) * 4LL),
       mlav::flat_span(new_lens, batch * 4LL), mlav::row_span(new_weights, batch, new_weight_stride * 4, new_width * 4),
       mlav::flat_span(page_refs, units * 4), mlav::flat_span(free_pages, units * 4), mlav::flat_span(free_count, 4),
-      pl->page_size > 1 ? mlav::row_span(kv_cache, num_layers, layer_stride * 2, pl->num_slots * mlav::ROW_BYTES) : mlav::flat_span(nullptr, 0)};
+      pl->page_size > 1 ? mlav::row_span(kv_cache, num_layers, num_layers > 1 ? layer_stride * 2 : 0, pl->num_slots * mlav::ROW_BYTES) : mlav::flat_span(nullptr, 0)};
   const mlav::Span read[] = {mlav::row_span(weights, batch, weight_stride * 4, weight_bytes), mlav::flat_span(kv_indices, 4),
                              mlav::flat_span(kv_indptr, (batch + 1) * 4LL), mlav::flat_span(kv_lens, batch * 4LL)};
   if (mlav::any_overlap(written, 8, read, 4)) return MLA_VERIFY_ERR_ARG;
